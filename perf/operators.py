@@ -274,7 +274,7 @@ def _quantise(x, g):
     b = x.unflatten(-1, (-1, 16))
     most = b.abs().amax(-1)
     most = torch.where(torch.isfinite(b).all(-1), most, torch.full_like(most, math.nan))
-    s8 = (most / (6 * g)).clamp(max=448).to(torch.float8_e4m3fn)
+    s8 = (most * (1 / (6 * g))).clamp(max=448).to(torch.float8_e4m3fn)
     s = (s8.float() * g).unsqueeze(-1)
     t = torch.where(s > 0, b.abs() / s, torch.zeros_like(b))
     # nearest, ties to the even code: the codes stand for 0, 1/2, 1, 3/2, 2, 3, 4, 6
