@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/spec_verify.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/spec_verify.h and include/spec_kv.h (argument marshalling only).
 
 PyTorch supplies device memory and streams; every step of the verify path runs in the CUDA
 library. There is no CPU fallback: if the library cannot be built or loaded, calls raise.
@@ -20,7 +20,9 @@ EXPORTS = ("spec_verify", "spec_verify_workspace_bytes", "spec_verify_ws", "spec
            "spec_verify_host", "spec_verify_device_error", "spec_verify_status_string",
            "spec_verify_plan", "spec_verify_route", "spec_verify_noalloc", "spec_draft_sample", "spec_residual_topf",
            "spec_lmhead_stats", "spec_verify_hidden", "sv_hbm_read_probe", "sv_wait_probe",
-           "spec_verify_workspace_error", "sv_wait_probe_at")
+           "spec_verify_workspace_error", "sv_wait_probe_at",
+           "spec_block_tables", "spec_qk_norm_rope", "spec_kv4_page_bytes", "spec_kv4_append",
+           "spec_kv4_attention")
 SV_PROBE_NOALLOC, SV_PROBE_WORKSPACE = 1, 2
 
 
@@ -80,8 +82,17 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
         _LL = ctypes.c_longlong
         lib.spec_verify_hidden.argtypes = [_I, _I, _I, _I, _P, _LL, _P, _LL, _P, _LL, _P, _P, _P,
                                            _F, _F, _I, _P, _I, _P, _P, _P, _P]
+        lib.spec_block_tables.argtypes = [_I] * 4 + [_P] * 6 + [_I] + [_P] * 11
+        lib.spec_qk_norm_rope.argtypes = [_I] * 7 + [_P, _LL, _P, _LL, _P, _P, _P, _P, _F, _P, _LL,
+                                                     _P, _LL, _P]
+        lib.spec_kv4_page_bytes.argtypes = [_I, _I]
+        lib.spec_kv4_page_bytes.restype = _SZ
+        lib.spec_kv4_append.argtypes = [_I] * 6 + [_P, _LL, _P, _LL, _P, _F, _F, _P, _P, _P, _P]
+        lib.spec_kv4_attention.argtypes = [_I] * 8 + [_P, _LL, _P, _P, _P, _P, _F, _F, _F, _I, _P,
+                                                      _P, _P]
         for name in EXPORTS:
-            if name not in ("spec_verify_workspace_bytes", "spec_verify_status_string"):
+            if name not in ("spec_verify_workspace_bytes", "spec_verify_status_string",
+                            "spec_kv4_page_bytes"):
                 getattr(lib, name).restype = _I
         _lib = lib
         return lib

@@ -21,7 +21,9 @@
 #include "sv_hverify.h"
 #include "sv_greedy.h"
 #include "sv_small.h"
+#include "sv_kv.h"
 #include "sv_probe.h"
+#include "spec_kv.h"
 
 namespace {
 
@@ -1085,6 +1087,49 @@ sv_status spec_verify_hidden(int B, int K, int V, int d, const void* hidden_targ
   const cudaError_t e = sv::hv_run(p, sms, r->ws + 1, &r->ws->error, s);
   if (e == cudaErrorNotSupported) return SV_ERR_UNSUPPORTED;
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
+                             int max_blocks, const void* q, long long q_token_stride,
+                             const void* cache, const int32_t* block_table,
+                             const int32_t* kv_lens, const int32_t* cu_new, float scale,
+                             float k_scale, float v_scale, int max_new, void* out,
+                             float* out_lse, void* stream) {
+  if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || num_pages < 1 ||
+      max_blocks < 1 || max_new < 0)
+    return SV_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return SV_ERR_INVALID_ARG;
+  if (!sv::kv_page_size_ok(page_size) || !sv::kv_head_dim_ok(D)) return SV_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks) * page_size >= (1LL << 31)) return SV_ERR_INVALID_ARG;
+  if (q_token_stride < static_cast<long long>(Hq) * D) return SV_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return SV_OK;
+  if (!q || !cache || !block_table || !kv_lens || !cu_new || !out) return SV_ERR_INVALID_ARG;
+  if (!aligned16(q, q_token_stride, 2) || !aligned16(cache, 0, 1) || !aligned16(out, 0, 1))
+    return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq >= (1LL << 31)) return SV_ERR_UNSUPPORTED;
+  sv::AttnParams P;
+  P.B = B;
+  P.T = T;
+  P.hq = Hq;
+  P.hkv = Hkv;
+  P.group = Hq / Hkv;
+  P.ps = page_size;
+  P.num_pages = num_pages;
+  P.max_blocks = max_blocks;
+  P.qs = q_token_stride;
+  P.q = q;
+  P.cache = static_cast<const unsigned char*>(cache);
+  P.table = block_table;
+  P.lens = kv_lens;
+  P.cu = cu_new;
+  P.c = static_cast<float>(static_cast<double>(scale) * static_cast<double>(k_scale) *
+                           1.4426950408889634);
+  P.vs = v_scale;
+  P.out = out;
+  P.lse = out_lse;
+  return sv::launch_attention(P, D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK
+                                                                                      : SV_ERR_CUDA;
 }
 
 const char* spec_verify_status_string(sv_status status) {

@@ -1,0 +1,48 @@
+// Shared by the cache operators (sv_tables.cu, sv_normrope.cu, sv_kv4.cu, sv_attn.cu): the layout of the
+// 4-bit cache and the host-side interface of the attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace sv {
+
+constexpr int kTablesMaxB = 8192;  // 20 bytes of shared memory a sequence
+
+inline bool kv_page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
+inline bool kv_head_dim_ok(int D) { return D == 64 || D == 128; }
+
+// Byte offsets inside one block of 16 tokens of one head (see include/spec_kv.h).
+template <int D>
+struct KvBlock {
+  static constexpr int kKeyCodes = 0;
+  static constexpr int kKeyScales = 8 * D;
+  static constexpr int kValCodes = 9 * D;
+  static constexpr int kValScales = 17 * D;
+  static constexpr int kBytes = 18 * D;
+  static constexpr int kChunk = D / 8;  // bytes of one chunk of a value pair's codes
+  // place of chunk g of pair p
+  static __host__ __device__ constexpr int place(int p, int g) {
+    return D == 128 ? g ^ ((p & 3) << 1) : g ^ (((p >> 1) & 1) << 2);
+  }
+};
+
+// Attention of new tokens over the cache (sv_attn.cu).
+struct AttnParams {
+  int B, T, hq, hkv, group;  // group = hq / hkv
+  int ps, num_pages, max_blocks;
+  long long qs;  // token stride of q in elements
+  const void* q;
+  const unsigned char* cache;
+  const int32_t *table, *lens, *cu;
+  float c;    // scale * k_scale * log2(e)
+  float vs;   // v_scale
+  void* out;
+  float* lse;
+};
+
+cudaError_t launch_attention(const AttnParams& P, int D, cudaStream_t stream);
+
+}  // namespace sv

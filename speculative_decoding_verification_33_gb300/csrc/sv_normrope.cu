@@ -1,0 +1,331 @@
+// Norms of queries and keys per head and the rotation by position (spec_qk_norm_rope).
+//
+// Every value is read once and written once; the norm and the rotation happen in registers in
+// between, so the pass is bound by HBM. A thread holds two 16-byte vectors of a head, chosen so
+// that both halves of each rotated pair are its own: vectors j and j + rot/2 for halves, two
+// neighbours for interleaved pairs. D / 16 bf16 threads share a head's sum of squares by
+// shuffles. A CTA takes a few tokens, computes their sines and cosines once, and runs through the
+// heads.
+//
+// The angle position * inv_freq needs more bits than float32 has (2^-24 of a position of 10^6 is
+// a twentieth of a turn) but only its fraction of a turn matters: inv_freq / 2 pi is held as a
+// 64-bit fixed-point fraction, whose product with the position, modulo 2^64, is that fraction,
+// exact to position * 2^-65 turns. The nearest quarter turn goes into signs, the rest, at most
+// an eighth, through sincospif.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "spec_kv.h"
+#include "sv_kv.h"
+
+namespace sv {
+namespace {
+
+constexpr int kNrThreads = 256;
+constexpr int kNrMaxD = 512;
+
+struct NormRopeParams {
+  int T, hq, hk, D, rot, inter;
+  long long qs, ks, oqs, oks;  // token strides in elements
+  const void *q, *k, *wq, *wk;
+  const int32_t* pos;
+  const double* freq;
+  float eps;
+  void *oq, *ok;
+  int tokens;   // tokens of a CTA
+  int splits;   // CTAs that share a token group's heads
+};
+
+// Fraction of a turn per position, times 2^64.
+__device__ __forceinline__ unsigned long long turn_fraction(double freq) {
+  double t = freq * 0.15915494309189533577;  // 1 / 2 pi
+  t -= rint(t);                              // whole turns a position do not matter; |t| <= 1/2
+  return static_cast<unsigned long long>(__double2ll_rn(t * 9223372036854775808.0)) << 1;
+}
+
+__device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int pos) {
+  const unsigned long long f = fraction * static_cast<unsigned long long>(static_cast<long long>(pos));
+  const int hi = static_cast<int>(static_cast<uint32_t>((f + 0x80000000ull) >> 32));  // 2^-32 turns
+  const int quarter = static_cast<int>((static_cast<uint32_t>(hi) + 0x20000000u) >> 30);
+  const int rest = hi - static_cast<int>(static_cast<uint32_t>(quarter) << 30);
+  float s, c;
+  sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+  const float c2 = (quarter & 1) ? s : c, s2 = (quarter & 1) ? c : s;
+  return make_float2(((quarter + 1) & 2) ? -c2 : c2, (quarter & 2) ? -s2 : s2);
+}
+
+template <typename T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+};
+__device__ __forceinline__ void unpack(uint4 a, float (&x)[4]) {
+  x[0] = __uint_as_float(a.x);
+  x[1] = __uint_as_float(a.y);
+  x[2] = __uint_as_float(a.z);
+  x[3] = __uint_as_float(a.w);
+}
+__device__ __forceinline__ void unpack(uint4 a, float (&x)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// LPH threads a head, each with two 16-byte vectors.
+template <typename T, int LPH>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P) {
+  constexpr int N = Vec<T>::n;
+  extern __shared__ float2 cs[];  // [tokens][rot / 2] cosine, sine
+  const int half = P.rot / 2;
+  const int group = blockIdx.x / P.splits, split = blockIdx.x - group * P.splits;
+  const int t0 = group * P.tokens, nt = min(P.tokens, P.T - t0);
+  unsigned long long turn = 0;
+  for (int i = threadIdx.x, last = -1; i < nt * half; i += kNrThreads) {
+    const int t = i / half, j = i - t * half;
+    if (j != last) turn = turn_fraction(P.freq[j]);  // the same j again where half divides the CTA
+    last = j;
+    cs[i] = cos_sin(turn, P.pos[t0 + t]);
+  }
+  __syncthreads();
+  const int heads = P.hq + P.hk;
+  const int per = (heads + P.splits - 1) / P.splits;
+  const int h0 = split * per, nh = min(per, heads - h0);
+  if (nh <= 0) return;
+  const int lane = threadIdx.x % LPH;
+  const unsigned mask = (LPH == 32 ? 0xFFFFFFFFu : (1u << LPH) - 1u)
+                        << ((threadIdx.x & 31) & ~(LPH - 1));  // the threads of this head
+  // vectors of this thread: (lane, lane + rotated half) while they last, else neighbours
+  const int hv = P.inter ? 0 : half / N;
+  const int va = lane < hv ? lane : 2 * lane, vb = lane < hv ? lane + hv : 2 * lane + 1;
+  const bool halves = lane < hv;
+  // interleaved: whole vectors are rotated or not
+  const bool pair_a = P.inter && va * N < P.rot, pair_b = P.inter && vb * N < P.rot;
+  for (int it = threadIdx.x / LPH; it < nt * nh; it += kNrThreads / LPH) {
+    const int t = it / nh, h = h0 + (it - t * nh);
+    const bool is_q = h < P.hq;
+    const int hh = is_q ? h : h - P.hq;
+    const long long row = t0 + t;
+    const T* x = static_cast<const T*>(is_q ? P.q : P.k) + row * (is_q ? P.qs : P.ks) +
+                 static_cast<long long>(hh) * P.D;
+    float a[N], b[N];
+    unpack(*(reinterpret_cast<const uint4*>(x) + va), a);
+    unpack(*(reinterpret_cast<const uint4*>(x) + vb), b);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+    for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mask, sum, d, LPH);
+    const float r = 1.0f / sqrtf(sum / static_cast<float>(P.D) + P.eps);
+    const T* w = static_cast<const T*>(is_q ? P.wq : P.wk);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      a[i] *= r;
+      b[i] *= r;
+    }
+    if (w) {
+      float wa[N], wb[N];
+      unpack(__ldg(reinterpret_cast<const uint4*>(w) + va), wa);
+      unpack(__ldg(reinterpret_cast<const uint4*>(w) + vb), wb);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        a[i] *= wa[i];
+        b[i] *= wb[i];
+      }
+    }
+    const float2* c = cs + t * half;
+    if (halves) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 f = c[va * N + i];
+        const float y0 = a[i] * f.x - b[i] * f.y, y1 = b[i] * f.x + a[i] * f.y;
+        a[i] = y0;
+        b[i] = y1;
+      }
+    }
+    if (pair_a) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 f = c[(va * N + i) / 2];
+        const float y0 = a[i] * f.x - a[i + 1] * f.y, y1 = a[i + 1] * f.x + a[i] * f.y;
+        a[i] = y0;
+        a[i + 1] = y1;
+      }
+    }
+    if (pair_b) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 f = c[(vb * N + i) / 2];
+        const float y0 = b[i] * f.x - b[i + 1] * f.y, y1 = b[i + 1] * f.x + b[i] * f.y;
+        b[i] = y0;
+        b[i + 1] = y1;
+      }
+    }
+    T* y = static_cast<T*>(is_q ? P.oq : P.ok) + row * (is_q ? P.oqs : P.oks) +
+           static_cast<long long>(hh) * P.D;
+    *(reinterpret_cast<uint4*>(y) + va) = pack(a);
+    *(reinterpret_cast<uint4*>(y) + vb) = pack(b);
+  }
+}
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Any even D and rot, any alignment: a warp a head, a pair of values at a time a lane.
+template <typename T>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_any_kernel(NormRopeParams P) {
+  const int heads = P.hq + P.hk, half = P.rot / 2;
+  const long long item = static_cast<long long>(blockIdx.x) * (kNrThreads / 32) + threadIdx.x / 32;
+  if (item >= static_cast<long long>(P.T) * heads) return;
+  const int lane = threadIdx.x % 32;
+  const long long row = item / heads;
+  const int h = static_cast<int>(item - row * heads);
+  const bool is_q = h < P.hq;
+  const int hh = is_q ? h : h - P.hq;
+  const T* x = static_cast<const T*>(is_q ? P.q : P.k) + row * (is_q ? P.qs : P.ks) +
+               static_cast<long long>(hh) * P.D;
+  T* y = static_cast<T*>(is_q ? P.oq : P.ok) + row * (is_q ? P.oqs : P.oks) +
+         static_cast<long long>(hh) * P.D;
+  const T* w = static_cast<const T*>(is_q ? P.wq : P.wk);
+  constexpr int kPairs = kNrMaxD / 64;  // pairs of a lane
+  float a[kPairs], b[kPairs];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int j = lane + 32 * i;  // pair; the first `half` are rotated
+    if (j >= P.D / 2) break;
+    const int ia = !P.inter && j < half ? j : 2 * j, ib = !P.inter && j < half ? j + half : 2 * j + 1;
+    a[i] = as_float(x[ia]);
+    b[i] = as_float(x[ib]);
+    sum += a[i] * a[i] + b[i] * b[i];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  const float r = 1.0f / sqrtf(sum / static_cast<float>(P.D) + P.eps);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int j = lane + 32 * i;
+    if (j >= P.D / 2) break;
+    const int ia = !P.inter && j < half ? j : 2 * j, ib = !P.inter && j < half ? j + half : 2 * j + 1;
+    float y0 = a[i] * r * (w ? as_float(w[ia]) : 1.f), y1 = b[i] * r * (w ? as_float(w[ib]) : 1.f);
+    if (j < half) {
+      const float2 f = cos_sin(turn_fraction(P.freq[j]), P.pos[row]);
+      const float z0 = y0 * f.x - y1 * f.y, z1 = y1 * f.x + y0 * f.y;
+      y0 = z0;
+      y1 = z1;
+    }
+    put(y + ia, y0);
+    put(y + ib, y1);
+  }
+}
+
+template <typename T>
+cudaError_t launch_norm_rope(const NormRopeParams& Q, bool fast, cudaStream_t s) {
+  NormRopeParams P = Q;
+  const int heads = P.hq + P.hk;
+  if (!fast) {
+    const long long warps = static_cast<long long>(P.T) * heads;
+    norm_rope_any_kernel<T><<<static_cast<unsigned>((warps + kNrThreads / 32 - 1) / (kNrThreads / 32)),
+                              kNrThreads, 0, s>>>(P);
+    return cudaGetLastError();
+  }
+  const int lph = P.D / (2 * Vec<T>::n);
+  // Up to 8 tokens a CTA while that leaves 8 CTAs a multiprocessor; fewer tokens than that: the
+  // heads of a token are shared out, one pass of the CTA's threads each.
+  P.tokens = std::max(1, std::min(8, P.T / (8 * 152)));
+  const int pass = kNrThreads / lph;
+  P.splits = P.T < 4 * 152 ? std::max(1, (heads + pass - 1) / pass) : 1;
+  const long long groups = (P.T + P.tokens - 1) / P.tokens;
+  const unsigned grid = static_cast<unsigned>(groups * P.splits);
+  const size_t smem = static_cast<size_t>(P.tokens) * (P.rot / 2) * sizeof(float2);
+  switch (lph) {
+    case 4: norm_rope_kernel<T, 4><<<grid, kNrThreads, smem, s>>>(P); break;
+    case 8: norm_rope_kernel<T, 8><<<grid, kNrThreads, smem, s>>>(P); break;
+    case 16: norm_rope_kernel<T, 16><<<grid, kNrThreads, smem, s>>>(P); break;
+    case 32: norm_rope_kernel<T, 32><<<grid, kNrThreads, smem, s>>>(P); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" sv_status spec_qk_norm_rope(int T, int Hq, int Hkv, int D, int rot, int interleaved,
+                                       sv_dtype dtype, const void* q, long long q_token_stride,
+                                       const void* k, long long k_token_stride,
+                                       const void* q_weight, const void* k_weight,
+                                       const int32_t* positions, const double* inv_freq,
+                                       float eps, void* out_q, long long out_q_token_stride,
+                                       void* out_k, long long out_k_token_stride, void* stream) {
+  if (T < 0 || Hq < 1 || Hkv < 0 || D < 2 || D % 2 || rot < 0 || rot > D || rot % 2)
+    return SV_ERR_INVALID_ARG;
+  if (dtype != SV_DTYPE_F32 && dtype != SV_DTYPE_BF16) return SV_ERR_INVALID_ARG;
+  if (!(std::isfinite(eps) && eps >= 0.f)) return SV_ERR_INVALID_ARG;
+  const long long rq = static_cast<long long>(Hq) * D, rk = static_cast<long long>(Hkv) * D;
+  if (q_token_stride < rq || out_q_token_stride < rq) return SV_ERR_INVALID_ARG;
+  if (Hkv > 0 && (k_token_stride < rk || out_k_token_stride < rk)) return SV_ERR_INVALID_ARG;
+  if (D > sv::kNrMaxD) return SV_ERR_UNSUPPORTED;
+  if (T == 0) return SV_OK;
+  if (!q || !out_q || (Hkv > 0 && (!k || !out_k))) return SV_ERR_INVALID_ARG;
+  if (rot > 0 && (!positions || !inv_freq)) return SV_ERR_INVALID_ARG;
+  if (q == out_q && q_token_stride != out_q_token_stride) return SV_ERR_INVALID_ARG;
+  if (Hkv > 0 && k == out_k && k_token_stride != out_k_token_stride) return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * (Hq + static_cast<long long>(Hkv)) > (1LL << 33))
+    return SV_ERR_UNSUPPORTED;  // the grid's size
+  sv::NormRopeParams P;
+  P.T = T;
+  P.hq = Hq;
+  P.hk = Hkv;
+  P.D = D;
+  P.rot = rot;
+  P.inter = interleaved ? 1 : 0;
+  P.qs = q_token_stride;
+  P.ks = k_token_stride;
+  P.oqs = out_q_token_stride;
+  P.oks = out_k_token_stride;
+  P.q = q;
+  P.k = k;
+  P.wq = q_weight;
+  P.wk = k_weight;
+  P.pos = positions;
+  P.freq = inv_freq;
+  P.eps = eps;
+  P.oq = out_q;
+  P.ok = out_k;
+  P.tokens = P.splits = 1;
+  // whole 16-byte vectors, both vectors of a thread rotated the same way, a power of two threads
+  const int n = dtype == SV_DTYPE_BF16 ? 8 : 4;
+  const size_t elt = dtype == SV_DTYPE_BF16 ? 2 : 4;
+  auto aligned = [&](const void* p, long long stride) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
+           (stride * static_cast<long long>(elt)) % 16 == 0;
+  };
+  const int lph = D / (2 * n);
+  bool fast = D % (2 * n) == 0 && (lph == 4 || lph == 8 || lph == 16 || lph == 32) &&
+              (P.inter ? rot : rot / 2) % n == 0 && aligned(q, q_token_stride) &&
+              aligned(out_q, out_q_token_stride) && aligned(q_weight, 0) && aligned(k_weight, 0);
+  if (Hkv > 0) fast = fast && aligned(k, k_token_stride) && aligned(out_k, out_k_token_stride);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == SV_DTYPE_BF16 ? sv::launch_norm_rope<__nv_bfloat16>(P, fast, s)
+                                               : sv::launch_norm_rope<float>(P, fast, s);
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}

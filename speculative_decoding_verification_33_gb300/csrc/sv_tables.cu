@@ -1,0 +1,320 @@
+// Block tables and slot maps of a paged cache from request lengths (spec_block_tables), one launch.
+//
+// The work is a few prefix sums over the sequences (pages taken, pages put back, tokens) and then
+// independent writes: 16 bytes a token, one table entry a new page. It is bound by latency, so
+// nothing is handed from one CTA to another: every CTA takes the prefix sums of all sequences
+// itself (their lengths are a few KB in L2), keeps what the tokens need in shared memory, and
+// writes its share of the tokens and pages. Pages that this call puts back are never taken by
+// it, so no CTA reads a ring entry or a table entry that another one writes.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "spec_kv.h"
+#include "sv_kv.h"
+
+namespace sv {
+namespace {
+
+constexpr int kTbThreads = 256;
+constexpr int kTbTokens = 4;  // consecutive tokens a thread writes (32-byte stores of slots)
+
+struct TablesParams {
+  int B, ps, max_blocks, max_tokens, ring_size;
+  const int32_t *ctx, *acc, *nw, *held;
+  int32_t *table, *ring;
+  const int64_t* counters;
+  int32_t *o_ctx, *o_held, *o_kv, *o_status, *o_cu, *o_pos, *o_seq;
+  int64_t *o_counters, *o_slots;
+};
+
+// One sequence of the call, from its lengths alone.
+struct Seq {
+  long long c, n, grow, shrink;
+  int held, bad;
+};
+
+__device__ __forceinline__ Seq load_seq(const TablesParams& P, int b) {
+  Seq s;
+  const int ctx = P.ctx[b], nw = P.nw[b], a = P.acc ? P.acc[b] : -1;
+  s.held = P.held[b];
+  const bool done = nw < 0;
+  s.c = done ? 0 : static_cast<long long>(ctx) + (a >= 0 ? static_cast<long long>(a) + 1 : 0);
+  s.n = done ? 0 : nw;
+  const long long need = (s.c + s.n + P.ps - 1) / P.ps;
+  s.bad = s.held < 0 || s.held > P.max_blocks ||
+          (!done && (ctx < 0 || s.c > static_cast<long long>(s.held) * P.ps || need > P.max_blocks));
+  if (s.bad) {
+    s.c = ctx;
+    s.n = s.grow = s.shrink = 0;
+  } else {
+    s.grow = need > s.held ? need - s.held : 0;
+    s.shrink = need < s.held ? s.held - need : 0;
+  }
+  return s;
+}
+
+// Exclusive prefix sum of `v` over the CTA's threads; *total is the sum. `part` holds one value
+// per warp; the call starts with a barrier, so that it may be used again.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kTbThreads / 32; ++w) {
+    const long long p = part[w];
+    if (w < warp) before += p;
+    sum += p;
+  }
+  *total = sum;
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
+  // per sequence: first token of the round, tokens before the round, pages held before and
+  // after the call, rank of its first queue entry taken or put back
+  extern __shared__ int32_t sm[];
+  int32_t* s_cu = sm;
+  int32_t* s_c = sm + P.B + 1;
+  int32_t* s_held = s_c + P.B;
+  int32_t* s_now = s_held + P.B;
+  int32_t* s_rank = s_now + P.B;
+  __shared__ long long part[kTbThreads / 32];
+
+  const int tid = threadIdx.x;
+  const int per = (P.B + kTbThreads - 1) / kTbThreads;
+  const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
+  const long long cap = P.ring_size;
+  const long long head = P.counters[0], tail = P.counters[1];
+  long long live = tail - head;
+  live = live < 0 ? 0 : live > cap ? cap : live;
+  long long h0 = cap ? head % cap : 0, t0 = cap ? tail % cap : 0;
+  h0 += h0 < 0 ? cap : 0;
+  t0 += t0 < 0 ? cap : 0;
+
+  long long grow = 0, shrink = 0, n = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load_seq(P, b);
+    grow += s.grow;
+    shrink += s.shrink;
+    n += s.n;
+  }
+  long long all_grow, all_shrink, all_n;
+  const long long grow0 = block_scan(grow, part, &all_grow);
+  const long long shrink0 = block_scan(shrink, part, &all_shrink);
+  if (all_grow > live) {  // tokens of the sequences whose pages run out do not count
+    long long g = grow0;
+    n = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(P, b);
+      g += s.grow;
+      n += s.grow > 0 && g > live ? 0 : s.n;
+    }
+  }
+  const long long n0 = block_scan(n, part, &all_n);
+  // ranks of the scheduled tokens: n0 unless some do not fit in the token arrays
+  long long u0 = n0, all_u = all_n;
+  if (all_n > P.max_tokens) {
+    long long g = grow0, m = n0, u = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(P, b);
+      g += s.grow;
+      const long long nb = s.grow > 0 && g > live ? 0 : s.n;
+      m += nb;
+      u += m > P.max_tokens ? 0 : nb;
+    }
+    u0 = block_scan(u, part, &all_u);
+  }
+
+  // the sequences: what the tokens need into shared memory, the outputs from CTA 0
+  long long g = grow0, f = shrink0, m = n0, u = u0, taken = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load_seq(P, b);
+    const long long g_before = g;
+    g += s.grow;
+    const bool lacks = s.grow > 0 && g > live;
+    const long long nb = lacks ? 0 : s.n;
+    m += nb;
+    const bool full = nb > 0 && m > P.max_tokens;
+    const int sched = static_cast<int>(full ? 0 : nb);
+    const bool takes = s.grow > 0 && !lacks;
+    const long long now = lacks ? s.held : s.held + s.grow - s.shrink;
+    s_cu[b] = static_cast<int32_t>(u);
+    s_c[b] = static_cast<int32_t>(s.c);
+    s_held[b] = s.held;
+    s_now[b] = static_cast<int32_t>(now);
+    s_rank[b] = static_cast<int32_t>(takes ? g_before : f);
+    if (takes) taken += s.grow;
+    u += sched;
+    f += s.shrink;
+    if (blockIdx.x == 0) {
+      P.o_ctx[b] = static_cast<int32_t>(s.c);
+      P.o_held[b] = static_cast<int32_t>(now);
+      P.o_kv[b] = static_cast<int32_t>(s.c + sched);
+      P.o_status[b] = s.bad ? -2 : lacks ? -1 : full ? -3 : sched > 0 ? 1 : 0;
+      P.o_cu[b] = s_cu[b];
+    }
+  }
+  if (blockIdx.x == 0) {
+    long long all_taken;
+    block_scan(taken, part, &all_taken);
+    if (tid == 0) {
+      P.o_counters[0] = head + all_taken;
+      P.o_counters[1] = tail + all_shrink;
+      P.o_cu[P.B] = static_cast<int32_t>(all_u);
+    }
+  }
+  if (tid == 0) s_cu[P.B] = static_cast<int32_t>(all_u);
+  __syncthreads();
+
+  // table entries of new pages, ring entries of pages put back: a warp a sequence, four loads in
+  // flight (a prompt takes hundreds of pages)
+  const int lane = tid & 31;
+  for (int b = blockIdx.x * (kTbThreads / 32) + (tid >> 5); b < P.B;
+       b += gridDim.x * (kTbThreads / 32)) {
+    const int held = s_held[b], now = s_now[b];
+    int32_t* row = P.table + static_cast<long long>(b) * P.max_blocks;
+    const bool takes = now > held;
+    const long long rank = s_rank[b];
+    int count = takes ? now - held : held - now;
+    // only counters that are not this ring's can ask for more places than it has
+    if (!takes) count = static_cast<int>(max(0LL, min(static_cast<long long>(count), cap - live - rank)));
+    for (int j0 = lane; j0 < count; j0 += 128) {
+      int32_t page[4];
+      long long at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + 32 * k;
+        at[k] = (takes ? h0 : t0) + rank + j;
+        at[k] -= at[k] >= cap ? cap : 0;
+        if (j < count) page[k] = takes ? P.ring[at[k]] : row[now + j];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + 32 * k;
+        if (j < count) (takes ? row[held + j] : P.ring[at[k]]) = page[k];
+      }
+    }
+  }
+
+  // the tokens
+  const int total = static_cast<int>(all_u);
+  const long long step = static_cast<long long>(gridDim.x) * kTbThreads * kTbTokens;
+  for (long long base = (static_cast<long long>(blockIdx.x) * kTbThreads + tid) * kTbTokens;
+       base < P.max_tokens; base += step) {
+    int b = 0;
+    if (base < total) {  // last sequence that starts at or before the token
+      int lo = 0, hi = P.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cu[mid] <= base) lo = mid; else hi = mid;
+      }
+      b = lo;
+    }
+    long long blk_of = -1;
+    int page = -1;
+#pragma unroll
+    for (int j = 0; j < kTbTokens; ++j) {
+      const long long t = base + j;
+      if (t >= P.max_tokens) break;
+      long long slot = -1;
+      int pos = 0, seq = -1;
+      if (t < total) {
+        while (s_cu[b + 1] <= t) {
+          ++b;
+          blk_of = -1;
+        }
+        seq = b;
+        pos = s_c[b] + static_cast<int>(t - s_cu[b]);
+        const int blk = pos / P.ps;
+        if (blk != blk_of) {
+          blk_of = blk;
+          const int held = s_held[b];
+          if (blk < held) {
+            page = P.table[static_cast<long long>(b) * P.max_blocks + blk];
+          } else {
+            long long i = h0 + s_rank[b] + (blk - held);
+            i -= i >= cap ? cap : 0;
+            page = P.ring[i];
+          }
+        }
+        slot = page < 0 ? -1 : static_cast<long long>(page) * P.ps + pos % P.ps;
+      }
+      P.o_slots[t] = slot;
+      P.o_pos[t] = pos;
+      P.o_seq[t] = seq;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" sv_status spec_block_tables(
+    int B, int page_size, int max_blocks, int max_tokens, const int32_t* ctx_lens,
+    const int32_t* accept_len, const int32_t* new_lens, int32_t* block_table, const int32_t* held,
+    int32_t* ring, int ring_size, const int64_t* counters, int32_t* out_ctx_lens,
+    int32_t* out_held, int64_t* out_counters, int32_t* out_kv_lens, int32_t* out_status,
+    int32_t* out_cu_new, int64_t* out_slots, int32_t* out_positions, int32_t* out_seq_ids,
+    void* stream) {
+  if (B < 0 || max_blocks < 1 || max_tokens < 0 || ring_size < 1) return SV_ERR_INVALID_ARG;
+  if (!sv::kv_page_size_ok(page_size)) return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_blocks) * page_size >= (1LL << 31)) return SV_ERR_INVALID_ARG;
+  if (!counters || !out_counters || !out_cu_new || !ring) return SV_ERR_INVALID_ARG;
+  if (counters == out_counters) return SV_ERR_INVALID_ARG;
+  if (B > 0) {
+    if (!ctx_lens || !new_lens || !block_table || !held || !out_ctx_lens || !out_held ||
+        !out_kv_lens || !out_status)
+      return SV_ERR_INVALID_ARG;
+    // every CTA reads all lengths while CTA 0 writes the new ones
+    const void* in[4] = {ctx_lens, accept_len, new_lens, held};
+    const void* out[4] = {out_ctx_lens, out_held, out_kv_lens, out_status};
+    for (const void* i : in)
+      for (const void* o : out)
+        if (i && i == o) return SV_ERR_INVALID_ARG;
+  }
+  if (max_tokens > 0 && (!out_slots || !out_positions || !out_seq_ids)) return SV_ERR_INVALID_ARG;
+  if (B > sv::kTablesMaxB) return SV_ERR_UNSUPPORTED;
+  sv::TablesParams P;
+  P.B = B;
+  P.ps = page_size;
+  P.max_blocks = max_blocks;
+  P.max_tokens = max_tokens;
+  P.ring_size = ring_size;
+  P.ctx = ctx_lens;
+  P.acc = accept_len;
+  P.nw = new_lens;
+  P.held = held;
+  P.table = block_table;
+  P.ring = ring;
+  P.counters = counters;
+  P.o_ctx = out_ctx_lens;
+  P.o_held = out_held;
+  P.o_kv = out_kv_lens;
+  P.o_status = out_status;
+  P.o_cu = out_cu_new;
+  P.o_pos = out_positions;
+  P.o_seq = out_seq_ids;
+  P.o_counters = out_counters;
+  P.o_slots = out_slots;
+  // one CTA for every 1024 tokens or 64 sequences, at most two a multiprocessor
+  const long long want =
+      1 + std::max((max_tokens - 1) / (sv::kTbThreads * sv::kTbTokens), (B - 1) / 64);
+  const int grid = static_cast<int>(std::min<long long>(want, 304));
+  const size_t smem = (5 * static_cast<size_t>(B) + 1) * sizeof(int32_t);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(sv::tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  sv::tables_kernel<<<grid, sv::kTbThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}

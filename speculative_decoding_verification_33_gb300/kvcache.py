@@ -1,0 +1,208 @@
+"""Python API of the paged key/value cache around the verify step, over torch tensors.
+
+The calls mirror include/spec_kv.h, which holds their definitions and the cache's layout; shapes,
+dtypes and strides are read from the tensors, outputs are allocated unless ``out`` supplies them.
+A round is ``block_tables`` -> (projections) -> ``qk_norm_rope`` -> ``kv4_append`` ->
+``kv4_attention`` -> (the rest of the layer, the head) -> ``verify`` / ``verify_hidden``, whose
+``accept_len`` goes into the next round's ``block_tables``.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._lib import SV_DTYPE_BF16, SV_DTYPE_F32
+from .api import _stream_handle
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, like: torch.Tensor) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(like.device.index)
+    return _stream_handle(stream)
+
+
+def _dev(t: torch.Tensor, dtype, shape, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(address, token stride) of [T, H, D] whose heads lie side by side."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D], got {tuple(t.shape)}")
+    T, H, D = t.shape
+    s = t.stride()
+    if not t.is_cuda or (s[2] != 1 and D > 1) or (s[1] != D and H > 1):
+        raise ValueError(f"{name} must be a CUDA tensor whose heads are contiguous in a token")
+    return t.data_ptr(), s[0] if T > 1 else H * D
+
+
+def _float_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return SV_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return SV_DTYPE_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                 held: torch.Tensor, ring: torch.Tensor, counters: torch.Tensor, *,
+                 page_size: int, max_tokens: int, accept_len: Optional[torch.Tensor] = None,
+                 out: Optional[dict] = None, stream=None) -> dict:
+    """Pages, slots and positions of the next round from the sequences' lengths
+    (``spec_block_tables``). ``block_table`` [B, max_blocks] and ``ring`` are updated in place;
+    ``counters`` is int64 [2], the rest int32. Returns {"ctx_lens", "held", "counters",
+    "cu_new", "kv_lens", "status", "slots", "positions", "seq_ids"}, buffers other than the
+    inputs: two sets in turn serve a loop."""
+    i32, i64 = torch.int32, torch.int64
+    B = ctx_lens.shape[0]
+    if block_table.dim() != 2 or ring.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks] and ring [pages]")
+    most = block_table.shape[1]
+    if out is None:
+        dev = ctx_lens.device
+
+        def new(n, t=i32):
+            return torch.empty(n, dtype=t, device=dev)
+        out = {"ctx_lens": new(B), "held": new(B), "counters": new(2, i64), "cu_new": new(B + 1),
+               "kv_lens": new(B), "status": new(B), "slots": new(max_tokens, i64),
+               "positions": new(max_tokens), "seq_ids": new(max_tokens)}
+    per, tok = (B,), (max_tokens,)
+    st = _lib.load().spec_block_tables(
+        B, page_size, most, max_tokens, _dev(ctx_lens, i32, per, "ctx_lens"),
+        0 if accept_len is None else _dev(accept_len, i32, per, "accept_len"),
+        _dev(new_lens, i32, per, "new_lens"), _dev(block_table, i32, (B, most), "block_table"),
+        _dev(held, i32, per, "held"), _dev(ring, i32, ring.shape, "ring"), ring.shape[0],
+        _dev(counters, i64, (2,), "counters"), _dev(out["ctx_lens"], i32, per, "out ctx_lens"),
+        _dev(out["held"], i32, per, "out held"),
+        _dev(out["counters"], i64, (2,), "out counters"),
+        _dev(out["kv_lens"], i32, per, "out kv_lens"), _dev(out["status"], i32, per, "out status"),
+        _dev(out["cu_new"], i32, (B + 1,), "out cu_new"), _dev(out["slots"], i64, tok, "out slots"),
+        _dev(out["positions"], i32, tok, "out positions"),
+        _dev(out["seq_ids"], i32, tok, "out seq_ids"), _stream(stream, ctx_lens))
+    _lib._check(st, "spec_block_tables")
+    return out
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                 inv_freq: torch.Tensor, *, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """Norm of every query and key head and the rotation by position, in one pass
+    (``spec_qk_norm_rope``). ``q`` [T, Hq, D] and ``k`` [T, Hkv, D] (or None) bf16 or f32, heads
+    contiguous in a token; ``positions`` [T] int32; ``inv_freq`` [rot / 2] float64. Returns
+    {"q", "k"}; ``out={"q": q, "k": k}`` works in place."""
+    T, hq, D = q.shape
+    code = _float_code(q, "q")
+    hk = 0 if k is None else k.shape[1]
+    if k is not None and (k.dtype != q.dtype or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("k must be [T, Hkv, D] of q's dtype")
+    if out is None:
+        out = {"q": torch.empty((T, hq, D), dtype=q.dtype, device=q.device)}
+        if k is not None:
+            out["k"] = torch.empty((T, hk, D), dtype=q.dtype, device=q.device)
+    for n, h in (("q", hq), ("k", hk)):
+        if h and (out[n].dtype != q.dtype or out[n].shape != (T, h, D)):
+            raise ValueError(f"out {n} must be {(T, h, D)} of q's dtype")
+    qp, qs = _rows(q, "q")
+    oq, oqs = _rows(out["q"], "out q")
+    kp, ks = _rows(k, "k") if k is not None else (0, 0)
+    ok, oks = _rows(out["k"], "out k") if k is not None else (0, 0)
+    st = _lib.load().spec_qk_norm_rope(
+        T, hq, hk, D, 2 * inv_freq.shape[0], bool(interleaved), code, qp, qs, kp, ks,
+        0 if q_weight is None else _dev(q_weight, q.dtype, (D,), "q_weight"),
+        0 if k_weight is None else _dev(k_weight, q.dtype, (D,), "k_weight"),
+        _dev(positions, torch.int32, (T,), "positions"),
+        _dev(inv_freq, torch.float64, (inv_freq.shape[0],), "inv_freq"), eps, oq, oqs, ok, oks,
+        _stream(stream, q))
+    _lib._check(st, "spec_qk_norm_rope")
+    return out
+
+
+def kv4_page_bytes(page_size: int, D: int) -> int:
+    """Bytes of one page of one head; 0 where the sizes are not supported."""
+    return int(_lib.load().spec_kv4_page_bytes(int(page_size), int(D)))
+
+
+def kv4_cache(num_pages: int, heads: int, D: int, page_size: int, device="cuda") -> torch.Tensor:
+    """An empty cache: uint8 [num_pages, heads, kv4_page_bytes(page_size, D)]."""
+    nbytes = kv4_page_bytes(page_size, D)
+    if not nbytes:
+        raise ValueError("page_size must be 16, 32, 64 or 128 and D 64 or 128")
+    return torch.zeros(num_pages, heads, nbytes, dtype=torch.uint8, device=device)
+
+
+def _cache(cache: torch.Tensor, heads: int, D: int, page_size: int) -> int:
+    if cache.dim() != 3 or cache.shape[1] != heads or \
+            cache.shape[2] != page_size * (D + D // 8):
+        raise ValueError(f"cache {tuple(cache.shape)} is not [pages, {heads}, page bytes] for "
+                         f"page_size {page_size}, D {D}")
+    return _dev(cache, torch.uint8, cache.shape, "cache")
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, *,
+               page_size: int, k_scale: float = 1.0, v_scale: float = 1.0,
+               out: Optional[dict] = None, values: bool = False, stream=None) -> dict:
+    """Write the keys and values of T tokens into the cache at ``slots`` (``spec_kv4_append``).
+    ``k``, ``v`` [T, Hkv, D] bf16 or f32; ``slots`` [T] int64, -1 for a token that is not
+    written. Returns {}, or with ``values`` (or ``out``) {"k", "v"}: bf16, what the cache now
+    stands for."""
+    T, H, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must share shape and dtype")
+    if out is None:
+        out = {n: torch.empty((T, H, D), dtype=torch.bfloat16, device=k.device)
+               for n in ("k", "v")} if values else {}
+    kp, ks = _rows(k, "k")
+    vp, vs = _rows(v, "v")
+    st = _lib.load().spec_kv4_append(
+        T, H, D, page_size, cache.shape[0], _float_code(k, "k"), kp, ks, vp, vs,
+        _dev(slots, torch.int64, (T,), "slots"), k_scale, v_scale,
+        _cache(cache, H, D, page_size),
+        _dev(out["k"], torch.bfloat16, (T, H, D), "out k") if out else 0,
+        _dev(out["v"], torch.bfloat16, (T, H, D), "out v") if out else 0, _stream(stream, k))
+    _lib._check(st, "spec_kv4_append")
+    return out
+
+
+def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                  kv_lens: torch.Tensor, cu_new: torch.Tensor, *, page_size: int,
+                  scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                  max_new: int = 1, out: Optional[dict] = None, stream=None) -> dict:
+    """Causal attention of the new tokens over the cache (``spec_kv4_attention``). ``q``
+    [T, Hq, D] bf16; ``block_table`` [B, max_blocks], ``kv_lens`` [B], ``cu_new`` [B + 1] int32;
+    ``max_new`` is the largest number of new tokens of a sequence, as far as known (speed only).
+    ``scale`` defaults to 1 / sqrt(D). Returns {"out" [T, Hq, D] bf16, "lse" [T, Hq] f32}; rows
+    of no sequence are left as they are."""
+    T, hq, D = q.shape
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    B = kv_lens.shape[0]
+    if block_table.dim() != 2 or cache.dim() != 3:
+        raise ValueError("block_table must be [B, max_blocks] and cache [pages, Hkv, page bytes]")
+    H = cache.shape[1]
+    if out is None:
+        out = {"out": torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device),
+               "lse": torch.empty((T, hq), dtype=torch.float32, device=q.device)}
+    qp, qs = _rows(q, "q")
+    lse = out.get("lse")
+    st = _lib.load().spec_kv4_attention(
+        B, T, hq, H, D, page_size, cache.shape[0], block_table.shape[1], qp, qs,
+        _cache(cache, H, D, page_size),
+        _dev(block_table, torch.int32, (B, block_table.shape[1]), "block_table"),
+        _dev(kv_lens, torch.int32, (B,), "kv_lens"), _dev(cu_new, torch.int32, (B + 1,), "cu_new"),
+        D ** -0.5 if scale is None else scale, k_scale, v_scale, max_new,
+        _dev(out["out"], torch.bfloat16, (T, hq, D), "out"),
+        0 if lse is None else _dev(lse, torch.float32, (T, hq), "lse"), _stream(stream, q))
+    _lib._check(st, "spec_kv4_attention")
+    return out
