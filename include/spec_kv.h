@@ -149,7 +149,7 @@ sv_status spec_kv4_append(int T, int Hkv, int D, int page_size, int num_pages, s
  *       sum, or NULL. Rows of no sequence are not written.
  * Scores, softmax and sums are held in float32; products take float16 operands: keys and values
  * are exact in it, queries too (scaled by a power of two), the softmax's weights are rounded to
- * it (2^-11 / 2 relative).
+ * it (by up to 2^-11 of each, or 2^-32 of the row's largest where that is more).
  */
 sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
                              int max_blocks, const void* q, long long q_token_stride,

@@ -194,14 +194,14 @@ def read_head(cache, pages, length, head, page_size, D, gk, gv):
 # ------------------------------------------------------------------------------ attention
 def attention(q, cache, block_table, kv_lens, cu_new, page_size, scale, gk, gv):
     """q [T, Hq, D] -> dict of out [T, Hq, D], lse [T, Hq], and for error bounds room [T, Hq, D]
-    = sum p |v| and zroom [T, Hq] = the largest sum |q k| * scale of a token seen. Rows of no
-    sequence are NaN in ``out`` and ``lse``."""
+    = sum p |v|, vsum [T, Hq, D] = sum |v| and zroom [T, Hq] = the largest sum |q k| * scale of a
+    token seen. Rows of no sequence are NaN in ``out`` and ``lse``."""
     q = np.asarray(q, np.float64)
     T, Hq, D = q.shape
     H, most = cache.shape[1], block_table.shape[1] * page_size
     G = Hq // H
     out, lse = np.full(q.shape, np.nan), np.full((T, Hq), np.nan)
-    room, zroom = np.zeros(q.shape), np.zeros((T, Hq))
+    room, vsum, zroom = np.zeros(q.shape), np.zeros(q.shape), np.zeros((T, Hq))
     for b in range(len(kv_lens)):
         r0, r1 = int(cu_new[b]), int(cu_new[b + 1])
         n, L = r1 - r0, min(max(int(kv_lens[b]), 0), most)
@@ -221,5 +221,6 @@ def attention(q, cache, block_table, kv_lens, cu_new, page_size, scale, gk, gv):
                         out[row, h] = p @ V[:seen] / p.sum()
                         lse[row, h] = m + math.log(p.sum()) if p.sum() > 0 else math.nan
                         room[row, h] = p @ np.abs(V[:seen]) / p.sum()
+                        vsum[row, h] = np.abs(V[:seen]).sum(0)
                         zroom[row, h] = (np.abs(K[:seen]) @ np.abs(q[row, h])).max() * abs(scale)
-    return {"out": out, "lse": lse, "room": room, "zroom": zroom}
+    return {"out": out, "lse": lse, "room": room, "vsum": vsum, "zroom": zroom}

@@ -40,7 +40,9 @@ struct StreamRes {
   size_t scr_bytes = 0;
   void* dd = nullptr;     // deferred draws of the walk (sv::walk_draw_carve) for batches of up
   int dd_cap = 0;         // to dd_cap sequences: order list (all zero between calls), decisions,
-};                        // masses
+                          // masses
+  void* att = nullptr;    // attention over the cache: error word, arrivals, pieces (sv_kv.h)
+};
 
 // Workspace of spec_verify_noalloc: the queue counters and error word the kernel needs (256
 // bytes), for batches of up to kNoAllocMaxB sequences, in device memory that belongs to this
@@ -69,14 +71,14 @@ sv_status noalloc_array(int dev, bool create, void** ws) {
   return SV_OK;
 }
 
-// Reads the error word of a workspace (after the caller synchronised its stream) and clears it.
+// Reads a workspace's error word (after the caller synchronised its stream) and clears it.
 // Returns SV_ERR_DEVICE_TIMEOUT if it was raised.
-sv_status take_error(Workspace* ws) {
+sv_status take_error(unsigned int* word) {
   unsigned int err = 0;
-  if (cudaMemcpy(&err, &ws->error, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpy(&err, word, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess)
     return SV_ERR_CUDA;
   if (!err) return SV_OK;
-  if (cudaMemset(&ws->error, 0, sizeof(err)) != cudaSuccess) return SV_ERR_CUDA;
+  if (cudaMemset(word, 0, sizeof(err)) != cudaSuccess) return SV_ERR_CUDA;
   return SV_ERR_DEVICE_TIMEOUT;
 }
 
@@ -832,27 +834,33 @@ sv_status spec_verify_device_error(void* stream) {
   if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
   Workspace* ws = nullptr;
   void* fixed = nullptr;
+  unsigned* att = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     auto it = g_res.find({dev, s});
-    if (it != g_res.end()) ws = it->second.ws;
+    if (it != g_res.end()) {
+      ws = it->second.ws;
+      att = static_cast<unsigned*>(it->second.att);
+    }
     const sv_status st = noalloc_array(dev, false, &fixed);
     if (st != SV_OK) return st;
   }
   if (cudaStreamSynchronize(s) != cudaSuccess) return SV_ERR_CUDA;
-  // both words are read and cleared, so one report covers both
-  const sv_status a = ws ? take_error(ws) : SV_OK;
-  const sv_status b = fixed ? take_error(static_cast<Workspace*>(fixed)) : SV_OK;
-  if (a == SV_ERR_CUDA || b == SV_ERR_CUDA) return SV_ERR_CUDA;
-  return (a == SV_ERR_DEVICE_TIMEOUT || b == SV_ERR_DEVICE_TIMEOUT) ? SV_ERR_DEVICE_TIMEOUT
-                                                                    : SV_OK;
+  // every word is read and cleared, so one report covers them all
+  const sv_status a = ws ? take_error(&ws->error) : SV_OK;
+  const sv_status b = fixed ? take_error(&static_cast<Workspace*>(fixed)->error) : SV_OK;
+  const sv_status c = att ? take_error(att) : SV_OK;
+  if (a == SV_ERR_CUDA || b == SV_ERR_CUDA || c == SV_ERR_CUDA) return SV_ERR_CUDA;
+  return (a == SV_ERR_DEVICE_TIMEOUT || b == SV_ERR_DEVICE_TIMEOUT || c == SV_ERR_DEVICE_TIMEOUT)
+             ? SV_ERR_DEVICE_TIMEOUT
+             : SV_OK;
 }
 
 sv_status spec_verify_workspace_error(void* workspace, void* stream) {
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return SV_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return SV_ERR_CUDA;
-  return take_error(static_cast<Workspace*>(workspace));
+  return take_error(&static_cast<Workspace*>(workspace)->error);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1128,8 +1136,34 @@ sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size
   P.vs = v_scale;
   P.out = out;
   P.lse = out_lse;
-  return sv::launch_attention(P, D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SV_OK
-                                                                                      : SV_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
+    const int sms = sm_count(dev);
+    if (sms <= 0 || 2 * sms > sv::kAttnMaxCtas) return SV_ERR_CUDA;
+    StreamRes& r = g_res[{dev, s}];
+    if (!r.att) {  // one size for every call: a captured call's workspace never moves
+      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+      if (cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
+        return SV_ERR_UNSUPPORTED;  // the workspace must exist before capture
+      const size_t need = sv::attention_workspace_bytes(sms);
+      void* w = nullptr;
+      if (cudaMalloc(&w, need) != cudaSuccess || cudaMemset(w, 0, need) != cudaSuccess) {
+        if (w) cudaFree(w);
+        return SV_ERR_CUDA;
+      }
+      r.att = w;
+    }
+    unsigned char* base = static_cast<unsigned char*>(r.att);
+    P.err = reinterpret_cast<unsigned*>(base);
+    P.arrived = reinterpret_cast<unsigned*>(base + 256);
+    P.part = reinterpret_cast<float*>(base + sv::kAttnHeader);
+    return sv::launch_attention(P, D, max_new, sms, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  } catch (...) {
+    return SV_ERR_CUDA;  // no memory for the host's table
+  }
 }
 
 const char* spec_verify_status_string(sv_status status) {

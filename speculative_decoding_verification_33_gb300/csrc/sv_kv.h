@@ -41,8 +41,18 @@ struct AttnParams {
   float vs;   // v_scale
   void* out;
   float* lse;
+  // workspace: error word, arrivals at the items cut between CTAs (zero between calls), pieces
+  unsigned* err;
+  unsigned* arrived;
+  float* part;
 };
 
-cudaError_t launch_attention(const AttnParams& P, int D, cudaStream_t stream);
+constexpr size_t kAttnHeader = 4096;  // bytes before the pieces: error word at 0, arrivals from 256
+constexpr int kAttnMaxCtas = (4096 - 256) / 4;
+
+// Bytes of the attention workspace on a device with `sms` multiprocessors; zeroed once.
+size_t attention_workspace_bytes(int sms);
+cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
+                             cudaStream_t stream);
 
 }  // namespace sv

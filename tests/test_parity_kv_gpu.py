@@ -302,13 +302,13 @@ def random_cache(pages, H, ps, D, seed):
 
 
 def _tolerance(ref, D):
-    """Per value: half a bf16 step; weights rounded to float16 (2^-11 of each, in the numerator
-    alone); scores summed in float32 (2^-24 of the magnitudes a step, D products and the scalings)
+    """Per value: half a bf16 step; weights rounded to float16 (2^-11 of each, or half its smallest
+    step of 2^-24 where the row's largest weight is 2^7, in the numerator alone); scores summed in float32 (2^-24 of the magnitudes a step, D products and the scalings)
     and exponentials (2^-22), each in numerator and denominator; the weighted sum (as much
     again)."""
     dz = (D + 8) * 2.0 ** -24 * ref["zroom"] + np.abs(np.nan_to_num(ref["lse"], neginf=0)) * 2.0 ** -22
     tol = 2.0 ** -8 * np.abs(ref["out"]) + ref["room"] * (2.0 ** -11 + 2 * dz[..., None] + 2.0 ** -19)
-    return tol + 1e-30, dz + 2.0 ** -20
+    return tol + 2.0 ** -32 * ref["vsum"] + 1e-30, dz + 2.0 ** -20
 
 
 def _compare(o, ref, D):
@@ -460,7 +460,7 @@ def test_attention_long_and_many(B, L, n, hq, hk, D, ps):
     q = torch.randn(T, hq, D, device="cuda", generator=g).to(BF16)
     o = sv.kv4_attention(q, cache, table, lens, cu, page_size=ps, max_new=n)
     ref = {"out": np.zeros((T, hq, D)), "lse": np.zeros((T, hq)), "room": np.zeros((T, hq, D)),
-           "zroom": np.zeros((T, hq))}
+           "vsum": np.zeros((T, hq, D)), "zroom": np.zeros((T, hq))}
     G = hq // hk
     for b in range(B):
         r0, r1, m = int(cu[b]), int(cu[b + 1]), int(lens[b])
@@ -472,6 +472,7 @@ def test_attention_long_and_many(B, L, n, hq, hk, D, ps):
             p = z.softmax(-1)
             ref["out"][r0:r1, h], ref["lse"][r0:r1, h] = host(p @ V), host(z.logsumexp(-1))
             ref["room"][r0:r1, h] = host(p @ V.abs())
+            ref["vsum"][r0:r1, h] = host(V.abs().sum(0))
             ref["zroom"][r0:r1, h] = host((x.abs() @ K.abs().T).amax(-1) * D ** -0.5)
     _compare(o, ref, D)
     again = sv.kv4_attention(q, cache, table, lens, cu, page_size=ps, max_new=n)
