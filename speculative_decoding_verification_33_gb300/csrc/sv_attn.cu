@@ -2,7 +2,7 @@
 //
 // Everything that a sequence's rows (new tokens x query heads of one key/value head) need of the
 // cache is read once for all of them: a block of 16 tokens is 18 D bytes, its products with R
-// rows 64 D R operations. The unit of work is one block for one tile of R = 8 NT rows. All
+// rows 64 D R operations. The unit of work is two blocks for one tile of R = 8 NT rows. All
 // units of the call, sequence after sequence, are cut into equal runs, one per persistent CTA, so that the
 // load is even whatever the lengths are; a head that is cut has its pieces joined by the last
 // CTA that finishes one of them, in their order, so results do not depend on timing. The warps
@@ -26,6 +26,7 @@
 
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "spec_kv.h"
 #include "sv_kv.h"
@@ -38,15 +39,19 @@ constexpr long long kWaitCycles = 4000000000LL;  // about 2 s: a copy that never
 constexpr float kLift = 7.f;    // weights are held times 2^7: float16 has more room above 1 than below
 constexpr float kSlack = 15.f;  // and may grow to 2^15 before the running maximum is moved
 
+constexpr int kUnit = 32;  // tokens of a unit: two blocks
+
 template <int D, int NT>
 struct AttnShape {
   static constexpr int kWarps = NT == 2 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPerSm = NT == 1 ? 2 : 1;   // CTAs an SM, by registers
   static constexpr int kRows = 8 * NT;
+  static constexpr bool kJoint = D == 64 || NT == 1 || NT == 3;  // by registers
   static constexpr int kBlock = KvBlock<D>::kBytes;
-  static constexpr int kStages = (NT == 1 ? 3 : NT == 2 ? 4 : 6) * (128 / D);
-  static constexpr int kRing = kWarps * kStages * kBlock;
+  static constexpr int kStages = (NT <= 2 ? 2 : 3) * (128 / D);
+  static constexpr int kStage = 2 * kBlock;
+  static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kQ = NT * (D / 16) * 32 * 8;
   static constexpr int kOutStride = D + 4;  // floats of a row of the joining buffer
   static constexpr int kOut = kWarps * 8 * kOutStride * 4;
@@ -55,11 +60,11 @@ struct AttnShape {
   static constexpr int kPart = kRows * (D + 2);  // floats of one piece's results
 };
 
-// Where a run of units lies: item (sequence b, head h, row tile rt) with its blocks.
+// Where a run of units lies: item (sequence b, head h, row tile rt) with its nu units.
 struct Walk {
-  long long base;  // unit of the item's first block
+  long long base;  // the item's first unit
   int b, h, rt;
-  int rts, nblk, len, n, r0;
+  int rts, nu, len, n, r0;
 };
 
 __device__ __forceinline__ void load_seq(const AttnParams& P, int rows_tile, int b, Walk& w) {
@@ -69,13 +74,13 @@ __device__ __forceinline__ void load_seq(const AttnParams& P, int rows_tile, int
   w.n = c1 - c0;
   w.len = min(max(P.lens[b], 0), P.max_blocks * P.ps);
   w.rts = (w.n * P.group + rows_tile - 1) / rows_tile;
-  w.nblk = max(1, (w.len + 15) >> 4);
+  w.nu = max(1, (w.len + kUnit - 1) / kUnit);
 }
 __device__ __forceinline__ long long seq_units(const AttnParams& P, const Walk& w) {
-  return static_cast<long long>(w.rts) * P.hkv * w.nblk;
+  return static_cast<long long>(w.rts) * P.hkv * w.nu;
 }
 __device__ __forceinline__ void next_item(const AttnParams& P, int rows_tile, Walk& w) {
-  w.base += w.nblk;
+  w.base += w.nu;
   if (++w.rt < w.rts) return;
   w.rt = 0;
   if (++w.h < P.hkv) return;
@@ -84,7 +89,7 @@ __device__ __forceinline__ void next_item(const AttnParams& P, int rows_tile, Wa
   do {
     if (++b >= P.B) {
       w.b = P.B;
-      w.nblk = 1 << 30;  // nothing follows
+      w.nu = 1 << 30;  // nothing follows
       return;
     }
     load_seq(P, rows_tile, b, w);
@@ -127,13 +132,100 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Keys of a block's 16 tokens as operands: token g in registers 0 and 2 of a step, g + 8 in 1 and 3
+template <int D>
+__device__ __forceinline__ void key_operands(const unsigned char* sb, int g, int c,
+                                             uint32_t (&f)[D / 16][4]) {
+  constexpr int N = D / 32;  // words of a thread's codes of one token
+  uint32_t ka[N], kb[N], sa[2], sc[2];
+  if (D == 128) {
+    *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(sb + g * 64 + c * 16);
+    *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(sb + g * 64 + 512 + c * 16);
+    const uint32_t x = e4m3x2(*reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kKeyScales + g * 8 + 2 * c));
+    const uint32_t y = e4m3x2(*reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kKeyScales + 64 + g * 8 + 2 * c));
+    sa[0] = __byte_perm(x, x, 0x1010);
+    sa[1] = __byte_perm(x, x, 0x3232);
+    sc[0] = __byte_perm(y, y, 0x1010);
+    sc[1] = __byte_perm(y, y, 0x3232);
+  } else {
+    *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(sb + g * 32 + c * 8);
+    *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(sb + g * 32 + 256 + c * 8);
+    const uint32_t x = sb[KvBlock<D>::kKeyScales + g * 4 + c];
+    const uint32_t y = sb[KvBlock<D>::kKeyScales + 32 + g * 4 + c];
+    sa[0] = sa[1] = e4m3x2(x | (x << 8));
+    sc[0] = sc[1] = e4m3x2(y | (y << 8));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {  // 8 values, two steps of the inner dimension
+    uint32_t a[4], b[4];
+    e2m1x8(ka[i], a);
+    e2m1x8(kb[i], b);
+    const int k = D == 128 ? i / 2 : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f[2 * i + h][0] = mul_f16x2(a[2 * h], sa[k]);
+      f[2 * i + h][1] = mul_f16x2(b[2 * h], sc[k]);
+      f[2 * i + h][2] = mul_f16x2(a[2 * h + 1], sa[k]);
+      f[2 * i + h][3] = mul_f16x2(b[2 * h + 1], sc[k]);
+    }
+  }
+}
+
+// Values of a block as operands, D / 8 values of the token pairs c and c + 4. A token that some
+// row does not see must not reach it as 0 * NaN: in a masked block its scale is taken as 0 where the
+// cache holds nothing (past the length) or a NaN; `nan_at` bit i then says that token i, which
+// some rows see, has a NaN scale among this thread's values.
+template <int D>
+__device__ __forceinline__ void value_operands(const unsigned char* sb, int g, int c, bool masked,
+                                               int t0, int len, int all_see,
+                                               uint32_t (&f)[D / 16][4], uint32_t& nan_at) {
+  constexpr int N = D / 32;  // words of a thread's codes of one token pair
+  uint32_t va[N], vb[N], fa, fb;
+  if (D == 128) {
+    const int at = c * 128 + 16 * KvBlock<D>::place(c, g);
+    *reinterpret_cast<uint4*>(va) = *reinterpret_cast<const uint4*>(sb + KvBlock<D>::kValCodes + at);
+    *reinterpret_cast<uint4*>(vb) = *reinterpret_cast<const uint4*>(sb + KvBlock<D>::kValCodes + 512 + at);
+    fa = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + c * 16 + 2 * g);
+    fb = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + 64 + c * 16 + 2 * g);
+  } else {
+    const int at = c * 64 + 8 * KvBlock<D>::place(c, g);
+    *reinterpret_cast<uint2*>(va) = *reinterpret_cast<const uint2*>(sb + KvBlock<D>::kValCodes + at);
+    *reinterpret_cast<uint2*>(vb) = *reinterpret_cast<const uint2*>(sb + KvBlock<D>::kValCodes + 256 + at);
+    fa = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + c * 8 + 2 * (g >> 1));
+    fb = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + 32 + c * 8 + 2 * (g >> 1));
+  }
+  if (masked) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = 2 * c + (k & 1) + 8 * (k >> 1), sh = 8 * (k & 1);
+      uint32_t& s = k < 2 ? fa : fb;
+      const bool bad = ((s >> sh) & 0x7Fu) == 0x7Fu;
+      if (t0 + i >= len || (bad && t0 + i >= all_see)) s &= ~(0xFFu << sh);
+      if (bad && t0 + i < len && t0 + i >= all_see) nan_at |= 1u << i;
+    }
+  }
+  fa = e4m3x2(fa);
+  fb = e4m3x2(fb);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t a[4], b[4];
+    e2m1x8(va[i], a);
+    e2m1x8(vb[i], b);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f[2 * i + h][0] = mul_f16x2(a[2 * h], fa);
+      f[2 * i + h][1] = mul_f16x2(a[2 * h + 1], fa);
+      f[2 * i + h][2] = mul_f16x2(b[2 * h], fb);
+      f[2 * i + h][3] = mul_f16x2(b[2 * h + 1], fb);
+    }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::kPerSm)
     attn_kernel(AttnParams P) {
   using S = AttnShape<D, NT>;
   constexpr int W = S::kWarps, NS = S::kStages, R = S::kRows, KS = D / 16, MT = D / 16;
-  constexpr int QW = D / 32;  // 32-bit words of a thread's key codes of one token
-  constexpr int VW = D / 32;  // ... and of its value codes of one token pair
   extern __shared__ __align__(128) unsigned char smem[];
   unsigned char* ring = smem;
   uint2* sq = reinterpret_cast<uint2*>(smem + S::kRing);  // query operands [NT][KS][lane]
@@ -202,56 +294,62 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     }
     __syncthreads();
     load_seq(P, R, static_cast<int>(s_start[0]), w);
-    const long long item = (u0 - s_start[1]) / w.nblk;
+    const long long item = (u0 - s_start[1]) / w.nu;
     w.h = static_cast<int>(item / w.rts);
     w.rt = static_cast<int>(item - static_cast<long long>(w.h) * w.rts);
-    w.base = s_start[1] + item * w.nblk;
+    w.base = s_start[1] + item * w.nu;
   }
 
   // ---- the warp's producer: copies of its units, kStages ahead
-  unsigned char* my_ring = ring + warp * NS * S::kBlock;
+  unsigned char* my_ring = ring + warp * NS * S::kStage;
   uint64_t* my_bar = bars + warp * NS;
   const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
   Walk pw = w;
   long long pu = u0 + warp;
-  int page = -1;
-  uint32_t absent = 0, phase = 0;  // per stage: nothing copied; parity of the next copy's phase
+  int page[2] = {-1, -1};          // pages of unit pu's blocks; -1: nothing to copy
+  uint32_t absent = 0, phase = 0;  // per stage and block: not copied; per stage: next copy's parity
   bool dead = false;
-  auto fetch_page = [&]() {  // page of unit pu, if there is one
-    page = -1;
+  auto fetch_pages = [&]() {
+    page[0] = page[1] = -1;
     if (pu >= u1) return;
-    while (pu >= pw.base + pw.nblk) next_item(P, R, pw);
-    if (pw.len > 0)
-      page = P.table[static_cast<long long>(pw.b) * P.max_blocks +
-                     (static_cast<int>(pu - pw.base) >> bpp_log)];
+    while (pu >= pw.base + pw.nu) next_item(P, R, pw);
+    const int blk = 2 * static_cast<int>(pu - pw.base);
+    const int32_t* row = P.table + static_cast<long long>(pw.b) * P.max_blocks;
+    if (16 * blk < pw.len) page[0] = row[blk >> bpp_log];
+    if (16 * blk + 16 < pw.len) page[1] = bpp_log ? page[0] : row[blk + 1];
   };
   auto issue = [&](int stage) {  // copy unit pu into the stage, move on to the next unit
     if (pu >= u1) return;
-    const bool there = page >= 0 && page < P.num_pages && !dead;
-    if (there) {
-      absent &= ~(1u << stage);
-      if (lane == 0) {
-        const int in_page = static_cast<int>(pu - pw.base) & ((1 << bpp_log) - 1);
-        const unsigned char* src =
-            P.cache +
-            (((static_cast<long long>(page) * P.hkv + pw.h) << bpp_log) + in_page) * S::kBlock;
-        mbar_arrive_expect_tx(&my_bar[stage], S::kBlock);
-        bulk_g2s(my_ring + stage * S::kBlock, src, S::kBlock, &my_bar[stage]);
+    const bool h0 = static_cast<unsigned>(page[0]) < static_cast<unsigned>(P.num_pages) && !dead;
+    const bool h1 = static_cast<unsigned>(page[1]) < static_cast<unsigned>(P.num_pages) && !dead;
+    absent = (absent & ~(3u << (2 * stage))) | ((h0 ? 0u : 1u) | (h1 ? 0u : 2u)) << (2 * stage);
+    if (lane == 0 && (h0 || h1)) {
+      mbar_arrive_expect_tx(&my_bar[stage], (h0 + h1) * S::kBlock);
+      const int in_page = 2 * static_cast<int>(pu - pw.base) & ((1 << bpp_log) - 1);
+      unsigned char* to = my_ring + stage * S::kStage;
+      if (bpp_log) {  // neighbours in one page
+        bulk_g2s(to, P.cache + (((static_cast<long long>(page[0]) * P.hkv + pw.h) << bpp_log) + in_page) * S::kBlock,
+                 (h0 + h1) * S::kBlock, &my_bar[stage]);
+      } else {
+        if (h0)
+          bulk_g2s(to, P.cache + (static_cast<long long>(page[0]) * P.hkv + pw.h) * S::kBlock,
+                   S::kBlock, &my_bar[stage]);
+        if (h1)
+          bulk_g2s(to + S::kBlock, P.cache + (static_cast<long long>(page[1]) * P.hkv + pw.h) * S::kBlock,
+                   S::kBlock, &my_bar[stage]);
       }
-    } else {
-      absent |= 1u << stage;
     }
     pu += W;
-    fetch_page();
+    fetch_pages();
   };
-  fetch_page();
+  fetch_pages();
   for (int i = 0; i < NS; ++i) issue(i);
 
   // ---- items of the run
   long long cu = u0 + warp;  // next unit of this warp
   int stage = 0;
   while (w.base < u1) {
-    const long long ua = max(w.base, u0), ub = min(w.base + w.nblk, u1);
+    const long long ua = max(w.base, u0), ub = min(w.base + w.nu, u1);
     const int rows = min(R, w.n * P.group - w.rt * R);  // rows of this tile
     const int tiles = (rows + 7) >> 3;
     // queries as float16 operands: each row times a power of two that brings its largest value
@@ -305,185 +403,180 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       l[t][0] = l[t][1] = 0.f;
     }
 
-    for (; cu < ub; cu += W) {
-      const unsigned char* sb = my_ring + stage * S::kBlock;
-      const bool gone = (absent >> stage) & 1u;
-      bool lost = gone;
-      if (!gone) {
-        if (!mbar_wait_bounded(&my_bar[stage], (phase >> stage) & 1u, kWaitCycles)) {
-          if (lane == 0) atomicOr(P.err, 1u);
-          dead = lost = true;
+    // The warp's units of this item, for TN tiles of rows: no branch on the tile inside
+    auto run = [&](auto tn) {
+      constexpr int TN = decltype(tn)::value;
+      for (; cu < ub; cu += W) {
+        const unsigned char* sb = my_ring + stage * S::kStage;
+        const int t0 = static_cast<int>(cu - w.base) * kUnit;
+        uint32_t lost = (absent >> (2 * stage)) & 3u;  // blocks that are not there
+        if (lost != 3u) {
+          const bool ok = mbar_wait_bounded(&my_bar[stage], (phase >> stage) & 1u, kWaitCycles);
+          phase ^= 1u << stage;
+          if (__any_sync(0xFFFFFFFFu, !ok)) {
+            if (lane == 0) atomicOr(P.err, 1u);
+            dead = true;
+            lost = 3u;
+          }
         }
-        phase ^= 1u << stage;
-      }
-      lost = __any_sync(0xFFFFFFFFu, lost);
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      const int t0 = static_cast<int>(cu - w.base) * 16;
-      const bool masked = t0 + 16 > all_see;
+        const bool masked = t0 + kUnit > all_see || lost;
 
-      // scores of 16 tokens and the tile's rows
-      float s[NT][4];
+        // scores of 32 tokens and the tile's rows
+        float s[2][TN][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      {
-        uint32_t ka[QW], kb[QW], sa[2], sc[2];  // tokens g and g + 8: codes, scales of 16 values each
-        if (D == 128) {
-          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(sb + g * 64 + c * 16);
-          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(sb + g * 64 + 512 + c * 16);
-          const uint32_t x = e4m3x2(*reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kKeyScales + g * 8 + 2 * c));
-          const uint32_t y = e4m3x2(*reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kKeyScales + 64 + g * 8 + 2 * c));
-          sa[0] = __byte_perm(x, x, 0x1010);
-          sa[1] = __byte_perm(x, x, 0x3232);
-          sc[0] = __byte_perm(y, y, 0x1010);
-          sc[1] = __byte_perm(y, y, 0x3232);
-        } else {
-          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(sb + g * 32 + c * 8);
-          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(sb + g * 32 + 256 + c * 8);
-          const uint32_t x = sb[KvBlock<D>::kKeyScales + g * 4 + c];
-          const uint32_t y = sb[KvBlock<D>::kKeyScales + 32 + g * 4 + c];
-          sa[0] = sa[1] = e4m3x2(x | (x << 8));
-          sc[0] = sc[1] = e4m3x2(y | (y << 8));
-        }
+        for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-        for (int i = 0; i < QW; ++i) {  // 8 values, two steps of the inner dimension
-          uint32_t a[4], b[4];
-          e2m1x8(ka[i], a);
-          e2m1x8(kb[i], b);
-          const uint32_t fa = sa[D == 128 ? i / 2 : 0], fb = sc[D == 128 ? i / 2 : 0];
+          for (int t = 0; t < TN; ++t) s[hb][t][0] = s[hb][t][1] = s[hb][t][2] = s[hb][t][3] = 0.f;
+        if constexpr (S::kJoint) {  // a query operand loaded once for both blocks
+          uint32_t kf[2][KS][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = mul_f16x2(a[k], fa);
-            b[k] = mul_f16x2(b[k], fb);
-          }
+          for (int hb = 0; hb < 2; ++hb) key_operands<D>(sb + hb * S::kBlock, g, c, kf[hb]);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t > 0 && t >= tiles) break;
-            const uint2 q0 = sq[(t * KS + 2 * i) * 32 + lane], q1 = sq[(t * KS + 2 * i + 1) * 32 + lane];
-            mma16816(s[t], a[0], b[0], a[1], b[1], q0.x, q0.y);
-            mma16816(s[t], a[2], b[2], a[3], b[3], q1.x, q1.y);
-          }
-        }
-      }
-      bool move = false;
+          for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t > 0 && t >= tiles) break;
-        const float2 qc = *reinterpret_cast<const float2*>(sqc + 8 * t + 2 * c);
+            for (int t = 0; t < TN; ++t) {
+              const uint2 q = sq[(t * KS + i) * 32 + lane];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s[t][k] *= k & 1 ? qc.y : qc.x;
-          if (masked || lost) {
-            const bool sees = t0 + g + 8 * (k >> 1) < svis[8 * t + 2 * c + (k & 1)];
-            s[t][k] = !sees ? -INFINITY : lost ? NAN : s[t][k];
-          }
-          move |= s[t][k] - m[t][k & 1] > kSlack;
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, move)) {  // a new maximum of some row
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t > 0 && t >= tiles) break;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(s[t][e], s[t][e + 2]);
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            x = fmaxf(m[t][e], x - kLift);
-            const float f = ex2_fast(m[t][e] - x);
-            m[t][e] = x;
-            l[t][e] *= f;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              O[t][j][e] *= f;
-              O[t][j][e + 2] *= f;
+              for (int hb = 0; hb < 2; ++hb)
+                mma16816(s[hb][t], kf[hb][i][0], kf[hb][i][1], kf[hb][i][2], kf[hb][i][3], q.x, q.y);
             }
+        } else {  // half the registers
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+            uint32_t kf[KS][4];
+            key_operands<D>(sb + hb * S::kBlock, g, c, kf);
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+              for (int t = 0; t < TN; ++t) {
+                const uint2 q = sq[(t * KS + i) * 32 + lane];
+                mma16816(s[hb][t], kf[i][0], kf[i][1], kf[i][2], kf[i][3], q.x, q.y);
+              }
           }
         }
-      }
-      uint32_t p[NT][2];
+        // exponents: score * factor of the row - maximum of the row
+        float x[2][TN][4];
+        float top = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (t > 0 && t >= tiles) break;
-        float x[4];
+        for (int t = 0; t < TN; ++t) {
+          const float2 qc = *reinterpret_cast<const float2*>(sqc + 8 * t + 2 * c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[k] = ex2_fast(s[t][k] - m[t][k & 1]);
-          l[t][k & 1] += x[k];
+          for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[hb][t][k] = fmaf(s[hb][t][k], k & 1 ? qc.y : qc.x, -m[t][k & 1]);
         }
-        p[t][0] = transpose8x8(pack_f16(x[0], x[1]));
-        p[t][1] = transpose8x8(pack_f16(x[2], x[3]));
-      }
-
-      // outputs: 2 token pairs of this thread, D / 8 values of each
-      if (!lost) {
-        uint32_t va[VW], vb[VW], fa, fb;
-        if (D == 128) {
-          const int at = c * 128 + 16 * KvBlock<D>::place(c, g);
-          *reinterpret_cast<uint4*>(va) = *reinterpret_cast<const uint4*>(sb + KvBlock<D>::kValCodes + at);
-          *reinterpret_cast<uint4*>(vb) = *reinterpret_cast<const uint4*>(sb + KvBlock<D>::kValCodes + 512 + at);
-          fa = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + c * 16 + 2 * g);
-          fb = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + 64 + c * 16 + 2 * g);
-        } else {
-          const int at = c * 64 + 8 * KvBlock<D>::place(c, g);
-          *reinterpret_cast<uint2*>(va) = *reinterpret_cast<const uint2*>(sb + KvBlock<D>::kValCodes + at);
-          *reinterpret_cast<uint2*>(vb) = *reinterpret_cast<const uint2*>(sb + KvBlock<D>::kValCodes + 256 + at);
-          fa = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + c * 8 + 2 * (g >> 1));
-          fb = *reinterpret_cast<const uint16_t*>(sb + KvBlock<D>::kValScales + 32 + c * 8 + 2 * (g >> 1));
-        }
-        // A token that some row does not see must not reach it as 0 * NaN: its scale is taken as 0
-        // where the cache holds nothing (past the length) or a NaN, and the rows that do see a
-        // NaN get it below.
-        uint32_t nan_at = 0;  // bit i: token t0 + i has a NaN scale in this thread's 16 values
+        uint32_t hidden = 0;  // a bit a score: tokens that the row does not see
         if (masked) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = 2 * c + (k & 1) + 8 * (k >> 1);
-            uint32_t& f = k < 2 ? fa : fb;
-            const int sh = 8 * (k & 1);
-            const bool bad = ((f >> sh) & 0x7Fu) == 0x7Fu;
-            if (t0 + i >= w.len || (bad && t0 + i >= all_see)) f &= ~(0xFFu << sh);
-            if (bad && t0 + i < w.len && t0 + i >= all_see) nan_at |= 1u << i;
-          }
+          for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (t0 + 16 * hb + g + 8 * (k >> 1) >= svis[8 * t + 2 * c + (k & 1)]) {
+                  x[hb][t][k] = -INFINITY;
+                  hidden |= 1u << (8 * t + 4 * hb + k);
+                } else if ((lost >> hb) & 1u) {
+                  x[hb][t][k] = s[hb][t][k] = NAN;
+                }
         }
-        fa = e4m3x2(fa);
-        fb = e4m3x2(fb);
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
-          uint32_t a[4], b[4];
-          e2m1x8(va[i], a);
-          e2m1x8(vb[i], b);
+        for (int t = 0; t < TN; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a[k] = mul_f16x2(a[k], fa);
-            b[k] = mul_f16x2(b[k], fb);
-          }
+          for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if (t > 0 && t >= tiles) break;
-            mma16816(O[t][2 * i], a[0], a[1], b[0], b[1], p[t][0], p[t][1]);
-            mma16816(O[t][2 * i + 1], a[2], a[3], b[2], b[3], p[t][0], p[t][1]);
-          }
-        }
-        if (masked && __any_sync(0xFFFFFFFFu, nan_at != 0)) {
-          nan_at |= __shfl_xor_sync(0xFFFFFFFFu, nan_at, 1);
-          nan_at |= __shfl_xor_sync(0xFFFFFFFFu, nan_at, 2);
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, x[hb][t][k]);
+        if (__any_sync(0xFFFFFFFFu, top > kSlack)) {  // a new maximum of some row
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < TN; ++t) {
+            const float2 qc = *reinterpret_cast<const float2*>(sqc + 8 * t + 2 * c);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int seen = svis[8 * t + 2 * c + e] - t0;
-              const uint32_t sees = seen >= 16 ? 0xFFFFu : seen > 0 ? (1u << seen) - 1u : 0u;
-              if (nan_at & sees) {
+              const float f = e ? qc.y : qc.x;
+              float z[4], y = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) O[t][j][e] = O[t][j][e + 2] = NAN;
+              for (int k = 0; k < 4; ++k) {
+                const int i = e + 2 * (k & 1);
+                z[k] = (hidden >> (8 * t + 4 * (k >> 1) + i)) & 1u ? -INFINITY : s[k >> 1][t][i] * f;
+                y = fmaxf(y, z[k]);
               }
+              y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+              y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
+              y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+              y = fmaxf(m[t][e], y - kLift);
+              const float down = ex2_fast(m[t][e] - y);
+              m[t][e] = y;
+              l[t][e] *= down;
+#pragma unroll
+              for (int j = 0; j < MT; ++j) {
+                O[t][j][e] *= down;
+                O[t][j][e + 2] *= down;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k >> 1][t][e + 2 * (k & 1)] = z[k] - y;
             }
+          }
         }
+        uint32_t p[2][TN][2];
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[hb][t][k] = ex2_fast(x[hb][t][k]);
+              l[t][k & 1] += x[hb][t][k];
+            }
+            p[hb][t][0] = transpose8x8(pack_f16(x[hb][t][0], x[hb][t][1]));
+            p[hb][t][1] = transpose8x8(pack_f16(x[hb][t][2], x[hb][t][3]));
+          }
+
+        // outputs
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+          if (masked && ((lost >> hb) & 1u)) continue;  // its rows are NaN already
+          uint32_t nan_at = 0;
+          uint32_t vf[MT][4];
+          value_operands<D>(sb + hb * S::kBlock, g, c, masked, t0 + 16 * hb, w.len, all_see, vf, nan_at);
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+              mma16816(O[t][j], vf[j][0], vf[j][1], vf[j][2], vf[j][3], p[hb][t][0], p[hb][t][1]);
+          if (masked && __any_sync(0xFFFFFFFFu, nan_at != 0)) {
+            nan_at |= __shfl_xor_sync(0xFFFFFFFFu, nan_at, 1);
+            nan_at |= __shfl_xor_sync(0xFFFFFFFFu, nan_at, 2);
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int seen = svis[8 * t + 2 * c + e] - t0 - 16 * hb;
+                const uint32_t sees = seen >= 16 ? 0xFFFFu : seen > 0 ? (1u << seen) - 1u : 0u;
+                if (nan_at & sees) {
+#pragma unroll
+                  for (int j = 0; j < MT; ++j) O[t][j][e] = O[t][j][e + 2] = NAN;
+                }
+              }
+          }
+        }
+        __syncwarp();
+        issue(stage);
+        stage = stage + 1 == NS ? 0 : stage + 1;
       }
-      __syncwarp();
-      issue(stage);
-      stage = stage + 1 == NS ? 0 : stage + 1;
+    };
+    if constexpr (NT == 1) {
+      run(std::integral_constant<int, 1>());
+    } else if constexpr (NT == 2) {
+      if (tiles == 1) run(std::integral_constant<int, 1>());
+      else run(std::integral_constant<int, 2>());
+    } else if constexpr (NT == 3) {
+      if (tiles <= 2) run(std::integral_constant<int, 2>());
+      else run(std::integral_constant<int, 3>());
+    } else {
+      if (tiles <= 2) run(std::integral_constant<int, 2>());
+      else if (tiles == 3) run(std::integral_constant<int, 3>());
+      else run(std::integral_constant<int, 4>());
     }
 
     // ---- join the warps
@@ -500,7 +593,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           swl[warp * R + 8 * t + 2 * c + e] = x;
         }
       }
-    const bool whole = ua == w.base && ub == w.base + w.nblk;
+    const bool whole = ua == w.base && ub == w.base + w.nu;
     // a piece's place: a CTA has at most two, one from its start and one to its end
     const int my_slot = 2 * blockIdx.x + (ua == u0 ? 0 : 1);
     float* my_part = P.part + static_cast<long long>(my_slot) * S::kPart;
@@ -564,7 +657,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     if (!whole) {
       // pieces of this item lie with CTAs first .. last; the last of them to arrive joins them
       const int first = static_cast<int>(((w.base + 1) * ctas + U - 1) / U) - 1;
-      const int last = static_cast<int>(((w.base + w.nblk) * ctas + U - 1) / U) - 1;
+      const int last = static_cast<int>(((w.base + w.nu) * ctas + U - 1) / U) - 1;
       __threadfence();
       __syncthreads();
       if (tid == 0)
