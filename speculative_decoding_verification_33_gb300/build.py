@@ -19,7 +19,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libspecverify.so"
 SOURCES = ["sv_kernel.cu", "sv_api.cu", "sv_probe.cu", "sv_rows.cu", "sv_lmhead.cu",
            "sv_hverify.cu", "sv_greedy.cu", "sv_small.cu", "sv_tables.cu", "sv_normrope.cu",
-           "sv_kv4.cu", "sv_attn.cu"]
+           "sv_kv4.cu", "sv_attn.cu", "sv_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -63,7 +63,8 @@ KERNEL_SOURCES = {
     "tables": ("sv_tables.cu", "sv_kv.h"),
     "normrope": ("sv_normrope.cu", "sv_kv.h"),
     "append": ("sv_kv4.cu", "sv_kv.h"),
-    "attention": ("sv_attn.cu", "sv_kv.h", "sv_ptx.cuh"),
+    "attention": ("sv_attn.cu", "sv_attn.cuh", "sv_kv.h", "sv_ptx.cuh"),
+    "attention_tc": ("sv_attn_tc.cu", "sv_attn.cuh", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
 }
 
 

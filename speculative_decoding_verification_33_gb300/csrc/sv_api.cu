@@ -850,6 +850,9 @@ sv_status spec_verify_device_error(void* stream) {
   const sv_status a = ws ? take_error(&ws->error) : SV_OK;
   const sv_status b = fixed ? take_error(&static_cast<Workspace*>(fixed)->error) : SV_OK;
   const sv_status c = att ? take_error(att) : SV_OK;
+  // a call that gave up may have left arrivals at its cut items
+  if (c == SV_ERR_DEVICE_TIMEOUT && cudaMemset(att, 0, sv::kAttnHeader) != cudaSuccess)
+    return SV_ERR_CUDA;
   if (a == SV_ERR_CUDA || b == SV_ERR_CUDA || c == SV_ERR_CUDA) return SV_ERR_CUDA;
   return (a == SV_ERR_DEVICE_TIMEOUT || b == SV_ERR_DEVICE_TIMEOUT || c == SV_ERR_DEVICE_TIMEOUT)
              ? SV_ERR_DEVICE_TIMEOUT

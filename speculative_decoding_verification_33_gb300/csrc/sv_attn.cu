@@ -33,15 +33,12 @@
 #include <type_traits>
 
 #include "spec_kv.h"
+#include "sv_attn.cuh"
 #include "sv_kv.h"
 #include "sv_ptx.cuh"
 
 namespace sv {
 namespace {
-
-constexpr long long kWaitCycles = 4000000000LL;  // about 2 s: a copy that never came
-constexpr float kLift = 7.f;    // weights are held times 2^7: float16 has more room above 1 than below
-constexpr float kSlack = 15.f;  // and may grow to 2^15 before the running maximum is moved
 
 template <int D, int NT>
 struct AttnShape {
@@ -66,70 +63,9 @@ struct AttnShape {
   static_assert(2 * (kSmem + 4096 + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-// Where a run of units lies: item (sequence b, head h, row tile rt) with its nu units.
-struct Walk {
-  long long base;  // the item's first unit
-  int b, h, rt;
-  int rts, nu, len, n, r0;
-};
-
-template <int R, int UNIT>
-__device__ __forceinline__ void load_seq(const AttnParams& P, int b, Walk& w) {
-  const int c0 = min(max(P.cu[b], 0), P.T), c1 = min(max(P.cu[b + 1], c0), P.T);
-  w.b = b;
-  w.r0 = c0;
-  w.n = c1 - c0;
-  w.len = min(max(P.lens[b], 0), P.max_blocks * P.ps);
-  w.rts = (w.n * P.group + R - 1) / R;
-  w.nu = max(1, (w.len + UNIT - 1) / UNIT);
-}
-__device__ __forceinline__ long long seq_units(const AttnParams& P, const Walk& w) {
-  return static_cast<long long>(w.rts) * P.hkv * w.nu;
-}
-template <int R, int UNIT>
-__device__ __forceinline__ void next_item(const AttnParams& P, Walk& w) {
-  w.base += w.nu;
-  if (++w.rt < w.rts) return;
-  w.rt = 0;
-  if (++w.h < P.hkv) return;
-  w.h = 0;
-  int b = w.b;
-  do {
-    if (++b >= P.B) {
-      w.b = P.B;
-      w.nu = 1 << 30;  // nothing follows
-      return;
-    }
-    load_seq<R, UNIT>(P, b, w);
-  } while (w.n == 0);
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// The four bytes of `w` as four registers of two e2m1 values each, in float16
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(b)));
-  return r;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -262,7 +198,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   uint64_t* bars = reinterpret_cast<uint64_t*>(sqc + R);
   uint32_t* slost = reinterpret_cast<uint32_t*>(bars + NP * NS);  // per stage: blocks not there
   __shared__ long long s_scan[2 * NP];
-  __shared__ long long s_run[4];  // first unit, past the last, all units, CTAs that have any
+  __shared__ Run s_run;
   __shared__ Walk s_walk[2];
   __shared__ Producer s_prod[NP];
   __shared__ long long s_queue[NP][32][NB];  // where the blocks of a pair's next units lie
@@ -275,61 +211,13 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     fence_mbar_init();
   }
 
-  // ---- this CTA's run of units
-  {
-    Walk w;
-    const int per = (P.B + S::kThreads - 1) / S::kThreads;
-    const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      load_seq<R, UNIT>(P, b, w);
-      mine += seq_units(P, w);
-    }
-    long long x = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-      if (lane >= d) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long before = 0, U = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-      const long long n = s_scan[i];
-      if (i < warp) before += n;
-      U += n;
-    }
-    before += x - mine;
-    // every pair of a CTA gets a unit at least
-    const long long ctas = min(static_cast<long long>(gridDim.x), (U + NP - 1) / NP);
-    if (blockIdx.x >= ctas) return;
-    const long long u0 = U * blockIdx.x / ctas;
-    if (u0 >= before && u0 < before + mine) {
-      for (int b = b0; b < b1; ++b) {
-        load_seq<R, UNIT>(P, b, w);
-        const long long n = seq_units(P, w);
-        if (u0 < before + n) {
-          const long long item = (u0 - before) / w.nu;
-          w.h = static_cast<int>(item / w.rts);
-          w.rt = static_cast<int>(item - static_cast<long long>(w.h) * w.rts);
-          w.base = before + item * w.nu;
-          s_walk[0] = w;
-          s_run[0] = u0;
-          s_run[1] = U * (blockIdx.x + 1) / ctas;
-          s_run[2] = U;
-          s_run[3] = ctas;
-          for (int i = 0; i < NP; ++i) {
-            s_prod[i].w = w;
-            s_prod[i].u = u0 + i;
-          }
-          break;
-        }
-        before += n;
-      }
-    }
-    __syncthreads();
+  // this CTA's run of units; every pair of a CTA gets a unit at least
+  if (!find_run<S::kThreads, R, UNIT>(P, NP, s_scan, &s_run, &s_walk[0])) return;
+  if (tid < NP) {
+    s_prod[tid].w = s_walk[0];
+    s_prod[tid].u = s_run.u0 + tid;
   }
+  __syncthreads();
 
   // ---- the pair's producer, its first warp: copies of its units into the ring. Where the blocks of
   // the next 32 units lie is looked up 32 at a time, a lane a unit, so that a copy waits for no
@@ -341,7 +229,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   int queued = 0;  // units of the queue that are copied
   auto look_up = [&]() {
     const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
-    const long long u1 = s_run[1], u = s_prod[pair].u + NP * lane;
+    const long long u1 = s_run.u1, u = s_prod[pair].u + NP * lane;
     Walk w = s_prod[pair].w;
     long long off[NB];
 #pragma unroll
@@ -403,8 +291,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     for (int i = 0; i < NS; ++i) issue(i);
   }
 
-  // ---- queries: each row times a power of two that brings its largest value to 2^14 .. 2^15, so
-  // that a value down to 2^-28 of that one is exact in float16; undone in the scores
+  // ---- queries
   uint4 raw[QPER];
   auto load_q = [&](const Walk& w) {
     const int rows = min(R, w.n * P.group - w.rt * R);
@@ -426,26 +313,18 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     for (int n = 0; n < QPER; ++n) {
       const int i = tid + n * S::kThreads, r = i / QV, j = i % QV;
       if (i >= R * QV) break;  // whole warps
-      const uint32_t x[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-      unsigned most = 0;  // largest finite magnitude's bits
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const unsigned v = (x[k >> 1] >> (16 * (k & 1))) & 0x7FFFu;
-        if (v < 0x7F80u) most = max(most, v);
-      }
+      unsigned most = largest_finite(raw[n]);
 #pragma unroll
       for (int d = QV / 2; d > 0; d >>= 1)
         most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d, QV));
-      const int k = min(14 - (static_cast<int>(most >> 7) - 127), 100);
-      const float up = __int_as_float((k + 127) << 23);
+      float undo;
+      const float up = query_scale(most, P.c, &undo);
       if (j == 0) {
         svis[r] = w.len - w.n + (w.rt * R + min(r, rows - 1)) / P.group + 1;
-        sqc[r] = P.c * __int_as_float((127 - k) << 23);
+        sqc[r] = undo;
       }
       uint32_t f[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        f[m] = pack_f16(__uint_as_float(x[m] << 16) * up, __uint_as_float(x[m] & 0xFFFF0000u) * up);
+      query_f16(raw[n], up, f);
       // values 8j .. 8j + 7: thread 8j / (D/4) of the row, steps s and s + 1 of the inner dimension
       const int s = 8 * j % (D / 4) / 4;
       uint2* to = sq + ((r >> 3) * KS + s) * 32 + (r & 7) * 4 + 8 * j / (D / 4);
@@ -456,13 +335,13 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   load_q(s_walk[0]);
 
   // ---- items of the run
-  int unit = static_cast<int>(s_run[0] - s_walk[0].base) + pair;  // next unit of this pair in the item
+  int unit = static_cast<int>(s_run.u0 - s_walk[0].base) + pair;  // next unit of this pair in the item
   int stage = 0, spent = -1;  // stage of that unit; stage of the last one, to be filled again
   uint32_t phase = 0;         // per stage: parity of the next copy
   uint2* my_p = sp + pair * NB * NT * 32;
   for (int item = 0;; item ^= 1) {
     const Walk& w = s_walk[item];
-    const int end = static_cast<int>(min(static_cast<long long>(w.nu), s_run[1] - w.base));
+    const int end = static_cast<int>(min(static_cast<long long>(w.nu), s_run.u1 - w.base));
     const int len = w.len;
     const int rows = min(R, w.n * P.group - w.rt * R);  // rows of this tile
     const int tiles = (rows + 7) >> 3;
@@ -649,24 +528,12 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         }
       }
     unit -= w.nu;  // in the next item
-    const bool whole = w.base >= s_run[0] && end == w.nu;
+    const bool whole = w.base >= s_run.u0 && end == w.nu;
     // a piece's place: a CTA has at most two, one from its start and one to its end
-    const int my_slot = 2 * blockIdx.x + (w.base <= s_run[0] ? 0 : 1);
+    const int my_slot = 2 * blockIdx.x + (w.base <= s_run.u0 ? 0 : 1);
     float* my_part = P.part + static_cast<long long>(my_slot) * S::kPart;
-    auto finish = [&](int r, int d, float4 o, float M, float L) {
-      const float inv = L == 0.f ? 0.f : P.vs / L;
-      const int row = w.rt * R + r;
-      const long long at = static_cast<long long>(w.r0 + row / P.group) * P.hq + w.h * P.group +
-                           row % P.group;
-      const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-      const __nv_bfloat162 b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(P.out) + at * D + d) = make_uint2(
-          *reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
-      if (d == 0 && P.lse)
-        P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-    };
     __syncthreads();
-    const bool more = w.base + w.nu < s_run[1];
+    const bool more = w.base + w.nu < s_run.u1;
     if (more) load_q(s_walk[item ^ 1]);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -704,7 +571,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           o.w += x.w;
         }
         if (whole) {
-          finish(r, d, o, M, L);
+          finish(P, w, R, r, d, D, o, M, L);
         } else {
           *reinterpret_cast<float4*>(my_part + r * D + d) = o;
           if (d == 0) {
@@ -714,45 +581,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         }
       }
     }
-    if (!whole) {
-      // pieces of this item lie with CTAs first .. last; the last of them to arrive joins them
-      const long long U = s_run[2], ctas = s_run[3];
-      const int first = static_cast<int>(((w.base + 1) * ctas + U - 1) / U) - 1;
-      const int last = static_cast<int>(((w.base + w.nu) * ctas + U - 1) / U) - 1;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0)
-        s_last = atomicAdd(&P.arrived[first], 1u) == static_cast<unsigned>(last - first);
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const long long first_u0 = U * first / ctas;
-        const int slot0 = 2 * first + (first_u0 >= w.base ? 0 : 1);
-        auto part_of = [&](int k) {
-          return P.part + static_cast<long long>(k == first ? slot0 : 2 * k) * S::kPart;
-        };
-        for (int i = tid; i < rows * (D / 4); i += S::kThreads) {
-          const int r = i / (D / 4), d = 4 * (i % (D / 4));
-          float M = -FLT_MAX, L = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(part_of(k) + R * D + r));
-#pragma unroll 4
-          for (int k = first; k <= last; ++k) {
-            const float* part = part_of(k);
-            const float f = ex2_fast(__ldcg(part + R * D + r) - M);
-            L += __ldcg(part + R * D + R + r) * f;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part + r * D + d));
-            o.x += x.x * f;
-            o.y += x.y * f;
-            o.z += x.z * f;
-            o.w += x.w * f;
-          }
-          finish(r, d, o, M, L);
-        }
-        if (tid == 0) P.arrived[first] = 0;  // ready for the next call
-      }
-    }
+    if (!whole)
+      join_pieces<S::kThreads, R, D>(P, w, s_run, rows, tid, &s_last, [] { __syncthreads(); });
     if (!more) break;
     __syncthreads();  // the joining buffers and statistics are free
   }
@@ -792,13 +622,17 @@ cudaError_t launch_dim(const AttnParams& P, int rows, int sms, cudaStream_t stre
 
 size_t attention_workspace_bytes(int sms) {
   // two pieces a CTA, two CTAs an SM
-  return kAttnHeader + static_cast<size_t>(sms) * 4 * kMaxRows * (128 + 2) * sizeof(float);
+  return kAttnHeader + static_cast<size_t>(sms) * 4 * kTcMaxRows * (128 + 2) * sizeof(float);
 }
 
+#ifndef TCROWS
+#define TCROWS 32
+#endif
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream) {
-  // rows of a tile: a sequence's rows in as few tiles as hold them, evenly
   const long long all = std::max(1LL, static_cast<long long>(max_new) * P.group);
+  if (D == 128 && all > TCROWS) return launch_attention_tc(P, sms, stream);
+  // rows of a tile: a sequence's rows in as few tiles as hold them, evenly
   const long long tiles = (all + kMaxRows - 1) / kMaxRows;
   const int rows = static_cast<int>((all + tiles - 1) / tiles);
   return D == 128 ? launch_dim<128>(P, rows, sms, stream) : launch_dim<64>(P, rows, sms, stream);

@@ -1,0 +1,762 @@
+// Attention over the 4-bit cache for many rows a head (D = 128), on the fifth-generation tensor cores.
+//
+// With 9 new tokens and 7 query heads a key/value head a cached value meets 63 rows, and the
+// products, not the bytes, bound the kernel of register operands (sv_attn.cu): a warp's matrix
+// instruction does 1024 multiplications a cycle and SM, tcgen05 four times that. Here a CTA takes
+// 128 tokens at a time:
+//   scores^T [128 tokens x N rows] = K [128 x 128, tensor memory] q^T [shared memory]
+//   outputs^T [128 values x N rows] += V^T [128 x 128 tokens, shared memory] p^T [shared memory]
+// with both results in tensor memory. K goes there as float16, a token a lane, so that it costs
+// the shared memory no bandwidth; a byte of value codes is one value of two tokens, which is what
+// a row of V^T holds side by side. A thread that has read a token's scores from its lane keeps the
+// sums of its weights; the running maximum of a row is moved when a score exceeds it by 2^8
+// (kSlack - kLift), a few times in a run, and only then are outputs read back and scaled.
+//
+// One CTA an SM, its warps specialised, two tiles in flight between any two of them: one copies
+// blocks in, one issues products, four unpack keys, four unpack values, sixteen take scores to
+// weights, each four of these a quarter of the rows. The first form, eight warps that did all of it in
+// turn behind barriers of the CTA, two CTAs an SM, took 363 us for 524301 tokens and 20 rows of 8
+// heads: its warps waited for the one that issued products. The work is cut and joined as in
+// sv_attn.cu, in units of 128 tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <cfloat>
+#include <cmath>
+#include <type_traits>
+#include <utility>
+
+#include "spec_kv.h"
+#include "sv_attn.cuh"
+#include "sv_kv.h"
+#include "sv_ptx.cuh"
+#include "sv_tc.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int D = 128;
+// warps: copies, products, keys (4), values (4), weights (4 x 4); the warps that reach tensor
+// memory come in fours, since a warp reaches the lanes of its index modulo 4
+constexpr int kWarpKeys = 2, kWarpValues = 6, kWarpWeights = 10, kTcWarps = 26;
+constexpr int kTcWThreads = 32 * (kTcWarps - kWarpWeights);
+constexpr int kTcThreads = 32 * kTcWarps;
+constexpr int kTcUnit = 128;   // tokens
+constexpr int kTcStages = 4;   // tiles of the cache's bytes on their way
+constexpr int kTcBlock = KvBlock<D>::kBytes;
+constexpr int kTcStage = 8 * kTcBlock;
+constexpr int kSlabV = 128 * 128;          // 128 values x 64 tokens of float16
+constexpr int kSlabR = kTcMaxRows * 128;   // rows x 64 values or tokens
+constexpr int kTcV = 2 * kSlabV, kTcQ = 2 * kSlabR, kTcP = 2 * kSlabR;  // each twice
+constexpr int kTcSmem = 1024 + 2 * (kTcV + kTcQ + kTcP) + kTcStages * kTcStage;
+// tensor memory columns: keys and scores twice, outputs
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 256, kTcCols = 512;
+constexpr int kTcPart = kTcMaxRows * (D + 2);
+static_assert(kTcSmem + 8 * 1024 <= 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The low word of a shared-memory operand's descriptor (smem_desc_sw128); its high word is the
+// same for every operand here. One thread issues all products, so what it computes for each counts.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, one step of 16, float16 operands; issued by one thread.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+// The same with A in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
+
+// Stores at a register's address plus a constant.
+template <int off>
+__device__ __forceinline__ void st_shared_f16(uint32_t at, float x) {
+  asm volatile("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %2;\n\tst.shared.b16 [%0+%1], h;\n\t}" ::"r"(at),
+               "n"(off), "f"(x));
+}
+template <int off>
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0+%1], {%2, %3, %4, %5};" ::"r"(at), "n"(off), "r"(a), "r"(b), "r"(c),
+               "r"(d));
+}
+// One try of a wait: the hardware holds the thread for some microseconds if the phase is not done.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
+// f(0), ..., f(N - 1) with constants as arguments
+template <int... I, class F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N>
+using Upto = std::make_integer_sequence<int, N>;
+
+constexpr int kWaitTries = 1 << 19;  // a second or more
+
+// 32 columns of this warp's lanes from r, complete (for this thread) after tmem_wait_st.
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Columns t and t + 32 and the seven after each: the row groups of this warp.
+__device__ __forceinline__ void tmem_ld_groups(uint32_t t, float (&v)[2][8]) {
+  uint32_t r[16];
+  asm volatile(
+      "{\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(t), "r"(t + 32)
+      : "memory");
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] = __uint_as_float(r[8 * k + j]);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Sums of 16 values over the warp's lanes: lane i < 16 gets the sum of value i.
+__device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1) {
+    const bool up = lane & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n];
+      v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, n);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
+}
+
+// What the roles share. Tile t uses buffer t & 1 of everything that is held twice.
+struct TcShared {
+  uint64_t raw_full[kTcStages], raw_empty[kTcStages];  // the cache's bytes
+  uint64_t k_full[2];             // keys unpacked
+  uint64_t s_full[2];             // scores there: the keys are spent, and so is all that products
+                                  // issued before them read
+  uint64_t vp_full[2];            // values unpacked and weights there (and the scores read)
+  uint64_t pv_done[2];            // values and weights spent, outputs up to date
+  uint64_t q_full[2], q_empty[2];  // queries of an item, twice as well
+  uint64_t end;
+  uint32_t tmem;
+  uint32_t lost[16];              // per tile modulo 16: blocks that are not there
+  Run run;
+  Walk first;
+  long long scan[kTcWarps];
+  alignas(16) float qc[2][kTcMaxRows];  // per row: score of a product of the operands
+  int vis[2][kTcMaxRows];         // tokens that it sees
+  alignas(16) float m[kTcMaxRows];  // running maxima
+  float down[kTcMaxRows];
+  float part[4][kTcMaxRows];      // per quarter of a tile's tokens: maxima, sums
+  uint32_t nan[4][8][4];          // per tile modulo 4 and 16 values: tokens with a NaN scale
+  int nans[4];                    // the tile that this speaks of, plus one
+  int last;
+};
+
+static_assert(offsetof(TcShared, qc) % 16 == 0 && offsetof(TcShared, m) % 16 == 0, "read as float4");
+
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
+  constexpr int R = kTcMaxRows;
+  extern __shared__ unsigned char dsm[];
+  __shared__ __align__(16) TcShared S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* base = dsm + ((1024u - (smem_u32(dsm) & 1023u)) & 1023u);
+  unsigned char* sval = base;
+  unsigned char* sq = sval + 2 * kTcV;
+  unsigned char* sp = sq + 2 * kTcQ;
+  unsigned char* ring = sp + 2 * kTcP;
+
+  if (tid == 0) {
+    for (int i = 0; i < kTcStages; ++i) {
+      mbar_init(&S.raw_full[i], 1);
+      mbar_init(&S.raw_empty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.vp_full[i], 20);
+      mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.q_full[i], 4);
+      mbar_init(&S.q_empty[i], 16);
+    }
+    mbar_init(&S.end, 1);
+    fence_mbar_init();
+    for (int i = 0; i < 4; ++i) S.nans[i] = 0;
+  }
+  if (!find_run<kTcThreads, R, kTcUnit>(P, 1, S.scan, &S.run, &S.first)) return;
+  if (warp == 1) tmem_alloc(&S.tmem, kTcCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  const long long u0 = S.run.u0, u1 = S.run.u1;
+  const int tiles = static_cast<int>(u1 - u0);
+  Walk w = S.first;
+  int unit = static_cast<int>(u0 - w.base);
+  // Every wait has a limit. A role that met it waits no more and runs through to its end, so that
+  // nobody waits for it for good; what comes out is not used.
+  int tries = kWaitTries;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar), p = parity & 1u;
+    int left = tries;
+    while (!mbar_try(at, p))
+      if (--left <= 0) {
+        tries = 0;
+        break;
+      }
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    wait(bar, parity);
+    __syncwarp();
+  };
+  auto arrive_warp = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto item_end = [&]() { return static_cast<int>(min(static_cast<long long>(w.nu), u1 - w.base)); };
+
+  if (warp == 0) {
+    // ---- copies: a lane a block
+    const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
+    int issued = 0;
+    for (int t = 0; t < tiles; ++t, ++unit) {
+      if (unit >= w.nu) {
+        next_item<R, kTcUnit>(P, w);
+        unit = 0;
+      }
+      const int blk = 8 * unit + lane;
+      int page = -1;
+      if (lane < 8 && 16 * blk < w.len)
+        page = P.table[static_cast<long long>(w.b) * P.max_blocks + (blk >> bpp_log)];
+      const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(P.num_pages);
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+      const int stage = t % kTcStages;
+      if (t >= kTcStages) wait_warp(&S.raw_empty[stage], t / kTcStages - 1);
+      if (!__all_sync(0xFFFFFFFFu, tries > 0)) break;
+      if (lane == 0) {
+        S.lost[t & 15] = ~mask & 0xFFu;
+        if (mask)
+          mbar_arrive_expect_tx(&S.raw_full[stage], __popc(mask) * kTcBlock);
+        else
+          mbar_arrive(&S.raw_full[stage]);
+      }
+      __syncwarp();
+      const bool whole = bpp_log == 3 && mask == 0xFFu;  // one page: neighbours
+      if (there && (!whole || lane == 0))
+        bulk_g2s(ring + stage * kTcStage + lane * kTcBlock,
+                 P.cache + (((static_cast<long long>(page) * P.hkv + w.h) << bpp_log) +
+                            (blk & ((1 << bpp_log) - 1))) * kTcBlock,
+                 whole ? kTcStage : kTcBlock, &S.raw_full[stage]);
+      ++issued;
+    }
+    // no copy is in flight when the CTA ends, whoever gave up
+    for (int i = max(0, issued - kTcStages); i < issued; ++i)
+      if (!mbar_wait_bounded(&S.raw_full[i % kTcStages], (i / kTcStages) & 1, kWaitCycles)) tries = 0;
+  } else if (warp == 1) {
+    // ---- products, issued by an elected thread (a thread that the compiler knows to be one: picked
+    // by its number it costs 96 to 111 cycles a product whatever its size, elected 39 with 32 rows)
+    int t = 0;
+    uint32_t idesc = 0, pv_idesc = 0;
+    bool pv_first = false;
+    const uint32_t a_val = desc_lo(smem_u32(sval)), a_q = desc_lo(smem_u32(sq)), a_p = desc_lo(smem_u32(sp));
+    auto outputs = [&](int i) {  // of tile i
+      const int b = i & 1;
+      wait_warp(&S.vp_full[b], i >> 1);
+      tc_fence_after();
+      const uint32_t a = a_val + b * (kTcV >> 4), p = a_p + b * (kTcP >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ss(tmem + kColO, a + (((kk >> 2) * kSlabV + 32 * (kk & 3)) >> 4),
+                    p + (((kk >> 2) * kSlabR + 32 * (kk & 3)) >> 4), pv_idesc, !pv_first || kk > 0);
+        tc_commit(&S.pv_done[b]);
+      }
+      __syncwarp();
+    };
+    for (int item = 0; t < tiles; ++item) {
+      const int end = item_end();
+      const int rows = min(R, w.n * P.group - w.rt * R);
+      // float16 operands, float32 sums, 128 x (rows to a multiple of 16)
+      idesc = (1u << 4) | (static_cast<uint32_t>((rows + 15) / 16 * 2) << 17) |
+              (static_cast<uint32_t>(128 >> 4) << 24);
+      const uint32_t q = a_q + (item & 1) * (kTcQ >> 4);
+      wait_warp(&S.q_full[item & 1], item >> 1);
+      for (bool first = true; unit < end; ++unit, ++t, first = false) {
+        const int b = t & 1;
+        // the scores of tile t - 2 have been read: its weights were there
+        wait_warp(&S.k_full[b], t >> 1);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_ts(tmem + kColS + 64 * b, tmem + kColK + 64 * b + 8 * kk,
+                      q + (((kk >> 2) * kSlabR + 32 * (kk & 3)) >> 4), idesc, kk > 0);
+          tc_commit(&S.s_full[b]);
+        }
+        __syncwarp();
+        if (t > 0) outputs(t - 1);
+        pv_idesc = idesc;
+        pv_first = first;
+      }
+      if (t < tiles) next_item<R, kTcUnit>(P, w);
+      unit = 0;
+    }
+    outputs(tiles - 1);
+    // all products are done before the memory goes
+    if (elect_one()) tc_commit(&S.end);
+    __syncwarp();
+    if (!mbar_wait_bounded(&S.end, 0, kWaitCycles)) tries = 0;
+  } else if (warp < kWarpValues) {
+    // ---- keys: a thread a token
+    constexpr int QV = D / 8, QPER = R * QV / 128;
+    const int q = warp & 3, tok = 32 * q + lane, kid = tid - 32 * kWarpKeys;
+    const uint32_t to = tmem + (static_cast<uint32_t>(q) << 21) + kColK;
+    int t = 0;
+    for (int item = 0; t < tiles; ++item) {
+      const int end = item_end(), rows = min(R, w.n * P.group - w.rt * R), qb = item & 1;
+      // queries in rows of 64 values (128 bytes), in the 128-byte swizzle
+      uint4 raw[QPER];
+#pragma unroll
+      for (int n = 0; n < QPER; ++n) {
+        const int r = 8 * n + kid / QV;
+        raw[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const int row = w.rt * R + r, i = row / P.group, head = w.h * P.group + row % P.group;
+          raw[n] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.q) +
+                                                        (w.r0 + i) * P.qs +
+                                                        static_cast<long long>(head) * D) + kid % QV);
+        }
+      }
+      if (item >= 2) wait_warp(&S.q_empty[qb], (item >> 1) - 1);
+#pragma unroll
+      for (int n = 0; n < QPER; ++n) {
+        if (8 * n >= rows) break;
+        const int r = 8 * n + kid / QV, j = kid % QV;
+        unsigned most = largest_finite(raw[n]);
+#pragma unroll
+        for (int d = QV / 2; d > 0; d >>= 1)
+          most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d, QV));
+        float undo;
+        const float up = query_scale(most, P.c, &undo);
+        if (j == 0) {
+          S.vis[qb][r] = w.len - w.n + (w.rt * R + min(r, rows - 1)) / P.group + 1;
+          S.qc[qb][r] = undo;
+        }
+        uint32_t f[4];
+        query_f16(raw[n], up, f);
+        *reinterpret_cast<uint4*>(sq + qb * kTcQ + (j >> 3) * kSlabR + r * 128 +
+                                  (((j & 7) ^ (r & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      fence_proxy_async();
+      arrive_warp(&S.q_full[qb]);
+      for (; unit < end; ++unit, ++t) {
+        const int stage = t % kTcStages, b = t & 1;
+        wait_warp(&S.raw_full[stage], t / kTcStages);
+        const unsigned char* blk = ring + stage * kTcStage + (tok >> 4) * kTcBlock;
+        // four vectors a token; neighbours start at different ones, which keeps the banks apart
+        const int turn = (lane >> 1) & 3;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = *reinterpret_cast<const uint4*>(blk + (tok & 15) * 64 + 16 * (i ^ turn));
+        const uint2 sc = *reinterpret_cast<const uint2*>(blk + KvBlock<D>::kKeyScales + (tok & 15) * 8);
+        arrive_warp(&S.raw_empty[stage]);
+        auto swap = [&](uint4& a, uint4& c, bool s) {
+          const uint4 y = a;
+          a = make_uint4(s ? c.x : a.x, s ? c.y : a.y, s ? c.z : a.z, s ? c.w : a.w);
+          c = make_uint4(s ? y.x : c.x, s ? y.y : c.y, s ? y.z : c.z, s ? y.w : c.w);
+        };
+        swap(x[0], x[1], turn & 1);
+        swap(x[2], x[3], turn & 1);
+        swap(x[0], x[2], turn & 2);
+        swap(x[1], x[3], turn & 2);
+        if (t >= 2) wait_warp(&S.s_full[b], (t >> 1) - 1);  // this buffer's products are done
+        tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t s4 = half ? sc.y : sc.x;
+          const uint32_t s01 = e4m3x2(s4), s23 = e4m3x2(s4 >> 16);
+          const uint32_t f[4] = {__byte_perm(s01, s01, 0x1010), __byte_perm(s01, s01, 0x3232),
+                                 __byte_perm(s23, s23, 0x1010), __byte_perm(s23, s23, 0x3232)};
+          const uint4 lo = x[2 * half], hi = x[2 * half + 1];
+          const uint32_t code[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          uint32_t k16[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t y[4];
+            e2m1x8(code[i], y);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) k16[4 * i + n] = mul_f16x2(y[n], f[i >> 1]);
+          }
+          tmem_st32(to + 64 * b + 32 * half, k16);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&S.k_full[b]);
+      }
+      if (t < tiles) next_item<R, kTcUnit>(P, w);
+      unit = 0;
+    }
+  } else if (warp < kWarpWeights) {
+    // ---- values: a thread 16 values (a scale's) of 8 tokens. Codes: 8 threads side by side read a
+    // pair's line of 128 bytes; operands: 8 threads side by side write 8 different 16-byte places of
+    // a row of 64 tokens.
+    const int vid = tid - 32 * kWarpValues, vg = lane & 7, vv = 4 * (warp - kWarpValues) + (lane >> 3);
+    const int vt = (((lane & 7) + vv) & 7) | (vv & 8);  // group of 8 tokens
+    const int code_at = (vt >> 1) * kTcBlock + KvBlock<D>::kValCodes + (vt & 1) * 4 * D;
+    const int scale_at = (vt >> 1) * kTcBlock + KvBlock<D>::kValScales + (vt & 1) * 64 + 2 * vg;
+    const uint32_t v_to = smem_u32(sval) + (vt >> 3) * kSlabV + 16 * vg * 128 + ((vt & 7) << 4);
+    int t = 0;
+    for (int item = 0; t < tiles; ++item) {
+      const int end = item_end(), len = w.len;
+      const int all_see = w.len - w.n + w.rt * R / P.group + 1;  // tokens that every row sees
+      for (; unit < end; ++unit, ++t) {
+        const int stage = t % kTcStages, b = t & 1, t0 = unit * kTcUnit;
+        wait_warp(&S.raw_full[stage], t / kTcStages);
+        const unsigned char* src = ring + stage * kTcStage;
+        uint4 x[4];
+        uint32_t sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = *reinterpret_cast<const uint4*>(src + code_at + i * D + 16 * (vg ^ (2 * i)));
+          sc[i] = *reinterpret_cast<const uint16_t*>(src + scale_at + 16 * i);
+        }
+        const uint32_t lost = S.lost[t & 15];
+        arrive_warp(&S.raw_empty[stage]);
+        if (t0 + kTcUnit > all_see || lost) {
+          // see sv_attn.cu: what some row does not see must not reach it as 0 * NaN
+          if (vid < 32) S.nan[t & 3][vid >> 2][vid & 3] = 0;
+          named_sync(5, 128);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const int k = 8 * vt + 2 * i + n, sh = 8 * n;
+              const bool bad = ((sc[i] >> sh) & 0x7Fu) == 0x7Fu;
+              if (t0 + k >= len || ((lost >> (k >> 4)) & 1u)) {
+                sc[i] &= ~(0xFFu << sh);
+              } else if (bad && t0 + k >= all_see) {
+                sc[i] &= ~(0xFFu << sh);
+                atomicOr(&S.nan[t & 3][vg][k >> 5], 1u << (k & 31));
+                S.nans[t & 3] = t + 1;
+              }
+            }
+        }
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = e4m3x2(sc[i]);
+        if (t >= 2) wait_warp(&S.pv_done[b], (t >> 1) - 1);  // this buffer's products are done
+        const uint32_t dst = v_to + b * kTcV;
+        each(Upto<4>(), [&](auto part_) {  // 4 values
+          constexpr int part = decltype(part_)::value;
+          uint32_t v16[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+            e2m1x8(part == 0 ? x[i].x : part == 1 ? x[i].y : part == 2 ? x[i].z : x[i].w, y);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v16[n][i] = mul_f16x2(y[n], f[i]);
+          }
+          each(Upto<4>(), [&](auto n_) {
+            constexpr int n = decltype(n_)::value, d = 4 * part + n;
+            // (vt ^ d) % 8 is the place in the swizzled row
+            st_shared_v4<d * 128>(dst ^ ((d & 7) << 4), v16[n][0], v16[n][1], v16[n][2], v16[n][3]);
+          });
+        });
+        fence_proxy_async();
+        arrive_warp(&S.vp_full[b]);
+      }
+      if (t < tiles) next_item<R, kTcUnit>(P, w);
+      unit = 0;
+    }
+  } else {
+    // ---- weights: a thread a token, a quarter of the rows: 8 (4 k + hh) + j
+    const int wid = tid - 32 * kWarpWeights, hh = wid >> 7, hid = wid & 127;
+    const int q = warp & 3, tok = 32 * q + lane;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(q) << 21);
+    const uint32_t p_to = smem_u32(sp) + (tok >> 6) * kSlabR + 2 * (tok & 7) + (((tok & 63) >> 3) << 4) + hh * 1024;
+    const int my_row = 8 * (4 * (hid >> 3) + hh) + (hid & 7);  // hid < 16: a row of this quarter
+    const int lane_row = 8 * (4 * (lane >> 3) + hh) + (lane & 7);  // lane < 16
+    int t = 0;
+    for (int item = 0; t < tiles; ++item) {
+      const int end = item_end(), rows = min(R, w.n * P.group - w.rt * R), qb = item & 1;
+      if (hid < 16) S.m[my_row] = -FLT_MAX;
+      wait_warp(&S.q_full[qb], item >> 1);
+      named_sync(1 + hh, 128);
+      const int all_see = S.vis[qb][0];
+      const float4* qc4 = reinterpret_cast<const float4*>(S.qc[qb] + 8 * hh);  // groups of 8 rows, 32 apart
+      const float4* m4 = reinterpret_cast<const float4*>(S.m + 8 * hh);
+      float l[2][8];  // sums of this token's weights
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l[k][j] = 0.f;
+      for (bool first = true; unit < end; ++unit, ++t, first = false) {
+        const int b = t & 1, t0 = unit * kTcUnit;
+        wait_warp(&S.s_full[b], t >> 1);
+        tc_fence_after();
+        float z[2][8];
+        tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
+        const uint32_t lost = S.lost[t & 15];
+        const bool masked = t0 + kTcUnit > all_see || lost;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r0 = 8 * (4 * k + hh);
+          if (r0 >= rows) break;
+          const float4 a = qc4[8 * k], c = qc4[8 * k + 1];
+          // rounded before the maximum is taken
+          z[k][0] = __fmul_rn(z[k][0], a.x);
+          z[k][1] = __fmul_rn(z[k][1], a.y);
+          z[k][2] = __fmul_rn(z[k][2], a.z);
+          z[k][3] = __fmul_rn(z[k][3], a.w);
+          z[k][4] = __fmul_rn(z[k][4], c.x);
+          z[k][5] = __fmul_rn(z[k][5], c.y);
+          z[k][6] = __fmul_rn(z[k][6], c.z);
+          z[k][7] = __fmul_rn(z[k][7], c.w);
+        }
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int r = 8 * (4 * k + hh) + j;
+              if (r < rows && t0 + tok >= S.vis[qb][r])
+                z[k][j] = -INFINITY;
+              else if ((lost >> (tok >> 4)) & 1u)
+                z[k][j] = NAN;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r0 = 8 * (4 * k + hh);
+          if (r0 >= rows) break;
+          const float4 a = m4[8 * k], c = m4[8 * k + 1];
+          top = fmaxf(top, fmaxf(fmaxf(fmaxf(z[k][0] - a.x, z[k][1] - a.y), fmaxf(z[k][2] - a.z, z[k][3] - a.w)),
+                                 fmaxf(fmaxf(z[k][4] - c.x, z[k][5] - c.y), fmaxf(z[k][6] - c.z, z[k][7] - c.w))));
+        }
+        if (named_sync_or(1 + hh, 128, top > kSlack)) {  // a new maximum of some row
+          float y = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (8 * (4 * k + hh) < rows) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float x = warp_max(z[k][j]);
+                if (lane == 8 * k + j) y = x;
+              }
+            }
+          if (lane < 16) S.part[q][lane_row] = y;
+          named_sync(1 + hh, 128);
+          if (hid < 16) {
+            const float old = S.m[my_row];
+            y = fmaxf(fmaxf(S.part[0][my_row], S.part[1][my_row]),
+                      fmaxf(S.part[2][my_row], S.part[3][my_row]));
+            const float now = fmaxf(old, y - kLift);
+            S.down[my_row] = ex2_fast(old - now);
+            S.m[my_row] = now;
+          }
+          named_sync(1 + hh, 128);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) l[k][j] *= S.down[8 * (4 * k + hh) + j];
+          if (!first) {
+            wait_warp(&S.pv_done[(t - 1) & 1], (t - 1) >> 1);
+            tc_fence_after();
+            float o[2][8];
+            tmem_ld_groups(mine + kColO + 8 * hh, o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r0 = 8 * (4 * k + hh);
+              if (r0 >= rows) break;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[k][j] *= S.down[r0 + j];
+              tmem_st8(mine + kColO + r0, o[k]);
+            }
+            tmem_wait_st();
+          }
+        }
+        // the products that read this buffer last were issued before these scores'
+        const uint32_t dst = p_to + b * kTcP;
+        each(Upto<2>(), [&](auto k_) {
+          constexpr int k = decltype(k_)::value;
+          const int r0 = 8 * (4 * k + hh);
+          if (r0 >= rows) return;
+          const float4 a = m4[8 * k], c = m4[8 * k + 1];
+          each(Upto<8>(), [&](auto j_) {
+            constexpr int j = decltype(j_)::value;
+            const float m = j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w
+                          : j == 4 ? c.x : j == 5 ? c.y : j == 6 ? c.z : c.w;
+            const float p = ex2_fast(z[k][j] - m);
+            l[k][j] += p;
+            st_shared_f16<(32 * k + j) * 128>(dst ^ (j << 4), p);
+          });
+        });
+        fence_proxy_async();
+        tc_fence_before();
+        arrive_warp(&S.vp_full[b]);
+        if (masked) {
+          wait_warp(&S.pv_done[b], t >> 1);
+          if (S.nans[t & 3] == t + 1) {  // rows that see a NaN value: NaN in its 16 values
+            tc_fence_after();
+            float o[2][8];
+            tmem_ld_groups(mine + kColO + 8 * hh, o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int r0 = 8 * (4 * k + hh);
+              if (r0 >= rows) break;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int seen = S.vis[qb][r0 + j] - t0;
+                bool hit = false;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                  const int here = seen - 32 * n;
+                  const uint32_t sees = here >= 32 ? 0xFFFFFFFFu : here > 0 ? (1u << here) - 1u : 0u;
+                  hit |= (S.nan[t & 3][tok >> 4][n] & sees) != 0;
+                }
+                if (hit) o[k][j] = NAN;
+              }
+              tmem_st8(mine + kColO + r0, o[k]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+        }
+      }
+
+      // the item's results, or this piece of them
+      wait_warp(&S.pv_done[(t - 1) & 1], (t - 1) >> 1);
+      tc_fence_after();
+      float o[2][8];
+      tmem_ld_groups(mine + kColO + 8 * hh, o);
+      tc_fence_before();
+      arrive_warp(&S.q_empty[qb]);
+      {
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * k + j] = l[k][j];
+        const float sum = warp_sums(v, lane);
+        if (lane < 16) S.part[q][lane_row] = sum;
+      }
+      named_sync(1 + hh, 128);
+      const bool whole = w.base >= u0 && end == w.nu;
+      float* part = P.part + static_cast<long long>(2 * blockIdx.x + (w.base <= u0 ? 0 : 1)) * kTcPart;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 8 * (4 * k + hh) + j;
+          if (r >= rows) break;
+          const float L = S.part[0][r] + S.part[1][r] + S.part[2][r] + S.part[3][r];
+          if (whole) {
+            const long long at = out_row(P, w, R, r);
+            static_cast<__nv_bfloat16*>(P.out)[at * D + tok] =
+                __float2bfloat16_rn(o[k][j] * (L == 0.f ? 0.f : P.vs / L));
+            if (tok == 0) store_lse(P, at, S.m[r], L);
+          } else {
+            part[r * D + tok] = o[k][j];
+            if (tok == 0) {
+              part[R * D + r] = S.m[r];
+              part[R * D + R + r] = L;
+            }
+          }
+        }
+      }
+      if (!whole)
+        join_pieces<kTcWThreads, R, D>(P, w, S.run, rows, wid, &S.last, [] { named_sync(6, kTcWThreads); });
+      named_sync(1 + hh, 128);  // maxima and sums may change
+      if (t < tiles) next_item<R, kTcUnit>(P, w);
+      unit = 0;
+    }
+  }
+  if (tries <= 0) atomicOr(P.err, 1u);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTcCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(const AttnParams& P, int sms, cudaStream_t stream) {
+  static bool ready[64] = {};  // per device: the attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  attn_tc_kernel<<<sms, kTcThreads, kTcSmem, stream>>>(P);
+  return cudaGetLastError();
+}
+
+}  // namespace sv

@@ -50,6 +50,9 @@ struct AttnParams {
 constexpr size_t kAttnHeader = 4096;  // bytes before the pieces: error word at 0, arrivals from 256
 constexpr int kAttnMaxCtas = (4096 - 256) / 4;
 
+constexpr int kTcMaxRows = 64;  // rows of a tile of the tcgen05 kernel (sv_attn_tc.cu), D = 128
+cudaError_t launch_attention_tc(const AttnParams& P, int sms, cudaStream_t stream);
+
 // Bytes of the attention workspace on a device with `sms` multiprocessors; zeroed once.
 size_t attention_workspace_bytes(int sms);
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,

@@ -369,21 +369,27 @@ def test_attention_new_tokens(n, hq, hk, D):
         _check_attention([n, n + 40], [n, n], hq, hk, D, 32, max_new=max_new)
 
 
-def test_attention_empty():
+HINTS = pytest.mark.parametrize("hint", [None, 64])  # 64: the kernel for many rows
+
+
+@HINTS
+def test_attention_empty(hint):
     """No tokens cached, no tokens brought, fewer cached than brought: rows that see nothing."""
-    o, ref = _check_attention([0, 5, 0, 3, 20], [2, 0, 0, 7, 1], 4, 2, 128, 16)
+    o, ref = _check_attention([0, 5, 0, 3, 20], [2, 0, 0, 7, 1], 4, 2, 128, 16, max_new=hint)
     assert (host(o["out"])[:2] == 0).all() and np.isneginf(host(o["lse"])[:6]).all()
-    _check_attention([-4, 9], [1, 1], 2, 1, 64, 16)
+    _check_attention([-4, 9], [1, 1], 2, 1, 64, 16, max_new=hint)
 
 
-def test_attention_sharp_and_flat():
-    _check_attention([200, 90], [3, 2], 8, 2, 128, 16, sharp=30.0)
-    _check_attention([200, 90], [3, 2], 8, 2, 128, 16, sharp=0.0)
+@HINTS
+def test_attention_sharp_and_flat(hint):
+    _check_attention([200, 300], [3, 2], 8, 2, 128, 16, sharp=30.0, max_new=hint)
+    _check_attention([200, 90], [3, 2], 8, 2, 128, 16, sharp=0.0, max_new=hint)
     _check_attention([60], [2], 2, 1, 64, 16, sharp=1e-20)
     _check_attention([60], [2], 2, 1, 64, 16, gk=3e-3, gv=200.0, strided=True)
 
 
-def test_attention_ignores_what_rows_do_not_see():
+@HINTS
+def test_attention_ignores_what_rows_do_not_see(hint):
     """NaN scales past the length, and in the keys and values of later drafts."""
     D, ps = 128, 16
 
@@ -395,7 +401,7 @@ def test_attention_ignores_what_rows_do_not_see():
         last[:, 8 * D + 9 * 8] = 0x7F       # a key of token 41
         last[:, 8 * D + 15 * 8:9 * D] = 0x7F  # the key of token 47
         c[table[1, 0], :, 0, 17 * D:] = 0xFF  # every value of the second sequence
-    o, ref = _check_attention([42, 16], [4, 1], 4, 2, D, ps, edit=edit)
+    o, ref = _check_attention([42, 16], [4, 1], 4, 2, D, ps, edit=edit, max_new=hint)
     x = host(o["out"])
     assert np.isfinite(x[0:2]).all()                       # sees up to 39
     assert np.isnan(x[2, :, :16]).all() and np.isfinite(x[2, :, 16:]).all()  # sees 40's NaN values
@@ -403,28 +409,41 @@ def test_attention_ignores_what_rows_do_not_see():
     assert np.isfinite(host(o["lse"])[2]).all()
 
 
-def test_attention_infinite_queries():
+@HINTS
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_infinite_queries(D, hint):
     def edit(cache, table, q):
         q[0, 0, 5] = math.inf
         q[1, 1, 6] = math.nan
         q[2, 2] = 1e36  # scores of up to 8e37: float32 holds them
         q[2, 3] = 1e-38
-    o, _ = _check_attention([40], [3], 4, 1, 64, 16, edit=edit)
+    o, _ = _check_attention([40], [3], 4, 1, D, 16, edit=edit, max_new=hint)
     assert host(o["out"])[2, 3].any()
 
 
-def test_attention_pages_outside_the_cache():
+@HINTS
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_pages_outside_the_cache(D, hint):
     """A page number outside the cache is not read; the rows that see its tokens are NaN."""
     def edit(cache, table, q):
         table[0, 1] = -3
         table[1, 2] = 1 << 30
-    o, _ = _check_attention([40, 33, 50], [2, 2, 2], 2, 1, 64, 16, edit=edit)
+    o, _ = _check_attention([40, 33, 50], [2, 2, 2], 2, 1, D, 16, edit=edit, max_new=hint)
     x = host(o["out"])
     assert np.isnan(x[:2]).all() and np.isfinite(x[2]).all() and np.isnan(x[3]).all()
 
 
-def test_attention_lengths_past_the_table():
-    _check_attention([500, 20], [1, 3], 2, 1, 64, 16, most=4)
+@HINTS
+def test_attention_lengths_past_the_table(hint):
+    _check_attention([500, 20], [1, 3], 2, 1, 128, 16, most=4, max_new=hint)
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+@pytest.mark.parametrize("hq,hk", [(2, 2), (6, 1), (16, 2), (14, 1)])
+def test_attention_tiles(ps, hq, hk):
+    """The kernel for many rows, with few and many of them, lengths around its tiles of 128."""
+    _check_attention([127, 128, 129, 255, 260, 1, 16], [1, 2, 3, 9, 5, 1, 4], hq, hk, 128, ps,
+                     max_new=64)
 
 
 def wide_cache(B, L, H, D, ps, seed):
@@ -445,7 +464,8 @@ def wide_cache(B, L, H, D, ps, seed):
 
 @pytest.mark.parametrize("B,L,n,hq,hk,D,ps", [
     (1, 50000, 1, 8, 1, 128, 64), (1, 50001, 5, 32, 8, 128, 128), (3, 4097, 9, 28, 4, 128, 16),
-    (40, 700, 2, 8, 2, 64, 32), (300, 40, 1, 4, 2, 64, 16), (2, 3000, 70, 8, 1, 64, 16)])
+    (40, 700, 2, 8, 2, 64, 32), (300, 40, 1, 4, 2, 64, 16), (2, 3000, 70, 8, 1, 64, 16),
+    (1, 30000, 9, 8, 1, 128, 64), (70, 500, 9, 14, 2, 128, 16), (2, 2900, 70, 8, 1, 128, 32)])
 def test_attention_long_and_many(B, L, n, hq, hk, D, ps):
     """Long sequences and large batches, against float64 on the values that the append reports:
     work split over the tokens of a sequence and joined, and many sequences to a CTA."""
