@@ -24,17 +24,29 @@ struct Walk {
   long long base;  // the item's first unit
   int b, h, rt;
   int rts, nu, len, n, r0;
+  int past;        // cu_new[b + 1]
+  int len1, past1;  // lengths of sequence b + 1: loaded with sequence b, used after it
 };
 
 template <int R, int UNIT>
-__device__ __forceinline__ void load_seq(const AttnParams& P, int b, Walk& w) {
-  const int c0 = min(max(P.cu[b], 0), P.T), c1 = min(max(P.cu[b + 1], c0), P.T);
+__device__ __forceinline__ void set_seq(const AttnParams& P, int b, int first, int past, int len,
+                                        Walk& w) {
+  const int c0 = min(max(first, 0), P.T), c1 = min(max(past, c0), P.T);
   w.b = b;
   w.r0 = c0;
   w.n = c1 - c0;
-  w.len = min(max(P.lens[b], 0), P.max_blocks * P.ps);
+  w.past = past;
+  w.len = min(max(len, 0), P.max_blocks * P.ps);
   w.rts = (w.n * P.group + R - 1) / R;
   w.nu = max(1, (w.len + UNIT - 1) / UNIT);
+}
+template <int R, int UNIT>
+__device__ __forceinline__ void load_seq(const AttnParams& P, int b, Walk& w) {
+  set_seq<R, UNIT>(P, b, P.cu[b], P.cu[b + 1], P.lens[b], w);
+}
+__device__ __forceinline__ void load_ahead(const AttnParams& P, Walk& w) {
+  w.len1 = P.lens[min(w.b + 1, P.B - 1)];
+  w.past1 = P.cu[min(w.b + 2, P.B)];
 }
 __device__ __forceinline__ long long seq_units(const AttnParams& P, const Walk& w) {
   return static_cast<long long>(w.rts) * P.hkv * w.nu;
@@ -46,14 +58,15 @@ __device__ __forceinline__ void next_item(const AttnParams& P, Walk& w) {
   w.rt = 0;
   if (++w.h < P.hkv) return;
   w.h = 0;
-  int b = w.b;
   do {
-    if (++b >= P.B) {
+    const int b = w.b + 1;
+    if (b >= P.B) {
       w.b = P.B;
       w.nu = 1 << 30;  // nothing follows
       return;
     }
-    load_seq<R, UNIT>(P, b, w);
+    set_seq<R, UNIT>(P, b, w.past, w.past1, w.len1, w);
+    load_ahead(P, w);
   } while (w.n == 0);
 }
 
@@ -149,6 +162,7 @@ __device__ __forceinline__ bool find_run(const AttnParams& P, int least, long lo
         w.h = static_cast<int>(item / w.rts);
         w.rt = static_cast<int>(item - static_cast<long long>(w.h) * w.rts);
         w.base = before + item * w.nu;
+        load_ahead(P, w);
         *first = w;
         run->u0 = u0;
         run->u1 = U * (blockIdx.x + 1) / ctas;

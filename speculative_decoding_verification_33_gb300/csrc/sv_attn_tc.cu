@@ -208,6 +208,7 @@ struct TcShared {
   alignas(16) float m[kTcMaxRows];  // running maxima
   float down[kTcMaxRows];
   float part[4][kTcMaxRows];      // per quarter of a tile's tokens: maxima, sums
+  long long at[kTcMaxRows];       // where a row's results go
   uint32_t nan[4][8][4];          // per tile modulo 4 and 16 values: tokens with a NaN scale
   int nans[4];                    // the tile that this speaks of, plus one
   int last;
@@ -276,38 +277,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   auto item_end = [&]() { return static_cast<int>(min(static_cast<long long>(w.nu), u1 - w.base)); };
 
   if (warp == 0) {
-    // ---- copies: a lane a block
+    // ---- copies. Where the blocks lie is looked up four tiles at a time, a lane a block, and a
+    // round before it is needed, so that no copy waits for a page number.
     const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
-    int issued = 0;
-    for (int t = 0; t < tiles; ++t, ++unit) {
-      if (unit >= w.nu) {
+    const int mine = lane >> 3, block = lane & 7;
+    int issued = 0, next_at = 0;
+    int next_page = -1;
+    unit += mine;  // of this lane's tile
+    auto look_up = [&](int t) {
+      next_page = -1;
+      while (unit >= w.nu) {
+        unit -= w.nu;
         next_item<R, kTcUnit>(P, w);
-        unit = 0;
       }
-      const int blk = 8 * unit + lane;
-      int page = -1;
-      if (lane < 8 && 16 * blk < w.len)
-        page = P.table[static_cast<long long>(w.b) * P.max_blocks + (blk >> bpp_log)];
+      const int blk = 8 * unit + block;
+      if (t + mine < tiles && 16 * blk < w.len) {
+        next_page = P.table[static_cast<long long>(w.b) * P.max_blocks + (blk >> bpp_log)];
+        next_at = (w.h << bpp_log) + (blk & ((1 << bpp_log) - 1));
+      }
+      unit += 4;
+    };
+    look_up(0);
+    for (int t0 = 0; t0 < tiles; t0 += 4) {
+      const int page = next_page, at = next_at;
+      look_up(t0 + 4);
       const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(P.num_pages);
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
-      const int stage = t % kTcStages;
-      if (t >= kTcStages) wait_warp(&S.raw_empty[stage], t / kTcStages - 1);
-      if (!__all_sync(0xFFFFFFFFu, tries > 0)) break;
-      if (lane == 0) {
-        S.lost[t & 15] = ~mask & 0xFFu;
-        if (mask)
-          mbar_arrive_expect_tx(&S.raw_full[stage], __popc(mask) * kTcBlock);
-        else
-          mbar_arrive(&S.raw_full[stage]);
+      const uint32_t all = __ballot_sync(0xFFFFFFFFu, there);
+      for (int i = 0; i < 4 && t0 + i < tiles; ++i) {
+        const int t = t0 + i, stage = t % kTcStages;
+        const uint32_t mask = (all >> (8 * i)) & 0xFFu;
+        if (t >= kTcStages) wait_warp(&S.raw_empty[stage], t / kTcStages - 1);
+        if (!__all_sync(0xFFFFFFFFu, tries > 0)) break;
+        if (lane == 0) {
+          S.lost[t & 15] = ~mask & 0xFFu;
+          if (mask)
+            mbar_arrive_expect_tx(&S.raw_full[stage], __popc(mask) * kTcBlock);
+          else
+            mbar_arrive(&S.raw_full[stage]);
+        }
+        __syncwarp();
+        const bool whole = bpp_log == 3 && mask == 0xFFu;  // one page: neighbours
+        if (there && mine == i && (!whole || block == 0))
+          bulk_g2s(ring + stage * kTcStage + block * kTcBlock,
+                   P.cache + (((static_cast<long long>(page) * P.hkv) << bpp_log) + at) * kTcBlock,
+                   whole ? kTcStage : kTcBlock, &S.raw_full[stage]);
+        ++issued;
       }
-      __syncwarp();
-      const bool whole = bpp_log == 3 && mask == 0xFFu;  // one page: neighbours
-      if (there && (!whole || lane == 0))
-        bulk_g2s(ring + stage * kTcStage + lane * kTcBlock,
-                 P.cache + (((static_cast<long long>(page) * P.hkv + w.h) << bpp_log) +
-                            (blk & ((1 << bpp_log) - 1))) * kTcBlock,
-                 whole ? kTcStage : kTcBlock, &S.raw_full[stage]);
-      ++issued;
     }
     // no copy is in flight when the CTA ends, whoever gave up
     for (int i = max(0, issued - kTcStages); i < issued; ++i)
@@ -546,6 +561,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       const int all_see = S.vis[qb][0];
       const float4* qc4 = reinterpret_cast<const float4*>(S.qc[qb] + 8 * hh);  // groups of 8 rows, 32 apart
       const float4* m4 = reinterpret_cast<const float4*>(S.m + 8 * hh);
+      // Rows that see a NaN value get NaN in its 16 values at the item's end: of tile i (unit u of the
+      // item), a bit a row. What the values' warps left for it is there once its products are done,
+      // and stays until four tiles later.
+      auto nan_rows = [&](int i, int u) {
+        uint32_t hits = 0;
+        if (S.nans[i & 3] != i + 1) return hits;
+        for (int k = 0; k < 16; ++k) {
+          const int r = 8 * (4 * (k >> 3) + hh) + (k & 7);
+          if (r >= rows) break;
+          const int seen = S.vis[qb][r] - u * kTcUnit;
+          for (int n = 0; n < 4; ++n) {
+            const int here = seen - 32 * n;
+            const uint32_t sees = here >= 32 ? 0xFFFFFFFFu : here > 0 ? (1u << here) - 1u : 0u;
+            if (S.nan[i & 3][tok >> 4][n] & sees) hits |= 1u << k;
+          }
+        }
+        return hits;
+      };
+      uint32_t poison = 0, past = 0;  // such rows; a bit a tile of the item: masked, the last one lowest
       float l[2][8];  // sums of this token's weights
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -559,6 +593,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
         const uint32_t lost = S.lost[t & 15];
         const bool masked = t0 + kTcUnit > all_see || lost;
+        if (past & 2u) poison |= nan_rows(t - 2, unit - 2);
+        past = (past << 1) | (masked ? 1u : 0u);
         float top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -656,34 +692,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         fence_proxy_async();
         tc_fence_before();
         arrive_warp(&S.vp_full[b]);
-        if (masked) {
-          wait_warp(&S.pv_done[b], t >> 1);
-          if (S.nans[t & 3] == t + 1) {  // rows that see a NaN value: NaN in its 16 values
-            tc_fence_after();
-            float o[2][8];
-            tmem_ld_groups(mine + kColO + 8 * hh, o);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int r0 = 8 * (4 * k + hh);
-              if (r0 >= rows) break;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int seen = S.vis[qb][r0 + j] - t0;
-                bool hit = false;
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                  const int here = seen - 32 * n;
-                  const uint32_t sees = here >= 32 ? 0xFFFFFFFFu : here > 0 ? (1u << here) - 1u : 0u;
-                  hit |= (S.nan[t & 3][tok >> 4][n] & sees) != 0;
-                }
-                if (hit) o[k][j] = NAN;
-              }
-              tmem_st8(mine + kColO + r0, o[k]);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        }
       }
 
       // the item's results, or this piece of them
@@ -692,6 +700,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       float o[2][8];
       tmem_ld_groups(mine + kColO + 8 * hh, o);
       tc_fence_before();
+      if (past & 2u) poison |= nan_rows(t - 2, end - 2);
+      if (past & 1u) poison |= nan_rows(t - 1, end - 1);
+      if (poison) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((poison >> (8 * k + j)) & 1u) o[k][j] = NAN;
+      }
       arrive_warp(&S.q_empty[qb]);
       {
         float v[16];
@@ -705,25 +722,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       named_sync(1 + hh, 128);
       const bool whole = w.base >= u0 && end == w.nu;
       float* part = P.part + static_cast<long long>(2 * blockIdx.x + (w.base <= u0 ? 0 : 1)) * kTcPart;
+      if (hid < 16 && my_row < rows) {  // a thread a row: its sum, its place, its factor
+        const float L = S.part[0][my_row] + S.part[1][my_row] + S.part[2][my_row] + S.part[3][my_row];
+        if (whole) {
+          const long long at = out_row(P, w, R, my_row);
+          S.at[my_row] = at * D;
+          S.down[my_row] = L == 0.f ? 0.f : P.vs / L;
+          store_lse(P, at, S.m[my_row], L);
+        } else {
+          S.at[my_row] = my_row * D;
+          S.down[my_row] = 1.f;
+          part[R * D + my_row] = S.m[my_row];
+          part[R * D + R + my_row] = L;
+        }
+      }
+      named_sync(1 + hh, 128);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int r = 8 * (4 * k + hh) + j;
           if (r >= rows) break;
-          const float L = S.part[0][r] + S.part[1][r] + S.part[2][r] + S.part[3][r];
-          if (whole) {
-            const long long at = out_row(P, w, R, r);
-            static_cast<__nv_bfloat16*>(P.out)[at * D + tok] =
-                __float2bfloat16_rn(o[k][j] * (L == 0.f ? 0.f : P.vs / L));
-            if (tok == 0) store_lse(P, at, S.m[r], L);
-          } else {
-            part[r * D + tok] = o[k][j];
-            if (tok == 0) {
-              part[R * D + r] = S.m[r];
-              part[R * D + R + r] = L;
-            }
-          }
+          const float x = o[k][j] * S.down[r];
+          if (whole)
+            static_cast<__nv_bfloat16*>(P.out)[S.at[r] + tok] = __float2bfloat16_rn(x);
+          else
+            part[S.at[r] + tok] = x;
         }
       }
       if (!whole)

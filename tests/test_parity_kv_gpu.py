@@ -410,6 +410,24 @@ def test_attention_ignores_what_rows_do_not_see(hint):
 
 
 @HINTS
+def test_attention_nan_inside_a_prompt(hint):
+    """A prompt of several tiles of rows and tokens with a NaN value and a NaN key in its middle: rows
+    before them stay what they are."""
+    D, ps = 128, 16
+
+    def edit(cache, table, q):
+        c = cache.reshape(cache.shape[0], cache.shape[1], ps // 16, 18 * D)
+        for tok, block in ((70, 2), (300, 5)):  # a value scale each
+            c[table[0, tok // ps], :, 0, 17 * D + (tok % 16 // 2) * 16 + 2 * block + tok % 2] = 0x7F
+        c[table[0, 350 // ps], :, 0, 8 * D + (350 % 16) * 8 + 3] = 0xFF  # a key
+    o, _ = _check_attention([400], [400], 2, 1, D, ps, edit=edit, max_new=hint)
+    x = host(o["out"])
+    assert np.isfinite(x[:70]).all() and np.isnan(x[70:, :, 32:48]).all()
+    assert np.isfinite(x[70:300, :, 48:]).all() and np.isnan(x[300:, :, 80:96]).all()
+    assert np.isfinite(x[300:350, :, 96:]).all() and np.isnan(x[350:]).all()
+
+
+@HINTS
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_infinite_queries(D, hint):
     def edit(cache, table, q):
