@@ -62,7 +62,7 @@ KERNEL_SOURCES = {
                 "sv_math.cuh", "sv_ptx.cuh"),
     "tables": ("sv_tables.cu", "sv_kv.h"),
     "normrope": ("sv_normrope.cu", "sv_kv.h"),
-    "append": ("sv_kv4.cu", "sv_kv.h"),
+    "append": ("sv_kv4.cu", "sv_kv.h", "sv_ptx.cuh"),
     "attention": ("sv_attn.cu", "sv_attn.cuh", "sv_kv.h", "sv_ptx.cuh"),
     "attention_tc": ("sv_attn_tc.cu", "sv_attn.cuh", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
 }

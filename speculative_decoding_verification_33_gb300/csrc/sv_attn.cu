@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   int unit = static_cast<int>(s_run.u0 - s_walk[0].base) + pair;  // next unit of this pair in the item
   int stage = 0, spent = -1;  // stage of that unit; stage of the last one, to be filled again
   uint32_t phase = 0;         // per stage: parity of the next copy
+  int tries = kWaitTries;
   uint2* my_p = sp + pair * NB * NT * 32;
   for (int item = 0;; item ^= 1) {
     const Walk& w = s_walk[item];
@@ -371,13 +372,17 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       for (; unit < end; unit += NP) {
         const unsigned char* sb = my_ring + stage * S::kStage;
         const int t0 = unit * UNIT;
-        const bool ok = mbar_wait_bounded(&my_bar[stage], (phase >> stage) & 1u, kWaitCycles);
-        phase ^= 1u << stage;
-        uint32_t lost = my_lost[stage];
-        if (__any_sync(0xFFFFFFFFu, !ok)) {
-          if (lane == 0) atomicOr(P.err, 1u);
-          lost = (1u << NB) - 1u;
+        {
+          const uint32_t bar = smem_u32(&my_bar[stage]), parity = (phase >> stage) & 1u;
+          for (int left = tries; !mbar_try(bar, parity);)
+            if (--left <= 0) {  // a copy that never came: its rows are not used
+              tries = 0;
+              break;
+            }
+          __syncwarp();
         }
+        phase ^= 1u << stage;
+        const uint32_t lost = my_lost[stage];
         const bool masked = t0 + UNIT > all_see || lost;
 
         // scores of this warp's block and the tile's rows
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     if (!more) break;
     __syncthreads();  // the joining buffers and statistics are free
   }
+  if (tries <= 0) atomicOr(P.err, 1u);
 }
 
 template <int D, int NT>

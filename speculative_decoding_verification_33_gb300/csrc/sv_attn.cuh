@@ -94,6 +94,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
+// One try of a wait: the hardware holds the thread for some microseconds if the phase is not done.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+constexpr int kWaitTries = 1 << 19;  // a second or more
+
 // Weights and values (o: 4 dimensions from d of row r of the item's tile, sum L at maximum M, in
 // base 2) into the output and its log-sum.
 __device__ __forceinline__ long long out_row(const AttnParams& P, const Walk& w, int tile_rows,

@@ -98,18 +98,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b
   asm volatile("st.shared.v4.b32 [%0+%1], {%2, %3, %4, %5};" ::"r"(at), "n"(off), "r"(a), "r"(b), "r"(c),
                "r"(d));
 }
-// One try of a wait: the hardware holds the thread for some microseconds if the phase is not done.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile(
@@ -125,8 +113,6 @@ __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
 }
 template <int N>
 using Upto = std::make_integer_sequence<int, N>;
-
-constexpr int kWaitTries = 1 << 19;  // a second or more
 
 // 32 columns of this warp's lanes from r, complete (for this thread) after tmem_wait_st.
 __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {

@@ -16,6 +16,7 @@
 
 #include "spec_kv.h"
 #include "sv_kv.h"
+#include "sv_ptx.cuh"
 
 namespace sv {
 namespace {
@@ -23,7 +24,9 @@ namespace {
 constexpr int kApThreads = 256;
 
 struct AppendParams {
-  int T, H, ps, num_pages;
+  int T, H, num_pages;
+  int ps_log;  // page_size = 2^ps_log
+  int plain;   // tensor scales near enough to 1 for the quotient's short form
   long long ks, vs;  // token strides of k and v, in elements
   const void *k, *v;
   const int64_t* slots;
@@ -70,40 +73,57 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(b)));
   return __half2float(__ushort_as_half(static_cast<unsigned short>(r & 0xFFFFu)));
 }
-// Two values -> a byte of e2m1 codes, `lo` in the low four bits; nearest even, held at 6
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+// Eight values -> four bytes of e2m1 codes, value 2j in the low four bits of byte j; nearest even,
+// held at 6
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* x) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
-__device__ __forceinline__ float2 from_e2m1x2(uint32_t b) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(b));
-  return __half22float2(*reinterpret_cast<__half2*>(&r));
+// ... and back, as float16 pairs
+__device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
 }
 
-// 16 values -> 8 bytes of codes (value 2j low, 2j + 1 high, in byte j) and the scale's bits
-__device__ __forceinline__ uint2 quantise(const float (&x)[16], float inv6g, float g,
+// 16 values -> 8 bytes of codes (value 2j low, 2j + 1 high, in byte j) and the scale's bits. The
+// quotients x / s are those of IEEE division. Where nothing can overflow (`plain`: the tensor scale is
+// within 2^+-60, so the scale s = e4m3 * g and 1 / s are normal, and |x| <= 7 s unless the block's scale
+// is held at 448) they come from one division for the block and Markstein's correction for
+// each value: with y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y), two fused operations, is RN(x / s)
+// (P. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
+// 16 divisions made the kernel issue-bound: 65013 tokens of 8 heads took 149 us.
+__device__ __forceinline__ uint2 quantise(const float (&x)[16], float inv6g, float g, bool plain,
                                           uint32_t* scale_bits) {
-  float m = 0.f;
-  bool fine = true;
+  float m = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    m = fmaxf(m, fabsf(x[i]));
-    fine &= fabsf(x[i]) <= 3.402823466e38f;
-  }
-  const uint32_t bits = fine ? to_e4m3(fminf(m * inv6g, 448.f)) : 0x7Fu;
+  for (int i = 1; i < 16; ++i) m = max_nan(m, fabsf(x[i]));
+  const uint32_t bits = m <= 3.402823466e38f ? to_e4m3(fminf(m * inv6g, 448.f)) : 0x7Fu;
   *scale_bits = bits;
   const float s = from_e4m3(bits) * g;
   uint2 codes = make_uint2(0u, 0u);
   if (s > 0.f) {  // neither zero nor NaN
+    float t[16];
+    if (plain && bits < 0x7Eu) {
+      const float y = 1.f / s;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t c = to_e2m1x2(x[2 * j] / s, x[2 * j + 1] / s);
-      if (j < 4) codes.x |= c << (8 * j); else codes.y |= c << (8 * (j - 4));
+      for (int i = 0; i < 16; ++i) {
+        const float q = x[i] * y;
+        t[i] = fmaf(fmaf(-q, s, x[i]), y, q);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = x[i] / s;
     }
+    codes = make_uint2(to_e2m1x8(t), to_e2m1x8(t + 8));
   }
   return codes;
 }
@@ -114,10 +134,15 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* to, uint2 codes, uin
   const float s = from_e4m3(scale_bits) * g;
   uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 f = from_e2m1x2(((j < 4 ? codes.x : codes.y) >> (8 * (j & 3))) & 0xFFu);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s, f.y * s);
-    w[j] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f[4];
+    from_e2m1x8(h ? codes.y : codes.x, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * s, v.y * s);
+      w[4 * h + j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
   }
   reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -132,30 +157,27 @@ __device__ __forceinline__ uint32_t spread(uint2 codes, int k) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kApThreads) append_kernel(AppendParams P) {
   constexpr int S = D / 16;  // scales of a token
-  const long long items = static_cast<long long>(P.T) * P.H * S;
-  const long long it = static_cast<long long>(blockIdx.x) * kApThreads + threadIdx.x;
-  if (it >= 2 * items) return;
-  const bool is_v = it >= items;
-  const long long r = is_v ? it - items : it;
+  const uint32_t items = static_cast<uint32_t>(P.T) * P.H * S;
+  const uint32_t r = blockIdx.x * kApThreads + threadIdx.x;
+  if (r >= items) return;
+  const bool is_v = blockIdx.y;
   const int sb = static_cast<int>(r % S);
-  const long long th = r / S;
-  const int h = static_cast<int>(th % P.H);
-  const int t = static_cast<int>(th / P.H);
+  const uint32_t th = r / S;
+  const int t = static_cast<int>(th / static_cast<uint32_t>(P.H));
+  const int h = static_cast<int>(th - static_cast<uint32_t>(t) * P.H);
   const long long slot = P.slots[t];
-  const long long most = static_cast<long long>(P.num_pages) * P.ps;
+  const long long most = static_cast<long long>(P.num_pages) << P.ps_log;
   const bool writes = slot >= 0 && slot < most;
-  const int nb = P.ps / 16;
   auto block_of = [&](long long s) {
-    const long long page = s / P.ps;
-    const int in = static_cast<int>(s - page * P.ps);
-    return P.cache + ((page * P.H + h) * nb + (in >> 4)) * KvBlock<D>::kBytes;
+    const int in = static_cast<int>(s) & ((1 << P.ps_log) - 1);
+    return P.cache + ((((s >> P.ps_log) * P.H + h) << (P.ps_log - 4)) + (in >> 4)) * KvBlock<D>::kBytes;
   };
-  const long long out_at = (static_cast<long long>(t) * P.H + h) * D + 16 * sb;
+  const long long out_at = static_cast<long long>(th) * D + 16 * sb;
   float x[16];
   uint32_t sc;
   if (!is_v) {
     load16(static_cast<const T*>(P.k) + t * P.ks + static_cast<long long>(h) * D + 16 * sb, x);
-    const uint2 codes = quantise(x, P.ik, P.gk, &sc);
+    const uint2 codes = quantise(x, P.ik, P.gk, P.plain, &sc);
     if (writes) {
       unsigned char* blk = block_of(slot);
       const int i = static_cast<int>(slot & 15);
@@ -171,7 +193,7 @@ __global__ void __launch_bounds__(kApThreads) append_kernel(AppendParams P) {
   if (with_prev) return;  // the even token's thread does this one too
   const T* src = static_cast<const T*>(P.v) + t * P.vs + static_cast<long long>(h) * D + 16 * sb;
   load16(src, x);
-  const uint2 codes = quantise(x, P.iv, P.gv, &sc);
+  const uint2 codes = quantise(x, P.iv, P.gv, P.plain, &sc);
   if (P.ov) store_values(P.ov + out_at, codes, sc, P.gv);
   if (!writes) return;
   unsigned char* blk = block_of(slot);
@@ -182,7 +204,7 @@ __global__ void __launch_bounds__(kApThreads) append_kernel(AppendParams P) {
   if (with_next) {
     uint32_t sc2;
     load16(src + P.vs, x);
-    const uint2 odd = quantise(x, P.iv, P.gv, &sc2);
+    const uint2 odd = quantise(x, P.iv, P.gv, P.plain, &sc2);
     if (P.ov) store_values(P.ov + out_at + static_cast<long long>(P.H) * D, odd, sc2, P.gv);
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = spread(codes, k) | (spread(odd, k) << 4);
@@ -211,9 +233,9 @@ __global__ void __launch_bounds__(kApThreads) append_kernel(AppendParams P) {
 
 template <typename T, int D>
 cudaError_t launch_append(const AppendParams& P, cudaStream_t s) {
-  const long long threads = 2LL * P.T * P.H * (D / 16);
-  const long long grid = (threads + kApThreads - 1) / kApThreads;
-  append_kernel<T, D><<<static_cast<unsigned>(grid), kApThreads, 0, s>>>(P);
+  const long long threads = static_cast<long long>(P.T) * P.H * (D / 16);
+  const dim3 grid(static_cast<unsigned>((threads + kApThreads - 1) / kApThreads), 2);  // keys, values
+  append_kernel<T, D><<<grid, kApThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -249,11 +271,13 @@ extern "C" sv_status spec_kv4_append(int T, int Hkv, int D, int page_size, int n
       !sv::row_aligned(cache, 0, 1) || !sv::row_aligned(out_k, 0, 1) ||
       !sv::row_aligned(out_v, 0, 1))
     return SV_ERR_INVALID_ARG;
-  if (2LL * T * Hkv * (D / 16) > (1LL << 38)) return SV_ERR_UNSUPPORTED;  // the grid's size
+  if (static_cast<long long>(T) * Hkv * (D / 16) >= (1LL << 31)) return SV_ERR_UNSUPPORTED;  // 32-bit items
   sv::AppendParams P;
   P.T = T;
   P.H = Hkv;
-  P.ps = page_size;
+  P.ps_log = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  const float lo = 8.6736174e-19f, hi = 1.1529215e18f;  // 2^-60, 2^60
+  P.plain = k_scale >= lo && k_scale <= hi && v_scale >= lo && v_scale <= hi;
   P.num_pages = num_pages;
   P.ks = k_token_stride;
   P.vs = v_token_stride;

@@ -89,14 +89,16 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// LPH threads a head, each with two 16-byte vectors.
+// LPH threads a head, each with two 16-byte vectors. Such a group stays with one token and takes
+// its heads in turn, so that sines, cosines and weights stay in registers; the next head is loaded
+// while this one is worked on.
 template <typename T, int LPH>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P) {
-  constexpr int N = Vec<T>::n;
+  constexpr int N = Vec<T>::n, G = kNrThreads / LPH;
   extern __shared__ float2 cs[];  // [tokens][rot / 2] cosine, sine
   const int half = P.rot / 2;
-  const int group = blockIdx.x / P.splits, split = blockIdx.x - group * P.splits;
-  const int t0 = group * P.tokens, nt = min(P.tokens, P.T - t0);
+  const int block = blockIdx.x / P.splits, split = blockIdx.x - block * P.splits;
+  const int t0 = block * P.tokens, nt = min(P.tokens, P.T - t0);
   unsigned long long turn = 0;
   for (int i = threadIdx.x, last = -1; i < nt * half; i += kNrThreads) {
     const int t = i / half, j = i - t * half;
@@ -105,83 +107,106 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P)
     cs[i] = cos_sin(turn, P.pos[t0 + t]);
   }
   __syncthreads();
-  const int heads = P.hq + P.hk;
-  const int per = (heads + P.splits - 1) / P.splits;
-  const int h0 = split * per, nh = min(per, heads - h0);
-  if (nh <= 0) return;
-  const int lane = threadIdx.x % LPH;
+  const int lane = threadIdx.x % LPH, group = threadIdx.x / LPH;
+  const int per = G / P.tokens;  // groups of a token
+  const int t = group / per;
+  if (t >= nt) return;
   const unsigned mask = (LPH == 32 ? 0xFFFFFFFFu : (1u << LPH) - 1u)
                         << ((threadIdx.x & 31) & ~(LPH - 1));  // the threads of this head
   // vectors of this thread: (lane, lane + rotated half) while they last, else neighbours
   const int hv = P.inter ? 0 : half / N;
-  const int va = lane < hv ? lane : 2 * lane, vb = lane < hv ? lane + hv : 2 * lane + 1;
   const bool halves = lane < hv;
+  const int va = halves ? lane : 2 * lane, vb = halves ? lane + hv : 2 * lane + 1;
   // interleaved: whole vectors are rotated or not
   const bool pair_a = P.inter && va * N < P.rot, pair_b = P.inter && vb * N < P.rot;
-  for (int it = threadIdx.x / LPH; it < nt * nh; it += kNrThreads / LPH) {
-    const int t = it / nh, h = h0 + (it - t * nh);
-    const bool is_q = h < P.hq;
-    const int hh = is_q ? h : h - P.hq;
-    const long long row = t0 + t;
-    const T* x = static_cast<const T*>(is_q ? P.q : P.k) + row * (is_q ? P.qs : P.ks) +
-                 static_cast<long long>(hh) * P.D;
-    float a[N], b[N];
-    unpack(*(reinterpret_cast<const uint4*>(x) + va), a);
-    unpack(*(reinterpret_cast<const uint4*>(x) + vb), b);
-    float sum = 0.f;
+  float2 f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-    for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mask, sum, d, LPH);
-    const float r = 1.0f / sqrtf(sum / static_cast<float>(P.D) + P.eps);
-    const T* w = static_cast<const T*>(is_q ? P.wq : P.wk);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      a[i] *= r;
-      b[i] *= r;
-    }
-    if (w) {
+  for (int i = 0; i < N; ++i) {
+    f[i] = make_float2(1.f, 0.f);
+    if (halves) f[i] = cs[t * half + va * N + i];
+    if (pair_a && i < N / 2) f[i] = cs[t * half + va * (N / 2) + i];
+    if (pair_b && i >= N / 2) f[i] = cs[t * half + vb * (N / 2) + i - N / 2];
+  }
+  const long long row = t0 + t;
+  const float inv_d = 1.f / static_cast<float>(P.D);
+  // heads of q, then of k: this group's are split * per + group % per and every (splits * per)-th on
+  int h = split * per + group % per;
+  const int step = P.splits * per;
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = which ? P.hk : P.hq;
+    if (h < heads) {
+      const uint4* w = static_cast<const uint4*>(which ? P.wk : P.wq);
       float wa[N], wb[N];
-      unpack(__ldg(reinterpret_cast<const uint4*>(w) + va), wa);
-      unpack(__ldg(reinterpret_cast<const uint4*>(w) + vb), wb);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        a[i] *= wa[i];
-        b[i] *= wb[i];
+      for (int i = 0; i < N; ++i) wa[i] = wb[i] = 1.f;
+      if (w) {
+        unpack(__ldg(w + va), wa);
+        unpack(__ldg(w + vb), wb);
+      }
+      const T* x = static_cast<const T*>(which ? P.k : P.q) + row * (which ? P.ks : P.qs) +
+                   static_cast<long long>(h) * P.D;
+      T* y = static_cast<T*>(which ? P.ok : P.oq) + row * (which ? P.oks : P.oqs) +
+             static_cast<long long>(h) * P.D;
+      const int hop = step * P.D;
+      uint4 na = *(reinterpret_cast<const uint4*>(x) + va), nb = *(reinterpret_cast<const uint4*>(x) + vb);
+#pragma unroll 1
+      for (; h < heads; h += step) {
+        float a[N], b[N];
+        unpack(na, a);
+        unpack(nb, b);
+        x += hop;
+        if (h + step < heads) {
+          na = *(reinterpret_cast<const uint4*>(x) + va);
+          nb = *(reinterpret_cast<const uint4*>(x) + vb);
+        }
+        float sum = 0.f, sum2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          sum = fmaf(a[i], a[i], sum);
+          sum2 = fmaf(b[i], b[i], sum2);
+        }
+        sum += sum2;
+#pragma unroll
+        for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mask, sum, d, LPH);
+        const float r = rsqrtf(fmaf(sum, inv_d, P.eps));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          a[i] *= r * wa[i];
+          b[i] *= r * wb[i];
+        }
+        if (halves) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float y0 = a[i] * f[i].x - b[i] * f[i].y, y1 = b[i] * f[i].x + a[i] * f[i].y;
+            a[i] = y0;
+            b[i] = y1;
+          }
+        }
+        if (pair_a) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float2 c = f[i / 2];
+            const float y0 = a[i] * c.x - a[i + 1] * c.y, y1 = a[i + 1] * c.x + a[i] * c.y;
+            a[i] = y0;
+            a[i + 1] = y1;
+          }
+        }
+        if (pair_b) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float2 c = f[N / 2 + i / 2];
+            const float y0 = b[i] * c.x - b[i + 1] * c.y, y1 = b[i + 1] * c.x + b[i] * c.y;
+            b[i] = y0;
+            b[i + 1] = y1;
+          }
+        }
+        *(reinterpret_cast<uint4*>(y) + va) = pack(a);
+        *(reinterpret_cast<uint4*>(y) + vb) = pack(b);
+        y += hop;
       }
     }
-    const float2* c = cs + t * half;
-    if (halves) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 f = c[va * N + i];
-        const float y0 = a[i] * f.x - b[i] * f.y, y1 = b[i] * f.x + a[i] * f.y;
-        a[i] = y0;
-        b[i] = y1;
-      }
-    }
-    if (pair_a) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 f = c[(va * N + i) / 2];
-        const float y0 = a[i] * f.x - a[i + 1] * f.y, y1 = a[i + 1] * f.x + a[i] * f.y;
-        a[i] = y0;
-        a[i + 1] = y1;
-      }
-    }
-    if (pair_b) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 f = c[(vb * N + i) / 2];
-        const float y0 = b[i] * f.x - b[i + 1] * f.y, y1 = b[i + 1] * f.x + b[i] * f.y;
-        b[i] = y0;
-        b[i + 1] = y1;
-      }
-    }
-    T* y = static_cast<T*>(is_q ? P.oq : P.ok) + row * (is_q ? P.oqs : P.oks) +
-           static_cast<long long>(hh) * P.D;
-    *(reinterpret_cast<uint4*>(y) + va) = pack(a);
-    *(reinterpret_cast<uint4*>(y) + vb) = pack(b);
+    h -= heads;
   }
 }
 
@@ -248,14 +273,13 @@ cudaError_t launch_norm_rope(const NormRopeParams& Q, bool fast, cudaStream_t s)
                               kNrThreads, 0, s>>>(P);
     return cudaGetLastError();
   }
-  const int lph = P.D / (2 * Vec<T>::n);
-  // Up to 8 tokens a CTA while that leaves 8 CTAs a multiprocessor; fewer tokens than that: the
-  // heads of a token are shared out, one pass of the CTA's threads each.
-  P.tokens = std::max(1, std::min(8, P.T / (8 * 152)));
-  const int pass = kNrThreads / lph;
-  P.splits = P.T < 4 * 152 ? std::max(1, (heads + pass - 1) / pass) : 1;
-  const long long groups = (P.T + P.tokens - 1) / P.tokens;
-  const unsigned grid = static_cast<unsigned>(groups * P.splits);
+  const int lph = P.D / (2 * Vec<T>::n), groups = kNrThreads / lph;
+  // Up to 8 tokens a CTA, as many as leave 8 CTAs a multiprocessor; with few tokens the heads of
+  // each are shared out so that a group has one.
+  P.tokens = 1;
+  while (P.tokens < 8 && P.tokens < groups && P.T / (2 * P.tokens) >= 8 * 152) P.tokens *= 2;
+  P.splits = P.T < 4 * 152 ? (heads + groups - 1) / groups : 1;
+  const unsigned grid = static_cast<unsigned>((P.T + P.tokens - 1) / P.tokens * static_cast<long long>(P.splits));
   const size_t smem = static_cast<size_t>(P.tokens) * (P.rot / 2) * sizeof(float2);
   switch (lph) {
     case 4: norm_rope_kernel<T, 4><<<grid, kNrThreads, smem, s>>>(P); break;
