@@ -93,24 +93,15 @@ __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
 // its heads in turn, so that sines, cosines and weights stay in registers; the next head is loaded
 // while this one is worked on.
 template <typename T, int LPH>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P) {
+__global__ void __launch_bounds__(kNrThreads, 4) norm_rope_kernel(NormRopeParams P) {
   constexpr int N = Vec<T>::n, G = kNrThreads / LPH;
-  extern __shared__ float2 cs[];  // [tokens][rot / 2] cosine, sine
+  extern __shared__ __align__(16) float2 cs[];  // per token: cosine, sine of each thread's pairs
   const int half = P.rot / 2;
   const int block = blockIdx.x / P.splits, split = blockIdx.x - block * P.splits;
   const int t0 = block * P.tokens, nt = min(P.tokens, P.T - t0);
-  unsigned long long turn = 0;
-  for (int i = threadIdx.x, last = -1; i < nt * half; i += kNrThreads) {
-    const int t = i / half, j = i - t * half;
-    if (j != last) turn = turn_fraction(P.freq[j]);  // the same j again where half divides the CTA
-    last = j;
-    cs[i] = cos_sin(turn, P.pos[t0 + t]);
-  }
-  __syncthreads();
   const int lane = threadIdx.x % LPH, group = threadIdx.x / LPH;
   const int per = G / P.tokens;  // groups of a token
   const int t = group / per;
-  if (t >= nt) return;
   const unsigned mask = (LPH == 32 ? 0xFFFFFFFFu : (1u << LPH) - 1u)
                         << ((threadIdx.x & 31) & ~(LPH - 1));  // the threads of this head
   // vectors of this thread: (lane, lane + rotated half) while they last, else neighbours
@@ -119,47 +110,54 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P)
   const int va = halves ? lane : 2 * lane, vb = halves ? lane + hv : 2 * lane + 1;
   // interleaved: whole vectors are rotated or not
   const bool pair_a = P.inter && va * N < P.rot, pair_b = P.inter && vb * N < P.rot;
-  float2 f[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    f[i] = make_float2(1.f, 0.f);
-    if (halves) f[i] = cs[t * half + va * N + i];
-    if (pair_a && i < N / 2) f[i] = cs[t * half + va * (N / 2) + i];
-    if (pair_b && i >= N / 2) f[i] = cs[t * half + vb * (N / 2) + i - N / 2];
-  }
-  const long long row = t0 + t;
-  const float inv_d = 1.f / static_cast<float>(P.D);
   // heads of q, then of k: this group's are split * per + group % per and every (splits * per)-th on
   int h = split * per + group % per;
   const int step = P.splits * per;
+  const long long row = t0 + min(t, nt - 1);
+  auto source = [&](bool k, int head) {
+    return reinterpret_cast<const uint4*>(static_cast<const T*>(k ? P.k : P.q) +
+                                          row * (k ? P.ks : P.qs) + static_cast<long long>(head) * P.D);
+  };
+  // the next head is on its way at any time, the first one while the sines are computed
+  uint4 na = make_uint4(0u, 0u, 0u, 0u), nb = na;
+  auto fetch = [&](int head) {  // of q, then of k
+    if (head >= P.hq + P.hk) return;
+    const uint4* x = source(head >= P.hq, head < P.hq ? head : head - P.hq);
+    na = __ldcs(x + va);
+    nb = __ldcs(x + vb);
+  };
+  fetch(h);
+  unsigned long long turn = 0;
+  for (int i = threadIdx.x, last = -1; i < nt * half; i += kNrThreads) {
+    const int t = i / half, j = i - t * half;
+    if (j != last) turn = turn_fraction(P.freq[j]);  // the same j again where half divides the CTA
+    last = j;
+    // pair j % N of thread j / N, so that a head's threads read side by side
+    cs[((t * (N / 2) + j % N / 2) * LPH + j / N) * 2 + j % 2] = cos_sin(turn, P.pos[t0 + t]);
+  }
+  __syncthreads();
+  if (t >= nt) return;
+  const float4* angles = reinterpret_cast<const float4*>(cs) + t * (N / 2) * LPH + lane;
+  const float inv_d = 1.f / static_cast<float>(P.D);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int heads = which ? P.hk : P.hq;
     if (h < heads) {
       const uint4* w = static_cast<const uint4*>(which ? P.wk : P.wq);
-      float wa[N], wb[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) wa[i] = wb[i] = 1.f;
+      uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
       if (w) {
-        unpack(__ldg(w + va), wa);
-        unpack(__ldg(w + vb), wb);
+        ra = __ldg(w + va);
+        rb = __ldg(w + vb);
       }
-      const T* x = static_cast<const T*>(which ? P.k : P.q) + row * (which ? P.ks : P.qs) +
-                   static_cast<long long>(h) * P.D;
       T* y = static_cast<T*>(which ? P.ok : P.oq) + row * (which ? P.oks : P.oqs) +
              static_cast<long long>(h) * P.D;
       const int hop = step * P.D;
-      uint4 na = *(reinterpret_cast<const uint4*>(x) + va), nb = *(reinterpret_cast<const uint4*>(x) + vb);
 #pragma unroll 1
       for (; h < heads; h += step) {
         float a[N], b[N];
         unpack(na, a);
         unpack(nb, b);
-        x += hop;
-        if (h + step < heads) {
-          na = *(reinterpret_cast<const uint4*>(x) + va);
-          nb = *(reinterpret_cast<const uint4*>(x) + vb);
-        }
+        fetch((which ? P.hq : 0) + h + step);
         float sum = 0.f, sum2 = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -170,39 +168,54 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(NormRopeParams P)
 #pragma unroll
         for (int d = LPH / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(mask, sum, d, LPH);
         const float r = rsqrtf(fmaf(sum, inv_d, P.eps));
+        if (w) {
+          float wa[N], wb[N];
+          unpack(ra, wa);
+          unpack(rb, wb);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          a[i] *= r * wa[i];
-          b[i] *= r * wb[i];
+          for (int i = 0; i < N; ++i) {
+            a[i] *= r * wa[i];
+            b[i] *= r * wb[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            a[i] *= r;
+            b[i] *= r;
+          }
         }
         if (halves) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float y0 = a[i] * f[i].x - b[i] * f[i].y, y1 = b[i] * f[i].x + a[i] * f[i].y;
+          for (int i = 0; i < N; i += 2) {
+            const float4 f = angles[i / 2 * LPH];
+            float y0 = a[i] * f.x - b[i] * f.y, y1 = b[i] * f.x + a[i] * f.y;
             a[i] = y0;
             b[i] = y1;
-          }
-        }
-        if (pair_a) {
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const float2 c = f[i / 2];
-            const float y0 = a[i] * c.x - a[i + 1] * c.y, y1 = a[i + 1] * c.x + a[i] * c.y;
-            a[i] = y0;
-            a[i + 1] = y1;
-          }
-        }
-        if (pair_b) {
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const float2 c = f[N / 2 + i / 2];
-            const float y0 = b[i] * c.x - b[i + 1] * c.y, y1 = b[i + 1] * c.x + b[i] * c.y;
-            b[i] = y0;
+            y0 = a[i + 1] * f.z - b[i + 1] * f.w;
+            y1 = b[i + 1] * f.z + a[i + 1] * f.w;
+            a[i + 1] = y0;
             b[i + 1] = y1;
           }
         }
-        *(reinterpret_cast<uint4*>(y) + va) = pack(a);
-        *(reinterpret_cast<uint4*>(y) + vb) = pack(b);
+        if (pair_a || pair_b) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const float4 f = angles[i / 2 * LPH];  // two pairs: of a, then of b
+            float* x = i < N / 2 ? a : b;
+            const int k = 2 * i % N;
+            if (i < N / 2 ? pair_a : pair_b) {
+              float y0 = x[k] * f.x - x[k + 1] * f.y, y1 = x[k + 1] * f.x + x[k] * f.y;
+              x[k] = y0;
+              x[k + 1] = y1;
+              y0 = x[k + 2] * f.z - x[k + 3] * f.w;
+              y1 = x[k + 3] * f.z + x[k + 2] * f.w;
+              x[k + 2] = y0;
+              x[k + 3] = y1;
+            }
+          }
+        }
+        __stcs(reinterpret_cast<uint4*>(y) + va, pack(a));
+        __stcs(reinterpret_cast<uint4*>(y) + vb, pack(b));
         y += hop;
       }
     }
@@ -280,7 +293,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& Q, bool fast, cudaStream_t s)
   while (P.tokens < 8 && P.tokens < groups && P.T / (2 * P.tokens) >= 8 * 152) P.tokens *= 2;
   P.splits = P.T < 4 * 152 ? (heads + groups - 1) / groups : 1;
   const unsigned grid = static_cast<unsigned>((P.T + P.tokens - 1) / P.tokens * static_cast<long long>(P.splits));
-  const size_t smem = static_cast<size_t>(P.tokens) * (P.rot / 2) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(P.tokens) * (P.D / 2) * sizeof(float2);
   switch (lph) {
     case 4: norm_rope_kernel<T, 4><<<grid, kNrThreads, smem, s>>>(P); break;
     case 8: norm_rope_kernel<T, 8><<<grid, kNrThreads, smem, s>>>(P); break;
