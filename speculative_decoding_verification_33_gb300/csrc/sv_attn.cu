@@ -211,8 +211,9 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     fence_mbar_init();
   }
 
-  // this CTA's run of units; every pair of a CTA gets a unit at least
-  if (!find_run<S::kThreads, R, UNIT>(P, NP, s_scan, &s_run, &s_walk[0])) return;
+  // This CTA's run of units. Every pair of a CTA gets two units at least: with one, more pieces are
+  // to be joined, and one request of 4097 tokens takes 15.8 us instead of 14.5
+  if (!find_run<S::kThreads, R, UNIT>(P, 2 * NP, s_scan, &s_run, &s_walk[0])) return;
   if (tid < NP) {
     s_prod[tid].w = s_walk[0];
     s_prod[tid].u = s_run.u0 + tid;
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       }
     }
     if (!whole)
-      join_pieces<S::kThreads, R, D>(P, w, s_run, rows, tid, &s_last, [] { __syncthreads(); });
+      join_pieces<S::kThreads, R, D, 8>(P, w, s_run, rows, tid, &s_last, [] { __syncthreads(); });
     if (!more) break;
     __syncthreads();  // the joining buffers and statistics are free
   }

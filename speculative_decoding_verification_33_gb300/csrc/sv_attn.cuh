@@ -129,6 +129,12 @@ __device__ __forceinline__ void finish(const AttnParams& P, const Walk& w, int t
   if (d == 0) store_lse(P, at, M, L);
 }
 
+// a / b for a >= 0, b > 0: the 64-bit division takes some hundred instructions, few calls need it
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // This CTA's run of the call's units. run: first unit, past the last, all units, CTAs that have any.
 struct Run {
   long long u0, u1, U, ctas;
@@ -164,22 +170,22 @@ __device__ __forceinline__ bool find_run(const AttnParams& P, int least, long lo
     U += n;
   }
   before += x - mine;
-  const long long ctas = min(static_cast<long long>(gridDim.x), (U + least - 1) / least);
+  const long long ctas = min(static_cast<long long>(gridDim.x), divide(U + least - 1, least));
   if (blockIdx.x >= ctas) return false;
-  const long long u0 = U * blockIdx.x / ctas;
+  const long long u0 = divide(U * blockIdx.x, ctas);
   if (u0 >= before && u0 < before + mine) {
     for (int b = b0; b < b1; ++b) {
       load_seq<R, UNIT>(P, b, w);
       const long long n = seq_units(P, w);
       if (u0 < before + n) {
-        const long long item = (u0 - before) / w.nu;
-        w.h = static_cast<int>(item / w.rts);
+        const long long item = divide(u0 - before, w.nu);
+        w.h = static_cast<int>(divide(item, w.rts));
         w.rt = static_cast<int>(item - static_cast<long long>(w.h) * w.rts);
         w.base = before + item * w.nu;
         load_ahead(P, w);
         *first = w;
         run->u0 = u0;
-        run->u1 = U * (blockIdx.x + 1) / ctas;
+        run->u1 = divide(U * (blockIdx.x + 1), ctas);
         run->U = U;
         run->ctas = ctas;
         break;
@@ -194,20 +200,20 @@ __device__ __forceinline__ bool find_run(const AttnParams& P, int least, long lo
 // A piece of an item is written (R x D outputs, maxima, sums at P.part + slot * part_floats): counts
 // it, and in the last CTA to arrive at the item joins its pieces, in their order. THREADS threads
 // call it, tid of them this one, with `sync` a barrier among them.
-template <int THREADS, int R, int D, class Sync>
+template <int THREADS, int R, int D, int BATCH, class Sync>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const Walk& w, const Run& run,
                                             int rows, int tid, int* s_last, Sync sync) {
   constexpr long long kPart = R * (D + 2);
   // pieces of this item lie with CTAs first .. last
-  const int first = static_cast<int>(((w.base + 1) * run.ctas + run.U - 1) / run.U) - 1;
-  const int last = static_cast<int>(((w.base + w.nu) * run.ctas + run.U - 1) / run.U) - 1;
+  const int first = static_cast<int>(divide((w.base + 1) * run.ctas + run.U - 1, run.U)) - 1;
+  const int last = static_cast<int>(divide((w.base + w.nu) * run.ctas + run.U - 1, run.U)) - 1;
   __threadfence();
   sync();
   if (tid == 0) *s_last = atomicAdd(&P.arrived[first], 1u) == static_cast<unsigned>(last - first);
   sync();
   if (!*s_last) return;
   __threadfence();
-  const int slot0 = 2 * first + (run.U * first / run.ctas >= w.base ? 0 : 1);
+  const int slot0 = 2 * first + (divide(run.U * first, run.ctas) >= w.base ? 0 : 1);
   auto part_of = [&](int k) {
     return P.part + static_cast<long long>(k == first ? slot0 : 2 * k) * kPart;
   };
@@ -215,18 +221,37 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const Walk& w, 
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
     float M = -FLT_MAX, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = first; k <= last; ++k) M = fmaxf(M, __ldcg(part_of(k) + R * D + r));
-#pragma unroll 4
-    for (int k = first; k <= last; ++k) {
-      const float* part = part_of(k);
-      const float f = ex2_fast(__ldcg(part + R * D + r) - M);
-      L += __ldcg(part + R * D + R + r) * f;
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + r * D + d));
-      o.x += x.x * f;
-      o.y += x.y * f;
-      o.z += x.z * f;
-      o.w += x.w * f;
+    // a few pieces at a time, so that their loads are in flight together
+    for (int k0 = first; k0 <= last; k0 += BATCH) {
+      float m[BATCH], l[BATCH], top = M;
+      float4 x[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        m[i] = -FLT_MAX;
+        l[i] = 0.f;
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + i <= last) {
+          const float* part = part_of(k0 + i);
+          m[i] = __ldcg(part + R * D + r);
+          l[i] = __ldcg(part + R * D + R + r);
+          x[i] = __ldcg(reinterpret_cast<const float4*>(part + r * D + d));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) top = fmaxf(top, m[i]);
+      const float down = ex2_fast(M - top);
+      M = top;
+      L *= down;
+      o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float f = ex2_fast(m[i] - M);
+        L += l[i] * f;
+        o.x += x[i].x * f;
+        o.y += x[i].y * f;
+        o.z += x[i].z * f;
+        o.w += x[i].w * f;
+      }
     }
     finish(P, w, R, r, d, D, o, M, L);
   }

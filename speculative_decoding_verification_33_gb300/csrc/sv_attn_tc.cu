@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         }
       }
       if (!whole)
-        join_pieces<kTcWThreads, R, D>(P, w, S.run, rows, wid, &S.last, [] { named_sync(6, kTcWThreads); });
+        join_pieces<kTcWThreads, R, D, 4>(P, w, S.run, rows, wid, &S.last, [] { named_sync(6, kTcWThreads); });
       named_sync(1 + hh, 128);  // maxima and sums may change
       if (t < tiles) next_item<R, kTcUnit>(P, w);
       unit = 0;
