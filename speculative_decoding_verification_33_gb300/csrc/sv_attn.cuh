@@ -129,12 +129,6 @@ __device__ __forceinline__ void finish(const AttnParams& P, const Walk& w, int t
   if (d == 0) store_lse(P, at, M, L);
 }
 
-// a / b for a >= 0, b > 0: the 64-bit division takes some hundred instructions, few calls need it
-__device__ __forceinline__ long long divide(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 // This CTA's run of the call's units. run: first unit, past the last, all units, CTAs that have any.
 struct Run {
   long long u0, u1, U, ctas;

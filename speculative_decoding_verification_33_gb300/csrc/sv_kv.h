@@ -29,6 +29,15 @@ struct KvBlock {
   }
 };
 
+#ifdef __CUDACC__
+// a / b for a >= 0, b > 0: the 64-bit division takes some hundred instructions, few calls need it
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+#endif
+
 // Attention of new tokens over the cache (sv_attn.cu).
 struct AttnParams {
   int B, T, hq, hkv, group;  // group = hq / hkv

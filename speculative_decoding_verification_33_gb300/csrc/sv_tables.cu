@@ -15,11 +15,10 @@
 namespace sv {
 namespace {
 
-constexpr int kTbThreads = 256;
 constexpr int kTbTokens = 4;  // consecutive tokens a thread writes (32-byte stores of slots)
 
 struct TablesParams {
-  int B, ps, max_blocks, max_tokens, ring_size;
+  int B, ps_log, max_blocks, max_tokens, ring_size;
   const int32_t *ctx, *acc, *nw, *held;
   int32_t *table, *ring;
   const int64_t* counters;
@@ -40,9 +39,9 @@ __device__ __forceinline__ Seq load_seq(const TablesParams& P, int b) {
   const bool done = nw < 0;
   s.c = done ? 0 : static_cast<long long>(ctx) + (a >= 0 ? static_cast<long long>(a) + 1 : 0);
   s.n = done ? 0 : nw;
-  const long long need = (s.c + s.n + P.ps - 1) / P.ps;
+  const long long need = (s.c + s.n + (1LL << P.ps_log) - 1) >> P.ps_log;
   s.bad = s.held < 0 || s.held > P.max_blocks ||
-          (!done && (ctx < 0 || s.c > static_cast<long long>(s.held) * P.ps || need > P.max_blocks));
+          (!done && (ctx < 0 || s.c > (static_cast<long long>(s.held) << P.ps_log) || need > P.max_blocks));
   if (s.bad) {
     s.c = ctx;
     s.n = s.grow = s.shrink = 0;
@@ -53,31 +52,44 @@ __device__ __forceinline__ Seq load_seq(const TablesParams& P, int b) {
   return s;
 }
 
-// Exclusive prefix sum of `v` over the CTA's threads; *total is the sum. `part` holds one value
-// per warp; the call starts with a barrier, so that it may be used again.
-__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* total) {
+// Exclusive prefix sums of N values over the CTA's threads; total[] the sums. `part` holds N values a
+// warp; the call starts with a barrier, so that it may be used again.
+template <int THREADS, int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long (*part)[N], long long (&total)[N]) {
+  constexpr int W = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  long long x[N];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
+  for (int i = 0; i < N; ++i) {
+    x[i] = v[i];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, x[i], d);
+      if (lane >= d) x[i] += y;
+    }
   }
   __syncthreads();
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  long long before = 0, sum = 0;
+  if (lane == 31)
 #pragma unroll
-  for (int w = 0; w < kTbThreads / 32; ++w) {
-    const long long p = part[w];
-    if (w < warp) before += p;
-    sum += p;
+    for (int i = 0; i < N; ++i) part[warp][i] = x[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {  // each warp sums up the warps
+    long long p = lane < W ? part[lane][i] : 0;
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, p, d);
+      if (lane >= d) p += y;
+    }
+    total[i] = __shfl_sync(0xFFFFFFFFu, p, W - 1);
+    const long long before = __shfl_sync(0xFFFFFFFFu, p, warp ? warp - 1 : 0);
+    v[i] = x[i] - v[i] + (warp ? before : 0);
   }
-  *total = sum;
-  return before + x - v;
 }
 
-__global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
+// A sequence a thread as far as the threads go: its lengths are then read once.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
   // per sequence: first token of the round, tokens before the round, pages held before and
   // after the call, rank of its first queue entry taken or put back
   extern __shared__ int32_t sm[];
@@ -86,57 +98,67 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
   int32_t* s_held = s_c + P.B;
   int32_t* s_now = s_held + P.B;
   int32_t* s_rank = s_now + P.B;
-  __shared__ long long part[kTbThreads / 32];
+  __shared__ long long part[THREADS / 32][3];
 
   const int tid = threadIdx.x;
-  const int per = (P.B + kTbThreads - 1) / kTbThreads;
+  const int per = (P.B + THREADS - 1) / THREADS;
   const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
   const long long cap = P.ring_size;
   const long long head = P.counters[0], tail = P.counters[1];
   long long live = tail - head;
   live = live < 0 ? 0 : live > cap ? cap : live;
-  long long h0 = cap ? head % cap : 0, t0 = cap ? tail % cap : 0;
-  h0 += h0 < 0 ? cap : 0;
-  t0 += t0 < 0 ? cap : 0;
+  auto wrap = [&](long long i) {  // i modulo cap
+    if (i >= 0) return i - divide(i, cap) * cap;
+    i %= cap;
+    return i < 0 ? i + cap : i;
+  };
+  const long long h0 = wrap(head), t0 = wrap(tail);
 
-  long long grow = 0, shrink = 0, n = 0;
+  Seq one;
+  if (b0 < b1) one = load_seq(P, b0);
+  auto sequence = [&](int b) { return b == b0 ? one : load_seq(P, b); };
+  long long sums[3] = {0, 0, 0}, all[3];  // pages taken, pages put back, tokens
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq(P, b);
-    grow += s.grow;
-    shrink += s.shrink;
-    n += s.n;
+    const Seq s = sequence(b);
+    sums[0] += s.grow;
+    sums[1] += s.shrink;
+    sums[2] += s.n;
   }
-  long long all_grow, all_shrink, all_n;
-  const long long grow0 = block_scan(grow, part, &all_grow);
-  const long long shrink0 = block_scan(shrink, part, &all_shrink);
+  block_scan<THREADS>(sums, part, all);
+  const long long grow0 = sums[0], shrink0 = sums[1], all_grow = all[0], all_shrink = all[1];
+  long long n0 = sums[2], all_n = all[2];
+  long long(*part1)[1] = reinterpret_cast<long long(*)[1]>(part);
   if (all_grow > live) {  // tokens of the sequences whose pages run out do not count
-    long long g = grow0;
-    n = 0;
+    long long g = grow0, n[1] = {0}, total[1];
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(P, b);
+      const Seq s = sequence(b);
       g += s.grow;
-      n += s.grow > 0 && g > live ? 0 : s.n;
+      n[0] += s.grow > 0 && g > live ? 0 : s.n;
     }
+    block_scan<THREADS>(n, part1, total);
+    n0 = n[0];
+    all_n = total[0];
   }
-  const long long n0 = block_scan(n, part, &all_n);
   // ranks of the scheduled tokens: n0 unless some do not fit in the token arrays
   long long u0 = n0, all_u = all_n;
   if (all_n > P.max_tokens) {
-    long long g = grow0, m = n0, u = 0;
+    long long g = grow0, m = n0, u[1] = {0}, total[1];
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(P, b);
+      const Seq s = sequence(b);
       g += s.grow;
       const long long nb = s.grow > 0 && g > live ? 0 : s.n;
       m += nb;
-      u += m > P.max_tokens ? 0 : nb;
+      u[0] += m > P.max_tokens ? 0 : nb;
     }
-    u0 = block_scan(u, part, &all_u);
+    block_scan<THREADS>(u, part1, total);
+    u0 = u[0];
+    all_u = total[0];
   }
 
   // the sequences: what the tokens need into shared memory, the outputs from CTA 0
   long long g = grow0, f = shrink0, m = n0, u = u0, taken = 0;
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq(P, b);
+    const Seq s = sequence(b);
     const long long g_before = g;
     g += s.grow;
     const bool lacks = s.grow > 0 && g > live;
@@ -163,10 +185,10 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
     }
   }
   if (blockIdx.x == 0) {
-    long long all_taken;
-    block_scan(taken, part, &all_taken);
+    long long sum[1] = {taken}, all_taken[1];
+    block_scan<THREADS>(sum, part1, all_taken);
     if (tid == 0) {
-      P.o_counters[0] = head + all_taken;
+      P.o_counters[0] = head + all_taken[0];
       P.o_counters[1] = tail + all_shrink;
       P.o_cu[P.B] = static_cast<int32_t>(all_u);
     }
@@ -177,8 +199,8 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
   // table entries of new pages, ring entries of pages put back: a warp a sequence, four loads in
   // flight (a prompt takes hundreds of pages)
   const int lane = tid & 31;
-  for (int b = blockIdx.x * (kTbThreads / 32) + (tid >> 5); b < P.B;
-       b += gridDim.x * (kTbThreads / 32)) {
+  for (int b = blockIdx.x * (THREADS / 32) + (tid >> 5); b < P.B;
+       b += gridDim.x * (THREADS / 32)) {
     const int held = s_held[b], now = s_now[b];
     int32_t* row = P.table + static_cast<long long>(b) * P.max_blocks;
     const bool takes = now > held;
@@ -206,8 +228,8 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
 
   // the tokens
   const int total = static_cast<int>(all_u);
-  const long long step = static_cast<long long>(gridDim.x) * kTbThreads * kTbTokens;
-  for (long long base = (static_cast<long long>(blockIdx.x) * kTbThreads + tid) * kTbTokens;
+  const long long step = static_cast<long long>(gridDim.x) * THREADS * kTbTokens;
+  for (long long base = (static_cast<long long>(blockIdx.x) * THREADS + tid) * kTbTokens;
        base < P.max_tokens; base += step) {
     int b = 0;
     if (base < total) {  // last sequence that starts at or before the token
@@ -233,7 +255,7 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
         }
         seq = b;
         pos = s_c[b] + static_cast<int>(t - s_cu[b]);
-        const int blk = pos / P.ps;
+        const int blk = pos >> P.ps_log;
         if (blk != blk_of) {
           blk_of = blk;
           const int held = s_held[b];
@@ -245,13 +267,28 @@ __global__ void __launch_bounds__(kTbThreads) tables_kernel(TablesParams P) {
             page = P.ring[i];
           }
         }
-        slot = page < 0 ? -1 : static_cast<long long>(page) * P.ps + pos % P.ps;
+        slot = page < 0 ? -1 : (static_cast<long long>(page) << P.ps_log) + (pos & ((1 << P.ps_log) - 1));
       }
       P.o_slots[t] = slot;
       P.o_pos[t] = pos;
       P.o_seq[t] = seq;
     }
   }
+}
+
+template <int THREADS>
+cudaError_t launch_tables(const TablesParams& P, cudaStream_t stream) {
+  // a CTA for every THREADS * kTbTokens tokens or 64 sequences, at most two a multiprocessor
+  const long long want = 1 + std::max((P.max_tokens - 1) / (THREADS * kTbTokens), (P.B - 1) / 64);
+  const int grid = static_cast<int>(std::max(1LL, std::min<long long>(want, 304)));
+  const size_t smem = (5 * static_cast<size_t>(P.B) + 1) * sizeof(int32_t);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        tables_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  tables_kernel<THREADS><<<grid, THREADS, smem, stream>>>(P);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -284,7 +321,7 @@ extern "C" sv_status spec_block_tables(
   if (B > sv::kTablesMaxB) return SV_ERR_UNSUPPORTED;
   sv::TablesParams P;
   P.B = B;
-  P.ps = page_size;
+  P.ps_log = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   P.max_blocks = max_blocks;
   P.max_tokens = max_tokens;
   P.ring_size = ring_size;
@@ -304,17 +341,9 @@ extern "C" sv_status spec_block_tables(
   P.o_seq = out_seq_ids;
   P.o_counters = out_counters;
   P.o_slots = out_slots;
-  // one CTA for every 1024 tokens or 64 sequences, at most two a multiprocessor
-  const long long want =
-      1 + std::max((max_tokens - 1) / (sv::kTbThreads * sv::kTbTokens), (B - 1) / 64);
-  const int grid = static_cast<int>(std::min<long long>(want, 304));
-  const size_t smem = (5 * static_cast<size_t>(B) + 1) * sizeof(int32_t);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(sv::tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess) {
-    cudaGetLastError();
-    return SV_ERR_CUDA;
-  }
-  sv::tables_kernel<<<grid, sv::kTbThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = B <= 128   ? sv::launch_tables<128>(P, st)
+                        : B <= 512 ? sv::launch_tables<512>(P, st)
+                                   : sv::launch_tables<1024>(P, st);
+  return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

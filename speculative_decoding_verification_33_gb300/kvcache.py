@@ -27,13 +27,21 @@ def _stream(stream, like: torch.Tensor) -> int:
 
 def _dev(t: torch.Tensor, dtype, shape, name: str) -> int:
     """Address of a contiguous CUDA tensor of this dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def _vec(t: torch.Tensor, dtype, n: int, name: str) -> int:
+    """Address of a contiguous CUDA tensor of this dtype that holds n values. These calls take some
+    microseconds in all, so what is checked of each of a dozen tensors counts."""
+    if t.dtype is dtype and t.numel() == n and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, dtype, (n,), name)
 
 
 def _rows(t: torch.Tensor, name: str):
@@ -68,7 +76,7 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
     B = ctx_lens.shape[0]
     if block_table.dim() != 2 or ring.dim() != 1:
         raise ValueError("block_table must be [B, max_blocks] and ring [pages]")
-    most = block_table.shape[1]
+    most, ring_size = block_table.shape[1], ring.shape[0]
     if out is None:
         dev = ctx_lens.device
 
@@ -77,19 +85,18 @@ def block_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: to
         out = {"ctx_lens": new(B), "held": new(B), "counters": new(2, i64), "cu_new": new(B + 1),
                "kv_lens": new(B), "status": new(B), "slots": new(max_tokens, i64),
                "positions": new(max_tokens), "seq_ids": new(max_tokens)}
-    per, tok = (B,), (max_tokens,)
     st = _lib.load().spec_block_tables(
-        B, page_size, most, max_tokens, _dev(ctx_lens, i32, per, "ctx_lens"),
-        0 if accept_len is None else _dev(accept_len, i32, per, "accept_len"),
-        _dev(new_lens, i32, per, "new_lens"), _dev(block_table, i32, (B, most), "block_table"),
-        _dev(held, i32, per, "held"), _dev(ring, i32, ring.shape, "ring"), ring.shape[0],
-        _dev(counters, i64, (2,), "counters"), _dev(out["ctx_lens"], i32, per, "out ctx_lens"),
-        _dev(out["held"], i32, per, "out held"),
-        _dev(out["counters"], i64, (2,), "out counters"),
-        _dev(out["kv_lens"], i32, per, "out kv_lens"), _dev(out["status"], i32, per, "out status"),
-        _dev(out["cu_new"], i32, (B + 1,), "out cu_new"), _dev(out["slots"], i64, tok, "out slots"),
-        _dev(out["positions"], i32, tok, "out positions"),
-        _dev(out["seq_ids"], i32, tok, "out seq_ids"), _stream(stream, ctx_lens))
+        B, page_size, most, max_tokens, _vec(ctx_lens, i32, B, "ctx_lens"),
+        0 if accept_len is None else _vec(accept_len, i32, B, "accept_len"),
+        _vec(new_lens, i32, B, "new_lens"), _vec(block_table, i32, B * most, "block_table"),
+        _vec(held, i32, B, "held"), _vec(ring, i32, ring_size, "ring"),
+        ring_size, _vec(counters, i64, 2, "counters"), _vec(out["ctx_lens"], i32, B, "out ctx_lens"),
+        _vec(out["held"], i32, B, "out held"), _vec(out["counters"], i64, 2, "out counters"),
+        _vec(out["kv_lens"], i32, B, "out kv_lens"), _vec(out["status"], i32, B, "out status"),
+        _vec(out["cu_new"], i32, B + 1, "out cu_new"),
+        _vec(out["slots"], i64, max_tokens, "out slots"),
+        _vec(out["positions"], i32, max_tokens, "out positions"),
+        _vec(out["seq_ids"], i32, max_tokens, "out seq_ids"), _stream(stream, ctx_lens))
     _lib._check(st, "spec_block_tables")
     return out
 
@@ -114,16 +121,17 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     for n, h in (("q", hq), ("k", hk)):
         if h and (out[n].dtype != q.dtype or out[n].shape != (T, h, D)):
             raise ValueError(f"out {n} must be {(T, h, D)} of q's dtype")
+    half = inv_freq.numel()
     qp, qs = _rows(q, "q")
     oq, oqs = _rows(out["q"], "out q")
     kp, ks = _rows(k, "k") if k is not None else (0, 0)
     ok, oks = _rows(out["k"], "out k") if k is not None else (0, 0)
     st = _lib.load().spec_qk_norm_rope(
-        T, hq, hk, D, 2 * inv_freq.shape[0], bool(interleaved), code, qp, qs, kp, ks,
-        0 if q_weight is None else _dev(q_weight, q.dtype, (D,), "q_weight"),
-        0 if k_weight is None else _dev(k_weight, q.dtype, (D,), "k_weight"),
-        _dev(positions, torch.int32, (T,), "positions"),
-        _dev(inv_freq, torch.float64, (inv_freq.shape[0],), "inv_freq"), eps, oq, oqs, ok, oks,
+        T, hq, hk, D, 2 * half, bool(interleaved), code, qp, qs, kp, ks,
+        0 if q_weight is None else _vec(q_weight, q.dtype, D, "q_weight"),
+        0 if k_weight is None else _vec(k_weight, q.dtype, D, "k_weight"),
+        _vec(positions, torch.int32, T, "positions"),
+        _vec(inv_freq, torch.float64, half, "inv_freq"), eps, oq, oqs, ok, oks,
         _stream(stream, q))
     _lib._check(st, "spec_qk_norm_rope")
     return out
@@ -167,7 +175,7 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
     vp, vs = _rows(v, "v")
     st = _lib.load().spec_kv4_append(
         T, H, D, page_size, cache.shape[0], _float_code(k, "k"), kp, ks, vp, vs,
-        _dev(slots, torch.int64, (T,), "slots"), k_scale, v_scale,
+        _vec(slots, torch.int64, T, "slots"), k_scale, v_scale,
         _cache(cache, H, D, page_size),
         _dev(out["k"], torch.bfloat16, (T, H, D), "out k") if out else 0,
         _dev(out["v"], torch.bfloat16, (T, H, D), "out v") if out else 0, _stream(stream, k))
@@ -200,7 +208,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         B, T, hq, H, D, page_size, cache.shape[0], block_table.shape[1], qp, qs,
         _cache(cache, H, D, page_size),
         _dev(block_table, torch.int32, (B, block_table.shape[1]), "block_table"),
-        _dev(kv_lens, torch.int32, (B,), "kv_lens"), _dev(cu_new, torch.int32, (B + 1,), "cu_new"),
+        _vec(kv_lens, torch.int32, B, "kv_lens"), _vec(cu_new, torch.int32, B + 1, "cu_new"),
         D ** -0.5 if scale is None else scale, k_scale, v_scale, max_new,
         _dev(out["out"], torch.bfloat16, (T, hq, D), "out"),
         0 if lse is None else _dev(lse, torch.float32, (T, hq), "lse"), _stream(stream, q))
