@@ -15,7 +15,7 @@
 namespace sv {
 namespace {
 
-constexpr int kTbTokens = 4;  // consecutive tokens a thread writes (32-byte stores of slots)
+constexpr int kTbTokens = 2;  // consecutive tokens a thread writes
 
 struct TablesParams {
   int B, ps_log, max_blocks, max_tokens, ring_size;
@@ -52,38 +52,55 @@ __device__ __forceinline__ Seq load_seq(const TablesParams& P, int b) {
   return s;
 }
 
+// Sums held at 2^31 - 1: no limit that they are compared with (free pages, token places) is larger,
+// so what is past it stays past it.
+constexpr uint32_t kMost = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kMost); }
+__device__ __forceinline__ uint32_t held_at_most(long long a) {
+  return a > static_cast<long long>(kMost) ? kMost : static_cast<uint32_t>(a);
+}
+
 // Exclusive prefix sums of N values over the CTA's threads; total[] the sums. `part` holds N values a
 // warp; the call starts with a barrier, so that it may be used again.
 template <int THREADS, int N>
-__device__ __forceinline__ void block_scan(long long (&v)[N], long long (*part)[N], long long (&total)[N]) {
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t (*part)[N], uint32_t (&total)[N]) {
   constexpr int W = THREADS / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x[N];
+  uint32_t x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = v[i];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x[i], d);
+      if (lane >= d) x[i] = add(x[i], y);
+    }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    x[i] = v[i];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, x[i], d);
-      if (lane >= d) x[i] += y;
-    }
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x[i], 1);
+    v[i] = lane ? y : 0;  // before this thread, within the warp
   }
   __syncthreads();
   if (lane == 31)
 #pragma unroll
     for (int i = 0; i < N; ++i) part[warp][i] = x[i];
   __syncthreads();
+  uint32_t p[N];  // each warp sums up the warps
 #pragma unroll
-  for (int i = 0; i < N; ++i) {  // each warp sums up the warps
-    long long p = lane < W ? part[lane][i] : 0;
+  for (int i = 0; i < N; ++i) p[i] = lane < W ? part[lane][i] : 0;
 #pragma unroll
-    for (int d = 1; d < W; d <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, p, d);
-      if (lane >= d) p += y;
+  for (int d = 1; d < W; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, p[i], d);
+      if (lane >= d) p[i] = add(p[i], y);
     }
-    total[i] = __shfl_sync(0xFFFFFFFFu, p, W - 1);
-    const long long before = __shfl_sync(0xFFFFFFFFu, p, warp ? warp - 1 : 0);
-    v[i] = x[i] - v[i] + (warp ? before : 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = __shfl_sync(0xFFFFFFFFu, p[i], W - 1);
+    const uint32_t before = __shfl_sync(0xFFFFFFFFu, p[i], warp ? warp - 1 : 0);
+    if (warp) v[i] = add(v[i], before);
   }
 }
 
@@ -98,12 +115,14 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
   int32_t* s_held = s_c + P.B;
   int32_t* s_now = s_held + P.B;
   int32_t* s_rank = s_now + P.B;
-  __shared__ long long part[THREADS / 32][3];
+  __shared__ uint32_t part[THREADS / 32][3];
 
   const int tid = threadIdx.x;
   const int per = (P.B + THREADS - 1) / THREADS;
   const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
   const long long cap = P.ring_size;
+  Seq one;
+  if (b0 < b1) one = load_seq(P, b0);
   const long long head = P.counters[0], tail = P.counters[1];
   long long live = tail - head;
   live = live < 0 ? 0 : live > cap ? cap : live;
@@ -114,26 +133,25 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
   };
   const long long h0 = wrap(head), t0 = wrap(tail);
 
-  Seq one;
-  if (b0 < b1) one = load_seq(P, b0);
   auto sequence = [&](int b) { return b == b0 ? one : load_seq(P, b); };
-  long long sums[3] = {0, 0, 0}, all[3];  // pages taken, pages put back, tokens
+  uint32_t sums[3] = {0, 0, 0}, all[3];  // pages taken, pages put back, tokens
   for (int b = b0; b < b1; ++b) {
     const Seq s = sequence(b);
-    sums[0] += s.grow;
-    sums[1] += s.shrink;
-    sums[2] += s.n;
+    sums[0] = add(sums[0], held_at_most(s.grow));
+    sums[1] = add(sums[1], held_at_most(s.shrink));
+    sums[2] = add(sums[2], held_at_most(s.n));
   }
   block_scan<THREADS>(sums, part, all);
   const long long grow0 = sums[0], shrink0 = sums[1], all_grow = all[0], all_shrink = all[1];
   long long n0 = sums[2], all_n = all[2];
-  long long(*part1)[1] = reinterpret_cast<long long(*)[1]>(part);
+  uint32_t(*part1)[1] = reinterpret_cast<uint32_t(*)[1]>(part);
   if (all_grow > live) {  // tokens of the sequences whose pages run out do not count
-    long long g = grow0, n[1] = {0}, total[1];
+    long long g = grow0;
+    uint32_t n[1] = {0}, total[1];
     for (int b = b0; b < b1; ++b) {
       const Seq s = sequence(b);
       g += s.grow;
-      n[0] += s.grow > 0 && g > live ? 0 : s.n;
+      n[0] = add(n[0], s.grow > 0 && g > live ? 0 : held_at_most(s.n));
     }
     block_scan<THREADS>(n, part1, total);
     n0 = n[0];
@@ -142,13 +160,14 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
   // ranks of the scheduled tokens: n0 unless some do not fit in the token arrays
   long long u0 = n0, all_u = all_n;
   if (all_n > P.max_tokens) {
-    long long g = grow0, m = n0, u[1] = {0}, total[1];
+    long long g = grow0, m = n0;
+    uint32_t u[1] = {0}, total[1];
     for (int b = b0; b < b1; ++b) {
       const Seq s = sequence(b);
       g += s.grow;
       const long long nb = s.grow > 0 && g > live ? 0 : s.n;
       m += nb;
-      u[0] += m > P.max_tokens ? 0 : nb;
+      u[0] = add(u[0], m > P.max_tokens ? 0 : held_at_most(nb));
     }
     block_scan<THREADS>(u, part1, total);
     u0 = u[0];
@@ -185,7 +204,7 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
     }
   }
   if (blockIdx.x == 0) {
-    long long sum[1] = {taken}, all_taken[1];
+    uint32_t sum[1] = {held_at_most(taken)}, all_taken[1];
     block_scan<THREADS>(sum, part1, all_taken);
     if (tid == 0) {
       P.o_counters[0] = head + all_taken[0];
@@ -240,38 +259,35 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(TablesParams P) {
       }
       b = lo;
     }
-    long long blk_of = -1;
-    int page = -1;
+    // where each token's page number stands, then all of them, then the results
+    const int32_t* at[kTbTokens];
+    int pos[kTbTokens], seq[kTbTokens], page[kTbTokens];
+#pragma unroll
+    for (int j = 0; j < kTbTokens; ++j) {
+      const long long t = base + j;
+      at[j] = nullptr;
+      pos[j] = 0;
+      seq[j] = -1;
+      if (t >= total) continue;
+      while (s_cu[b + 1] <= t) ++b;
+      seq[j] = b;
+      pos[j] = s_c[b] + static_cast<int>(t - s_cu[b]);
+      const int blk = pos[j] >> P.ps_log, held = s_held[b];
+      long long i = h0 + s_rank[b] + (blk - held);
+      i -= i >= cap ? cap : 0;
+      at[j] = blk < held ? P.table + static_cast<long long>(b) * P.max_blocks + blk : P.ring + i;
+    }
+#pragma unroll
+    for (int j = 0; j < kTbTokens; ++j) page[j] = at[j] ? *at[j] : -1;
 #pragma unroll
     for (int j = 0; j < kTbTokens; ++j) {
       const long long t = base + j;
       if (t >= P.max_tokens) break;
-      long long slot = -1;
-      int pos = 0, seq = -1;
-      if (t < total) {
-        while (s_cu[b + 1] <= t) {
-          ++b;
-          blk_of = -1;
-        }
-        seq = b;
-        pos = s_c[b] + static_cast<int>(t - s_cu[b]);
-        const int blk = pos >> P.ps_log;
-        if (blk != blk_of) {
-          blk_of = blk;
-          const int held = s_held[b];
-          if (blk < held) {
-            page = P.table[static_cast<long long>(b) * P.max_blocks + blk];
-          } else {
-            long long i = h0 + s_rank[b] + (blk - held);
-            i -= i >= cap ? cap : 0;
-            page = P.ring[i];
-          }
-        }
-        slot = page < 0 ? -1 : (static_cast<long long>(page) << P.ps_log) + (pos & ((1 << P.ps_log) - 1));
-      }
-      P.o_slots[t] = slot;
-      P.o_pos[t] = pos;
-      P.o_seq[t] = seq;
+      P.o_slots[t] = page[j] < 0 ? -1
+                                 : (static_cast<long long>(page[j]) << P.ps_log) +
+                                       (pos[j] & ((1 << P.ps_log) - 1));
+      P.o_pos[t] = pos[j];
+      P.o_seq[t] = seq[j];
     }
   }
 }
@@ -343,7 +359,6 @@ extern "C" sv_status spec_block_tables(
   P.o_slots = out_slots;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = B <= 128   ? sv::launch_tables<128>(P, st)
-                        : B <= 512 ? sv::launch_tables<512>(P, st)
-                                   : sv::launch_tables<1024>(P, st);
+                                                          : sv::launch_tables<512>(P, st);
   return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
