@@ -117,55 +117,58 @@ struct KeyCodes {
   }
 };
 
-// Half h of a thread's values of a block as operands: D / 16 values of the token pairs c and
-// c + 4. A token that some row does not see must not reach it as 0 * NaN: in a masked block its
-// scale is taken as 0 where the cache holds nothing (past the length) or a NaN; `nan_at` bit i then
-// says that token i, which some rows see, has a NaN scale among this thread's values.
+// Half h of a thread's values of a block: D / 16 values of the token pairs c and c + 4.
 template <int D>
-__device__ __forceinline__ void value_operands(const unsigned char* blk, int g, int c, int h,
-                                               bool masked, int t0, int len, int all_see,
-                                               uint32_t (&f)[D / 32][4], uint32_t& nan_at) {
-  constexpr int N = D / 64;  // words of a thread's codes of one token pair
-  uint32_t va[N], vb[N], fa, fb;
-  const unsigned char* codes = blk + KvBlock<D>::kValCodes + c * D +
-                               KvBlock<D>::kChunk * KvBlock<D>::place(c, g) + 4 * N * h;
-  const unsigned char* scales = blk + KvBlock<D>::kValScales + c * (D / 8) +
-                                2 * (D == 128 ? g : g >> 1);
-  if (D == 128) {
-    *reinterpret_cast<uint2*>(va) = *reinterpret_cast<const uint2*>(codes);
-    *reinterpret_cast<uint2*>(vb) = *reinterpret_cast<const uint2*>(codes + 4 * D);
-  } else {
-    va[0] = *reinterpret_cast<const uint32_t*>(codes);
-    vb[0] = *reinterpret_cast<const uint32_t*>(codes + 4 * D);
+struct ValueCodes {
+  static constexpr int N = D / 64;  // words of codes of one token pair
+  uint32_t a[N], b[N], sa, sb;
+  __device__ __forceinline__ void load(const unsigned char* blk, int g, int c, int h) {
+    const unsigned char* codes = blk + KvBlock<D>::kValCodes + c * D +
+                                 KvBlock<D>::kChunk * KvBlock<D>::place(c, g) + 4 * N * h;
+    const unsigned char* scales = blk + KvBlock<D>::kValScales + c * (D / 8) +
+                                  2 * (D == 128 ? g : g >> 1);
+    if (D == 128) {
+      *reinterpret_cast<uint2*>(a) = *reinterpret_cast<const uint2*>(codes);
+      *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(codes + 4 * D);
+    } else {
+      a[0] = *reinterpret_cast<const uint32_t*>(codes);
+      b[0] = *reinterpret_cast<const uint32_t*>(codes + 4 * D);
+    }
+    sa = *reinterpret_cast<const uint16_t*>(scales);
+    sb = *reinterpret_cast<const uint16_t*>(scales + D / 2);
   }
-  fa = *reinterpret_cast<const uint16_t*>(scales);
-  fb = *reinterpret_cast<const uint16_t*>(scales + D / 2);
-  if (masked) {
+  // A token that some row does not see must not reach it as 0 * NaN: its scale is taken as 0 where
+  // the cache holds nothing (past the length) or a NaN. Bit i of what is returned says that token
+  // i, which some rows see, has a NaN scale among this thread's values.
+  __device__ __forceinline__ uint32_t mask(int c, int t0, int len, int all_see) {
+    uint32_t nan_at = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = 2 * c + (k & 1) + 8 * (k >> 1), sh = 8 * (k & 1);
-      uint32_t& s = k < 2 ? fa : fb;
+      uint32_t& s = k < 2 ? sa : sb;
       const bool bad = ((s >> sh) & 0x7Fu) == 0x7Fu;
       if (t0 + i >= len || (bad && t0 + i >= all_see)) s &= ~(0xFFu << sh);
       if (bad && t0 + i < len && t0 + i >= all_see) nan_at |= 1u << i;
     }
+    return nan_at;
   }
-  fa = e4m3x2(fa);
-  fb = e4m3x2(fb);
+  __device__ __forceinline__ void operands(uint32_t (&f)[D / 32][4]) const {
+    const uint32_t fa = e4m3x2(sa), fb = e4m3x2(sb);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t x[4], y[4];
-    e2m1x8(va[i], x);
-    e2m1x8(vb[i], y);
+    for (int i = 0; i < N; ++i) {
+      uint32_t x[4], y[4];
+      e2m1x8(a[i], x);
+      e2m1x8(b[i], y);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      f[2 * i + n][0] = mul_f16x2(x[2 * n], fa);
-      f[2 * i + n][1] = mul_f16x2(x[2 * n + 1], fa);
-      f[2 * i + n][2] = mul_f16x2(y[2 * n], fb);
-      f[2 * i + n][3] = mul_f16x2(y[2 * n + 1], fb);
+      for (int n = 0; n < 2; ++n) {
+        f[2 * i + n][0] = mul_f16x2(x[2 * n], fa);
+        f[2 * i + n][1] = mul_f16x2(x[2 * n + 1], fa);
+        f[2 * i + n][2] = mul_f16x2(y[2 * n], fb);
+        f[2 * i + n][3] = mul_f16x2(y[2 * n + 1], fb);
+      }
     }
   }
-}
+};
 
 // Where a pair's producer looks up next.
 struct Producer {
@@ -474,6 +477,9 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           my_p[(h * NT + t) * 32 + lane] =
               make_uint2(transpose8x8(pack_f16(x[0], x[1])), transpose8x8(pack_f16(x[2], x[3])));
         }
+        ValueCodes<D> vc[NB];  // read ahead of the barrier
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vc[b].load(sb + b * S::kBlock, g, c, h);
         named_sync(1 + pair, 64);
 
         // this warp's half of the outputs, over all blocks
@@ -481,7 +487,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         for (int b = 0; b < NB; ++b) {
           if (masked && ((lost >> b) & 1u)) continue;  // nothing to add, or its rows are NaN already
           uint32_t nan_at = 0, vf[MH][4];
-          value_operands<D>(sb + b * S::kBlock, g, c, h, masked, t0 + 16 * b, len, all_see, vf, nan_at);
+          if (masked) nan_at = vc[b].mask(c, t0 + 16 * b, len, all_see);
+          vc[b].operands(vf);
 #pragma unroll
           for (int t = 0; t < TN; ++t) {
             const uint2 p = my_p[(b * NT + t) * 32 + lane];
@@ -612,17 +619,24 @@ cudaError_t launch_tiles(const AttnParams& P, int sms, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-constexpr int kMaxRows = 32;  // rows of a tile
+// Rows of a tile, at most. For D = 128 the kernel of sv_attn_tc.cu takes what has more: with 28 rows
+// a head it takes 156 us for 300001 tokens of 8 heads and 148 us for 64 sequences of up to 8192
+// tokens, this one 175 and 154; with 24 rows it takes 149 and 141 us, this one 134 and 111. It has
+// no form for D = 64.
+template <int D>
+constexpr int kMaxRows = D == 128 ? 24 : 32;
 
 template <int D>
-cudaError_t launch_dim(const AttnParams& P, int rows, int sms, cudaStream_t stream) {
-  switch ((rows + 7) / 8) {
-    case 0:
+cudaError_t launch_dim(const AttnParams& P, long long all, int sms, cudaStream_t stream) {
+  // rows of a tile: a sequence's rows in as few tiles as hold them, evenly
+  const long long tiles = (all + kMaxRows<D> - 1) / kMaxRows<D>;
+  switch (((all + tiles - 1) / tiles + 7) / 8) {
     case 1: return launch_tiles<D, 1>(P, sms, stream);
     case 2: return launch_tiles<D, 2>(P, sms, stream);
     case 3: return launch_tiles<D, 3>(P, sms, stream);
-    default: return launch_tiles<D, 4>(P, sms, stream);
   }
+  if constexpr (kMaxRows<D> > 24) return launch_tiles<D, 4>(P, sms, stream);
+  return cudaErrorInvalidValue;  // not reached
 }
 
 }  // namespace
@@ -632,17 +646,11 @@ size_t attention_workspace_bytes(int sms) {
   return kAttnHeader + static_cast<size_t>(sms) * 4 * kTcMaxRows * (128 + 2) * sizeof(float);
 }
 
-#ifndef TCROWS
-#define TCROWS 32
-#endif
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream) {
   const long long all = std::max(1LL, static_cast<long long>(max_new) * P.group);
-  if (D == 128 && all > TCROWS) return launch_attention_tc(P, sms, stream);
-  // rows of a tile: a sequence's rows in as few tiles as hold them, evenly
-  const long long tiles = (all + kMaxRows - 1) / kMaxRows;
-  const int rows = static_cast<int>((all + tiles - 1) / tiles);
-  return D == 128 ? launch_dim<128>(P, rows, sms, stream) : launch_dim<64>(P, rows, sms, stream);
+  if (D == 64) return launch_dim<64>(P, all, sms, stream);
+  return all <= kMaxRows<128> ? launch_dim<128>(P, all, sms, stream) : launch_attention_tc(P, sms, stream);
 }
 
 }  // namespace sv
