@@ -50,7 +50,9 @@ constexpr int kTcBlock = KvBlock<D>::kBytes;
 constexpr int kTcStage = 8 * kTcBlock;
 constexpr int kSlabV = 128 * 128;          // 128 values x 64 tokens of float16
 constexpr int kSlabR = kTcMaxRows * 128;   // rows x 64 values or tokens
-constexpr int kTcV = 2 * kSlabV, kTcQ = 2 * kSlabR, kTcP = 2 * kSlabR;  // each twice
+constexpr int kTcV = 2 * kSlabV, kTcQ = 2 * kSlabR;  // each twice
+constexpr int kTcP = 128 * 2 * kTcMaxRows;  // weights, 64 rows of a token side by side; twice
+static_assert(kTcMaxRows == 64, "a token's weights are a line of 128 bytes");
 constexpr int kTcSmem = 1024 + 2 * (kTcV + kTcQ + kTcP) + kTcStages * kTcStage;
 // tensor memory columns: keys and scores twice, outputs
 constexpr uint32_t kColK = 0, kColS = 128, kColO = 256, kTcCols = 512;
@@ -89,11 +91,6 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, ui
 
 // Stores at a register's address plus a constant.
 template <int off>
-__device__ __forceinline__ void st_shared_f16(uint32_t at, float x) {
-  asm volatile("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %2;\n\tst.shared.b16 [%0+%1], h;\n\t}" ::"r"(at),
-               "n"(off), "f"(x));
-}
-template <int off>
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0+%1], {%2, %3, %4, %5};" ::"r"(at), "n"(off), "r"(a), "r"(b), "r"(c),
                "r"(d));
@@ -127,16 +124,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t (&r)[32]) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t t, const float (&v)[8]) {
+__device__ __forceinline__ void tmem_st8(uint32_t t, const float2 (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
-               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
                : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 // Columns t and t + 32 and the seven after each: the row groups of this warp.
-__device__ __forceinline__ void tmem_ld_groups(uint32_t t, float (&v)[2][8]) {
+__device__ __forceinline__ void tmem_ld_groups(uint32_t t, float2 (&v)[2][4]) {
   uint32_t r[16];
   asm volatile(
       "{\n\t"
@@ -151,7 +148,29 @@ __device__ __forceinline__ void tmem_ld_groups(uint32_t t, float (&v)[2][8]) {
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[k][j] = __uint_as_float(r[8 * k + j]);
+    for (int j = 0; j < 4; ++j)
+      v[k][j] = make_float2(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+}
+
+// Two floats at a time
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -191,7 +210,7 @@ struct TcShared {
   long long scan[kTcWarps];
   alignas(16) float qc[2][kTcMaxRows];  // per row: score of a product of the operands
   int vis[2][kTcMaxRows];         // tokens that it sees
-  alignas(16) float m[kTcMaxRows];  // running maxima
+  alignas(16) float nm[kTcMaxRows];  // running maxima, negated
   float down[kTcMaxRows];
   float part[4][kTcMaxRows];      // per quarter of a tile's tokens: maxima, sums
   long long at[kTcMaxRows];       // where a row's results go
@@ -200,7 +219,7 @@ struct TcShared {
   int last;
 };
 
-static_assert(offsetof(TcShared, qc) % 16 == 0 && offsetof(TcShared, m) % 16 == 0, "read as float4");
+static_assert(offsetof(TcShared, qc) % 16 == 0 && offsetof(TcShared, nm) % 16 == 0, "read as float4");
 
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   constexpr int R = kTcMaxRows;
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           tc_mma_ss(tmem + kColO, a + (((kk >> 2) * kSlabV + 32 * (kk & 3)) >> 4),
-                    p + (((kk >> 2) * kSlabR + 32 * (kk & 3)) >> 4), pv_idesc, !pv_first || kk > 0);
+                    p + ((kk * 16 * 128) >> 4), pv_idesc, !pv_first || kk > 0);
         tc_commit(&S.pv_done[b]);
       }
       __syncwarp();
@@ -356,7 +375,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         }
         __syncwarp();
         if (t > 0) outputs(t - 1);
-        pv_idesc = idesc;
+        pv_idesc = idesc | (1u << 16);  // weights lie token by token
         pv_first = first;
       }
       if (t < tiles) next_item<R, kTcUnit>(P, w);
@@ -535,18 +554,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
     const int wid = tid - 32 * kWarpWeights, hh = wid >> 7, hid = wid & 127;
     const int q = warp & 3, tok = 32 * q + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>(q) << 21);
-    const uint32_t p_to = smem_u32(sp) + (tok >> 6) * kSlabR + 2 * (tok & 7) + (((tok & 63) >> 3) << 4) + hh * 1024;
+    // 8 rows of a token are 16 bytes, in the 128-byte swizzle; the other 8 lie 64 bytes away
+    const uint32_t p_to = smem_u32(sp) + tok * 128 + ((hh ^ (tok & 7)) << 4);
     const int my_row = 8 * (4 * (hid >> 3) + hh) + (hid & 7);  // hid < 16: a row of this quarter
     const int lane_row = 8 * (4 * (lane >> 3) + hh) + (lane & 7);  // lane < 16
     int t = 0;
     for (int item = 0; t < tiles; ++item) {
       const int end = item_end(), rows = min(R, w.n * P.group - w.rt * R), qb = item & 1;
-      if (hid < 16) S.m[my_row] = -FLT_MAX;
+      if (hid < 16) S.nm[my_row] = FLT_MAX;
       wait_warp(&S.q_full[qb], item >> 1);
       named_sync(1 + hh, 128);
       const int all_see = S.vis[qb][0];
       const float4* qc4 = reinterpret_cast<const float4*>(S.qc[qb] + 8 * hh);  // groups of 8 rows, 32 apart
-      const float4* m4 = reinterpret_cast<const float4*>(S.m + 8 * hh);
+      const float4* nm4 = reinterpret_cast<const float4*>(S.nm + 8 * hh);
       // Rows that see a NaN value get NaN in its 16 values at the item's end: of tile i (unit u of the
       // item), a bit a row. What the values' warps left for it is there once its products are done,
       // and stays until four tiles later.
@@ -566,115 +586,119 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         return hits;
       };
       uint32_t poison = 0, past = 0;  // such rows; a bit a tile of the item: masked, the last one lowest
-      float l[2][8];  // sums of this token's weights
+      float2 l[2][4];  // sums of this token's weights
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) l[k][j] = 0.f;
+        for (int j = 0; j < 4; ++j) l[k][j] = make_float2(0.f, 0.f);
       for (bool first = true; unit < end; ++unit, ++t, first = false) {
         const int b = t & 1, t0 = unit * kTcUnit;
         wait_warp(&S.s_full[b], t >> 1);
         tc_fence_after();
-        float z[2][8];
-        tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
         const uint32_t lost = S.lost[t & 15];
         const bool masked = t0 + kTcUnit > all_see || lost;
         if (past & 2u) poison |= nan_rows(t - 2, unit - 2);
         past = (past << 1) | (masked ? 1u : 0u);
-        float top = -INFINITY;
+        // Scores less their rows' maxima. If one of them is too large they are read once more, and
+        // the maxima are moved.
+        float2 z[2][4];
+        for (bool move = false;;) {
+          tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r0 = 8 * (4 * k + hh);
-          if (r0 >= rows) break;
-          const float4 a = qc4[8 * k], c = qc4[8 * k + 1];
-          // rounded before the maximum is taken
-          z[k][0] = __fmul_rn(z[k][0], a.x);
-          z[k][1] = __fmul_rn(z[k][1], a.y);
-          z[k][2] = __fmul_rn(z[k][2], a.z);
-          z[k][3] = __fmul_rn(z[k][3], a.w);
-          z[k][4] = __fmul_rn(z[k][4], c.x);
-          z[k][5] = __fmul_rn(z[k][5], c.y);
-          z[k][6] = __fmul_rn(z[k][6], c.z);
-          z[k][7] = __fmul_rn(z[k][7], c.w);
-        }
-        if (masked) {
+          for (int k = 0; k < 2; ++k) {
+            if (8 * (4 * k + hh) >= rows) break;
+            const float4 a = qc4[8 * k], c = qc4[8 * k + 1];
+            // rounded before the maximum is taken
+            z[k][0] = mul2(z[k][0], make_float2(a.x, a.y));
+            z[k][1] = mul2(z[k][1], make_float2(a.z, a.w));
+            z[k][2] = mul2(z[k][2], make_float2(c.x, c.y));
+            z[k][3] = mul2(z[k][3], make_float2(c.z, c.w));
+          }
+          if (masked) {
+            const bool here = !((lost >> (tok >> 4)) & 1u);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int r = 8 * (4 * k + hh) + j;
-              if (r < rows && t0 + tok >= S.vis[qb][r])
-                z[k][j] = -INFINITY;
-              else if ((lost >> (tok >> 4)) & 1u)
-                z[k][j] = NAN;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r0 = 8 * (4 * k + hh);
-          if (r0 >= rows) break;
-          const float4 a = m4[8 * k], c = m4[8 * k + 1];
-          top = fmaxf(top, fmaxf(fmaxf(fmaxf(z[k][0] - a.x, z[k][1] - a.y), fmaxf(z[k][2] - a.z, z[k][3] - a.w)),
-                                 fmaxf(fmaxf(z[k][4] - c.x, z[k][5] - c.y), fmaxf(z[k][6] - c.z, z[k][7] - c.w))));
-        }
-        if (named_sync_or(1 + hh, 128, top > kSlack)) {  // a new maximum of some row
-          float y = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (8 * (4 * k + hh) < rows) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float x = warp_max(z[k][j]);
-                if (lane == 8 * k + j) y = x;
+              for (int j = 0; j < 4; ++j) {
+                const int r = 8 * (4 * k + hh) + 2 * j;
+                if (r < rows && t0 + tok >= S.vis[qb][r]) z[k][j].x = -INFINITY;
+                else if (!here) z[k][j].x = NAN;
+                if (r + 1 < rows && t0 + tok >= S.vis[qb][r + 1]) z[k][j].y = -INFINITY;
+                else if (!here) z[k][j].y = NAN;
               }
-            }
-          if (lane < 16) S.part[q][lane_row] = y;
-          named_sync(1 + hh, 128);
-          if (hid < 16) {
-            const float old = S.m[my_row];
-            y = fmaxf(fmaxf(S.part[0][my_row], S.part[1][my_row]),
-                      fmaxf(S.part[2][my_row], S.part[3][my_row]));
-            const float now = fmaxf(old, y - kLift);
-            S.down[my_row] = ex2_fast(old - now);
-            S.m[my_row] = now;
           }
-          named_sync(1 + hh, 128);
+          if (move) {
+            float y = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
+              if (8 * (4 * k + hh) < rows) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) l[k][j] *= S.down[8 * (4 * k + hh) + j];
-          if (!first) {
-            wait_warp(&S.pv_done[(t - 1) & 1], (t - 1) >> 1);
-            tc_fence_after();
-            float o[2][8];
-            tmem_ld_groups(mine + kColO + 8 * hh, o);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int r0 = 8 * (4 * k + hh);
-              if (r0 >= rows) break;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[k][j] *= S.down[r0 + j];
-              tmem_st8(mine + kColO + r0, o[k]);
+                for (int j = 0; j < 4; ++j) {
+                  const float x0 = warp_max(z[k][j].x), x1 = warp_max(z[k][j].y);
+                  if (lane == 8 * k + 2 * j) y = x0;
+                  if (lane == 8 * k + 2 * j + 1) y = x1;
+                }
+              }
+            if (lane < 16) S.part[q][lane_row] = y;
+            named_sync(1 + hh, 128);
+            if (hid < 16) {
+              const float old = -S.nm[my_row];
+              y = fmaxf(fmaxf(S.part[0][my_row], S.part[1][my_row]),
+                        fmaxf(S.part[2][my_row], S.part[3][my_row]));
+              const float now = fmaxf(old, y - kLift);
+              S.down[my_row] = ex2_fast(old - now);
+              S.nm[my_row] = -now;
             }
-            tmem_wait_st();
+            named_sync(1 + hh, 128);
+            const float2* down2 = reinterpret_cast<const float2*>(S.down + 8 * hh);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) l[k][j] = mul2(l[k][j], down2[16 * k + j]);
+            if (!first) {
+              wait_warp(&S.pv_done[(t - 1) & 1], (t - 1) >> 1);
+              tc_fence_after();
+              float2 o[2][4];
+              tmem_ld_groups(mine + kColO + 8 * hh, o);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int r0 = 8 * (4 * k + hh);
+                if (r0 >= rows) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[k][j] = mul2(o[k][j], down2[16 * k + j]);
+                tmem_st8(mine + kColO + r0, o[k]);
+              }
+              tmem_wait_st();
+            }
           }
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (8 * (4 * k + hh) >= rows) break;
+            const float4 a = nm4[8 * k], c = nm4[8 * k + 1];
+            z[k][0] = add2(z[k][0], make_float2(a.x, a.y));
+            z[k][1] = add2(z[k][1], make_float2(a.z, a.w));
+            z[k][2] = add2(z[k][2], make_float2(c.x, c.y));
+            z[k][3] = add2(z[k][3], make_float2(c.z, c.w));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max3(top, z[k][j].x, z[k][j].y);
+          }
+          if (move || !named_sync_or(1 + hh, 128, top > kSlack)) break;
+          move = true;
         }
         // the products that read this buffer last were issued before these scores'
-        const uint32_t dst = p_to + b * kTcP;
-        each(Upto<2>(), [&](auto k_) {
-          constexpr int k = decltype(k_)::value;
-          const int r0 = 8 * (4 * k + hh);
-          if (r0 >= rows) return;
-          const float4 a = m4[8 * k], c = m4[8 * k + 1];
-          each(Upto<8>(), [&](auto j_) {
-            constexpr int j = decltype(j_)::value;
-            const float m = j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w
-                          : j == 4 ? c.x : j == 5 ? c.y : j == 6 ? c.z : c.w;
-            const float p = ex2_fast(z[k][j] - m);
-            l[k][j] += p;
-            st_shared_f16<(32 * k + j) * 128>(dst ^ (j << 4), p);
-          });
-        });
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (8 * (4 * k + hh) >= rows) break;
+          uint32_t p16[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 p = make_float2(ex2_fast(z[k][j].x), ex2_fast(z[k][j].y));
+            l[k][j] = add2(l[k][j], p);
+            p16[j] = pack_f16(p.x, p.y);
+          }
+          st_shared_v4<0>((p_to + b * kTcP) ^ (64 * k), p16[0], p16[1], p16[2], p16[3]);
+        }
         fence_proxy_async();
         tc_fence_before();
         arrive_warp(&S.vp_full[b]);
@@ -683,9 +707,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       // the item's results, or this piece of them
       wait_warp(&S.pv_done[(t - 1) & 1], (t - 1) >> 1);
       tc_fence_after();
-      float o[2][8];
-      tmem_ld_groups(mine + kColO + 8 * hh, o);
+      float2 o2[2][4];
+      tmem_ld_groups(mine + kColO + 8 * hh, o2);
       tc_fence_before();
+      float o[2][8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[k][j] = j & 1 ? o2[k][j >> 1].y : o2[k][j >> 1].x;
       if (past & 2u) poison |= nan_rows(t - 2, end - 2);
       if (past & 1u) poison |= nan_rows(t - 1, end - 1);
       if (poison) {
@@ -701,7 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * k + j] = l[k][j];
+          for (int j = 0; j < 8; ++j) v[8 * k + j] = j & 1 ? l[k][j >> 1].y : l[k][j >> 1].x;
         const float sum = warp_sums(v, lane);
         if (lane < 16) S.part[q][lane_row] = sum;
       }
@@ -714,11 +743,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
           const long long at = out_row(P, w, R, my_row);
           S.at[my_row] = at * D;
           S.down[my_row] = L == 0.f ? 0.f : P.vs / L;
-          store_lse(P, at, S.m[my_row], L);
+          store_lse(P, at, -S.nm[my_row], L);
         } else {
           S.at[my_row] = my_row * D;
           S.down[my_row] = 1.f;
-          part[R * D + my_row] = S.m[my_row];
+          part[R * D + my_row] = -S.nm[my_row];
           part[R * D + R + my_row] = L;
         }
       }
