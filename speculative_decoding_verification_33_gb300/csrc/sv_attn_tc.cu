@@ -39,10 +39,10 @@ namespace sv {
 namespace {
 
 constexpr int D = 128;
-// warps: copies, products, keys (4), values (4), weights (4 x 4); the warps that reach tensor
+// warps: copies, products, keys (4), values (4), weights (4 x 4), items; the warps that reach tensor
 // memory come in fours, since a warp reaches the lanes of its index modulo 4
-constexpr int kWarpKeys = 2, kWarpValues = 6, kWarpWeights = 10, kTcWarps = 26;
-constexpr int kTcWThreads = 32 * (kTcWarps - kWarpWeights);
+constexpr int kWarpKeys = 2, kWarpValues = 6, kWarpWeights = 10, kWarpItems = 26, kTcWarps = 27;
+constexpr int kTcWThreads = 32 * (kWarpItems - kWarpWeights);
 constexpr int kTcThreads = 32 * kTcWarps;
 constexpr int kTcUnit = 128;   // tokens
 constexpr int kTcStages = 4;   // tiles of the cache's bytes on their way
@@ -193,6 +193,15 @@ __device__ __forceinline__ float warp_sums(float (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
 }
 
+// An item of the run, or the part of it that the run has: its units unit .. end - 1.
+struct TcItem {
+  Walk w;
+  long long out0;  // the output's row that S.at counts from
+  int unit, end, rows;
+  int all_see;     // tokens that every row sees
+  bool whole;
+};
+
 // What the roles share. Tile t uses buffer t & 1 of everything that is held twice.
 struct TcShared {
   uint64_t raw_full[kTcStages], raw_empty[kTcStages];  // the cache's bytes
@@ -202,6 +211,8 @@ struct TcShared {
   uint64_t vp_full[2];            // values unpacked and weights there (and the scores read)
   uint64_t pv_done[2];            // values and weights spent, outputs up to date
   uint64_t q_full[2], q_empty[2];  // queries of an item, twice as well
+  uint64_t item_full[4];           // the item itself
+  TcItem items[4];
   uint64_t end;
   uint32_t tmem;
   uint32_t lost[16];              // per tile modulo 16: blocks that are not there
@@ -211,15 +222,16 @@ struct TcShared {
   alignas(16) float qc[2][kTcMaxRows];  // per row: score of a product of the operands
   int vis[2][kTcMaxRows];         // tokens that it sees
   alignas(16) float nm[kTcMaxRows];  // running maxima, negated
-  float down[kTcMaxRows];
+  alignas(16) float down[kTcMaxRows];
   float part[4][kTcMaxRows];      // per quarter of a tile's tokens: maxima, sums
-  long long at[kTcMaxRows];       // where a row's results go
+  alignas(16) int at[4][kTcMaxRows];  // its row of the output, from the item's first (of four items)
   uint32_t nan[4][8][4];          // per tile modulo 4 and 16 values: tokens with a NaN scale
   int nans[4];                    // the tile that this speaks of, plus one
   int last;
 };
 
-static_assert(offsetof(TcShared, qc) % 16 == 0 && offsetof(TcShared, nm) % 16 == 0, "read as float4");
+static_assert(offsetof(TcShared, qc) % 16 == 0 && offsetof(TcShared, at) % 16 == 0 &&
+                  offsetof(TcShared, down) % 16 == 0 && offsetof(TcShared, nm) % 16 == 0, "read as float4");
 
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   constexpr int R = kTcMaxRows;
@@ -246,6 +258,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       mbar_init(&S.q_empty[i], 16);
     }
     mbar_init(&S.end, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.item_full[i], 1);
+      S.items[i] = TcItem{};  // what a role reads that gave up waiting: it goes on to its end
+      S.items[i].end = S.items[i].rows = 1;
+    }
     fence_mbar_init();
     for (int i = 0; i < 4; ++i) S.nans[i] = 0;
   }
@@ -255,10 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem;
-  const long long u0 = S.run.u0, u1 = S.run.u1;
-  const int tiles = static_cast<int>(u1 - u0);
-  Walk w = S.first;
-  int unit = static_cast<int>(u0 - w.base);
+  const int tiles = static_cast<int>(S.run.u1 - S.run.u0);
   // Every wait has a limit. A role that met it waits no more and runs through to its end, so that
   // nobody waits for it for good; what comes out is not used.
   int tries = kWaitTries;
@@ -279,13 +293,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  auto item_end = [&]() { return static_cast<int>(min(static_cast<long long>(w.nu), u1 - w.base)); };
 
   if (warp == 0) {
     // ---- copies. Where the blocks lie is looked up four tiles at a time, a lane a block, and a
     // round before it is needed, so that no copy waits for a page number.
     const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
     const int mine = lane >> 3, block = lane & 7;
+    Walk w = S.first;
+    int unit = static_cast<int>(S.run.u0 - w.base);
     int issued = 0, next_at = 0;
     int next_page = -1;
     unit += mine;  // of this lane's tile
@@ -354,14 +369,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       __syncwarp();
     };
     for (int item = 0; t < tiles; ++item) {
-      const int end = item_end();
-      const int rows = min(R, w.n * P.group - w.rt * R);
+      // the last item's outputs do not wait for queries
+      bool late = t > 0 && !mbar_test(&S.q_full[item & 1], (item >> 1) & 1);
+      if (__any_sync(0xFFFFFFFFu, late)) {
+        outputs(t - 1);
+        late = true;
+      }
+      wait_warp(&S.q_full[item & 1], item >> 1);
+      const int end = S.items[item & 3].end, rows = S.items[item & 3].rows;
       // float16 operands, float32 sums, 128 x (rows to a multiple of 16)
       idesc = (1u << 4) | (static_cast<uint32_t>((rows + 15) / 16 * 2) << 17) |
               (static_cast<uint32_t>(128 >> 4) << 24);
       const uint32_t q = a_q + (item & 1) * (kTcQ >> 4);
-      wait_warp(&S.q_full[item & 1], item >> 1);
-      for (bool first = true; unit < end; ++unit, ++t, first = false) {
+      bool first = true;
+      for (int unit = S.items[item & 3].unit; unit < end; ++unit, ++t, first = false) {
         const int b = t & 1;
         // the scores of tile t - 2 have been read: its weights were there
         wait_warp(&S.k_full[b], t >> 1);
@@ -374,14 +395,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
           tc_commit(&S.s_full[b]);
         }
         __syncwarp();
-        if (t > 0) outputs(t - 1);
+        if (t > 0 && !(first && late)) outputs(t - 1);
         pv_idesc = idesc | (1u << 16);  // weights lie token by token
         pv_first = first;
       }
-      if (t < tiles) next_item<R, kTcUnit>(P, w);
-      unit = 0;
     }
-    outputs(tiles - 1);
+    outputs(t - 1);
     // all products are done before the memory goes
     if (elect_one()) tc_commit(&S.end);
     __syncwarp();
@@ -393,7 +412,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
     const uint32_t to = tmem + (static_cast<uint32_t>(q) << 21) + kColK;
     int t = 0;
     for (int item = 0; t < tiles; ++item) {
-      const int end = item_end(), rows = min(R, w.n * P.group - w.rt * R), qb = item & 1;
+      wait_warp(&S.item_full[item & 3], item >> 2);
+      const TcItem& it = S.items[item & 3];
+      const Walk& w = it.w;
+      const int end = it.end, rows = it.rows, qb = item & 1, row0 = w.rt * R, i0 = row0 / P.group;
       // queries in rows of 64 values (128 bytes), in the 128-byte swizzle
       uint4 raw[QPER];
 #pragma unroll
@@ -407,7 +429,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
                                                         static_cast<long long>(head) * D) + kid % QV);
         }
       }
-      if (item >= 2) wait_warp(&S.q_empty[qb], (item >> 1) - 1);
 #pragma unroll
       for (int n = 0; n < QPER; ++n) {
         if (8 * n >= rows) break;
@@ -419,7 +440,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         float undo;
         const float up = query_scale(most, P.c, &undo);
         if (j == 0) {
-          S.vis[qb][r] = w.len - w.n + (w.rt * R + min(r, rows - 1)) / P.group + 1;
+          const int row = row0 + min(r, rows - 1), i = row / P.group;
+          S.vis[qb][r] = w.len - w.n + i + 1;
+          S.at[item & 3][r] = (i - i0) * P.hq + row - i * P.group;
           S.qc[qb][r] = undo;
         }
         uint32_t f[4];
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       }
       fence_proxy_async();
       arrive_warp(&S.q_full[qb]);
-      for (; unit < end; ++unit, ++t) {
+      for (int unit = it.unit; unit < end; ++unit, ++t) {
         const int stage = t % kTcStages, b = t & 1;
         wait_warp(&S.raw_full[stage], t / kTcStages);
         const unsigned char* blk = ring + stage * kTcStage + (tok >> 4) * kTcBlock;
@@ -474,8 +497,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         tc_fence_before();
         arrive_warp(&S.k_full[b]);
       }
-      if (t < tiles) next_item<R, kTcUnit>(P, w);
-      unit = 0;
     }
   } else if (warp < kWarpWeights) {
     // ---- values: a thread 16 values (a scale's) of 8 tokens. Codes: 8 threads side by side read a
@@ -488,9 +509,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
     const uint32_t v_to = smem_u32(sval) + (vt >> 3) * kSlabV + 16 * vg * 128 + ((vt & 7) << 4);
     int t = 0;
     for (int item = 0; t < tiles; ++item) {
-      const int end = item_end(), len = w.len;
-      const int all_see = w.len - w.n + w.rt * R / P.group + 1;  // tokens that every row sees
-      for (; unit < end; ++unit, ++t) {
+      wait_warp(&S.item_full[item & 3], item >> 2);
+      const int end = S.items[item & 3].end, len = S.items[item & 3].w.len;
+      const int all_see = S.items[item & 3].all_see;
+      for (int unit = S.items[item & 3].unit; unit < end; ++unit, ++t) {
         const int stage = t % kTcStages, b = t & 1, t0 = unit * kTcUnit;
         wait_warp(&S.raw_full[stage], t / kTcStages);
         const unsigned char* src = ring + stage * kTcStage;
@@ -546,8 +568,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         fence_proxy_async();
         arrive_warp(&S.vp_full[b]);
       }
-      if (t < tiles) next_item<R, kTcUnit>(P, w);
-      unit = 0;
+    }
+  } else if (warp == kWarpItems) {
+    // ---- items: one thread walks through them, ahead of all others, so that nobody waits for a
+    // sequence's lengths. An item takes the place of the fourth before it, which nobody reads any
+    // more once the weights of the second before it are done.
+    if (lane == 0) {
+      Walk w = S.first;
+      int unit = static_cast<int>(S.run.u0 - w.base), t = 0;
+      for (int item = 0;; ++item) {
+        if (item >= 2) wait(&S.q_empty[item & 1], (item >> 1) - 1);
+        TcItem& it = S.items[item & 3];
+        it.w = w;
+        it.unit = unit;
+        it.end = static_cast<int>(min(static_cast<long long>(w.nu), S.run.u1 - w.base));
+        it.rows = min(R, w.n * P.group - w.rt * R);
+        const int i0 = w.rt * R / P.group;
+        it.all_see = w.len - w.n + i0 + 1;
+        it.out0 = static_cast<long long>(w.r0 + i0) * P.hq + w.h * P.group;
+        it.whole = w.base >= S.run.u0 && it.end == w.nu;
+        mbar_arrive(&S.item_full[item & 3]);
+        t += it.end - unit;
+        if (t >= tiles) break;
+        next_item<R, kTcUnit>(P, w);
+        unit = 0;
+      }
     }
   } else {
     // ---- weights: a thread a token, a quarter of the rows: 8 (4 k + hh) + j
@@ -560,11 +605,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
     const int lane_row = 8 * (4 * (lane >> 3) + hh) + (lane & 7);  // lane < 16
     int t = 0;
     for (int item = 0; t < tiles; ++item) {
-      const int end = item_end(), rows = min(R, w.n * P.group - w.rt * R), qb = item & 1;
+      const int qb = item & 1;
       if (hid < 16) S.nm[my_row] = FLT_MAX;
       wait_warp(&S.q_full[qb], item >> 1);
       named_sync(1 + hh, 128);
-      const int all_see = S.vis[qb][0];
+      const TcItem& it = S.items[item & 3];
+      const int end = it.end, rows = it.rows, all_see = it.all_see;
       const float4* qc4 = reinterpret_cast<const float4*>(S.qc[qb] + 8 * hh);  // groups of 8 rows, 32 apart
       const float4* nm4 = reinterpret_cast<const float4*>(S.nm + 8 * hh);
       // Rows that see a NaN value get NaN in its 16 values at the item's end: of tile i (unit u of the
@@ -591,7 +637,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) l[k][j] = make_float2(0.f, 0.f);
-      for (bool first = true; unit < end; ++unit, ++t, first = false) {
+      bool first = true;
+      for (int unit = it.unit; unit < end; ++unit, ++t, first = false) {
         const int b = t & 1, t0 = unit * kTcUnit;
         wait_warp(&S.s_full[b], t >> 1);
         tc_fence_after();
@@ -600,9 +647,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         if (past & 2u) poison |= nan_rows(t - 2, unit - 2);
         past = (past << 1) | (masked ? 1u : 0u);
         // Scores less their rows' maxima. If one of them is too large they are read once more, and
-        // the maxima are moved.
+        // the maxima are moved, as an item's first are in any case.
         float2 z[2][4];
-        for (bool move = false;;) {
+        for (bool move = first;;) {
           tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -735,41 +782,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         if (lane < 16) S.part[q][lane_row] = sum;
       }
       named_sync(1 + hh, 128);
-      const bool whole = w.base >= u0 && end == w.nu;
-      float* part = P.part + static_cast<long long>(2 * blockIdx.x + (w.base <= u0 ? 0 : 1)) * kTcPart;
-      if (hid < 16 && my_row < rows) {  // a thread a row: its sum, its place, its factor
+      const bool whole = it.whole;
+      float* part = P.part + static_cast<long long>(2 * blockIdx.x + (it.w.base <= S.run.u0 ? 0 : 1)) * kTcPart;
+      if (hid < 16 && my_row < rows) {  // a thread a row: its sum, its factor
         const float L = S.part[0][my_row] + S.part[1][my_row] + S.part[2][my_row] + S.part[3][my_row];
         if (whole) {
-          const long long at = out_row(P, w, R, my_row);
-          S.at[my_row] = at * D;
           S.down[my_row] = L == 0.f ? 0.f : P.vs / L;
-          store_lse(P, at, -S.nm[my_row], L);
+          store_lse(P, it.out0 + S.at[item & 3][my_row], -S.nm[my_row], L);
         } else {
-          S.at[my_row] = my_row * D;
-          S.down[my_row] = 1.f;
           part[R * D + my_row] = -S.nm[my_row];
           part[R * D + R + my_row] = L;
         }
       }
       named_sync(1 + hh, 128);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.out) + it.out0 * D + tok;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+        const int r0 = 8 * (4 * k + hh);
+        if (r0 >= rows) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 8 * (4 * k + hh) + j;
+        for (int n = 0; n < 2; ++n) {
+          const int r = r0 + 4 * n;
           if (r >= rows) break;
-          const float x = o[k][j] * S.down[r];
-          if (whole)
-            static_cast<__nv_bfloat16*>(P.out)[S.at[r] + tok] = __float2bfloat16_rn(x);
-          else
-            part[S.at[r] + tok] = x;
+          const float* x = o[k] + 4 * n;
+          if (whole) {
+            const float4 f = *reinterpret_cast<const float4*>(S.down + r);
+            const int4 at = *reinterpret_cast<const int4*>(S.at[item & 3] + r);
+            out[static_cast<long long>(at.x) * D] = __float2bfloat16_rn(x[0] * f.x);
+            if (r + 1 < rows) out[static_cast<long long>(at.y) * D] = __float2bfloat16_rn(x[1] * f.y);
+            if (r + 2 < rows) out[static_cast<long long>(at.z) * D] = __float2bfloat16_rn(x[2] * f.z);
+            if (r + 3 < rows) out[static_cast<long long>(at.w) * D] = __float2bfloat16_rn(x[3] * f.w);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part[(r + j) * D + tok] = x[j];
+          }
         }
       }
       if (!whole)
-        join_pieces<kTcWThreads, R, D, 4>(P, w, S.run, rows, wid, &S.last, [] { named_sync(6, kTcWThreads); });
+        join_pieces<kTcWThreads, R, D, 4>(P, it.w, S.run, rows, wid, &S.last, [] { named_sync(6, kTcWThreads); });
       named_sync(1 + hh, 128);  // maxima and sums may change
-      if (t < tiles) next_item<R, kTcUnit>(P, w);
-      unit = 0;
     }
   }
   if (tries <= 0) atomicOr(P.err, 1u);
