@@ -47,6 +47,18 @@ struct AttnShape {
   static constexpr int kPerSm = 2;
   static constexpr int kRows = 8 * NT;
   static constexpr int kUnit = 32;  // tokens: a block for each warp of a pair
+  // Work as it is cut: 524301 tokens of 8 heads take 134, 166, 215 and 280 us with 1 to 4 tiles. With
+  // an item's start and end for nothing, 64 sequences of up to 8192 tokens, 24 rows a head, take
+  // 113 us and 256 of up to 1024 tokens 135 us; for 96, 88 and 86 us.
+  static constexpr int kDearest = NT == 1 ? 5 : NT == 2 ? 6 : NT == 3 ? 8 : 10;
+  static constexpr int kOver = 96;
+  // Every pair of a CTA gets three units or so at least: with one, more pieces are to be joined, and
+  // one request of 4000 tokens, 24 rows a head, takes 21.9 us instead of 17.6
+  static constexpr int kLeast = 3 * kPairs;
+  static __device__ __forceinline__ int weight(int rows) {
+    const int tiles = NT == 1 ? 1 : max((rows + 7) >> 3, NT - 1 > 2 ? 2 : NT - 1);
+    return tiles <= 1 ? 5 : tiles == 2 ? 6 : tiles == 3 ? 8 : 10;
+  }
   static constexpr int kBlock = KvBlock<D>::kBytes;
   static constexpr int kStage = 2 * kBlock;
   static constexpr int kStages = 3 * (128 / D);
@@ -200,7 +212,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   float* sqc = reinterpret_cast<float*>(svis + R);      // [R] score of a product of the operands
   uint64_t* bars = reinterpret_cast<uint64_t*>(sqc + R);
   uint32_t* slost = reinterpret_cast<uint32_t*>(bars + NP * NS);  // per stage: blocks not there
-  __shared__ long long s_scan[2 * NP];
+  __shared__ longlong2 s_scan[2 * NP];
   __shared__ Run s_run;
   __shared__ Walk s_walk[2];
   __shared__ Producer s_prod[NP];
@@ -214,9 +226,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     fence_mbar_init();
   }
 
-  // This CTA's run of units. Every pair of a CTA gets two units at least: with one, more pieces are
-  // to be joined, and one request of 4097 tokens takes 15.8 us instead of 14.5
-  if (!find_run<S::kThreads, R, UNIT>(P, 2 * NP, s_scan, &s_run, &s_walk[0])) return;
+  if (!find_run<S::kThreads, S>(P, s_scan, &s_run, &s_walk[0])) return;
   if (tid < NP) {
     s_prod[tid].w = s_walk[0];
     s_prod[tid].u = s_run.u0 + tid;
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
 #pragma unroll
     for (int i = 0; i < NB; ++i) off[i] = -1;
     if (u < u1) {
-      while (u >= w.base + w.nu) next_item<R, UNIT>(P, w);
+      while (u >= w.base + w.nu) next_item<S>(P, w);
       const int blk = NB * static_cast<int>(u - w.base);
       const int32_t* row = P.table + static_cast<long long>(w.b) * P.max_blocks;
 #pragma unroll
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     store_q(w);
     if (tid == 0) {
       Walk nw = w;
-      next_item<R, UNIT>(P, nw);
+      next_item<S>(P, nw);
       s_walk[item ^ 1] = nw;
     }
     __syncthreads();
@@ -542,8 +552,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       }
     unit -= w.nu;  // in the next item
     const bool whole = w.base >= s_run.u0 && end == w.nu;
-    // a piece's place: a CTA has at most two, one from its start and one to its end
-    const int my_slot = 2 * blockIdx.x + (w.base <= s_run.u0 ? 0 : 1);
+    const int my_slot = 2 * blockIdx.x + (w.base < s_run.u0 ? 0 : 1);
     float* my_part = P.part + static_cast<long long>(my_slot) * S::kPart;
     __syncthreads();
     const bool more = w.base + w.nu < s_run.u1;

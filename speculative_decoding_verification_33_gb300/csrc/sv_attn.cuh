@@ -19,16 +19,22 @@ constexpr long long kWaitCycles = 4000000000LL;  // about 2 s: a copy that never
 constexpr float kLift = 7.f;    // weights are held times 2^7: float16 has more room above 1 than below
 constexpr float kSlack = 15.f;  // and may grow to 2^15 before the running maximum is moved
 
+// Work is cut by what it is estimated to cost, in the cost of small parts of a unit. A kernel says
+// (class W) how many rows a tile and tokens a unit have, what a unit costs for a tile of so many
+// rows, and what an item's start and end cost together; that is counted behind its last unit.
+//
 // Where a run of units lies: item (sequence b, head h, row tile rt) with its nu units.
 struct Walk {
   long long base;  // the item's first unit
+  long long cost;  // of all that comes before
   int b, h, rt;
   int rts, nu, len, n, r0;
+  int wt;          // cost of a unit
   int past;        // cu_new[b + 1]
   int len1, past1;  // lengths of sequence b + 1: loaded with sequence b, used after it
 };
 
-template <int R, int UNIT>
+template <class W>
 __device__ __forceinline__ void set_seq(const AttnParams& P, int b, int first, int past, int len,
                                         Walk& w) {
   const int c0 = min(max(first, 0), P.T), c1 = min(max(past, c0), P.T);
@@ -37,23 +43,26 @@ __device__ __forceinline__ void set_seq(const AttnParams& P, int b, int first, i
   w.n = c1 - c0;
   w.past = past;
   w.len = min(max(len, 0), P.max_blocks * P.ps);
-  w.rts = (w.n * P.group + R - 1) / R;
-  w.nu = max(1, (w.len + UNIT - 1) / UNIT);
+  w.rts = (w.n * P.group + W::kRows - 1) / W::kRows;
+  w.nu = max(1, (w.len + W::kUnit - 1) / W::kUnit);
+  w.wt = W::weight(min(W::kRows, w.n * P.group));
 }
-template <int R, int UNIT>
+template <class W>
 __device__ __forceinline__ void load_seq(const AttnParams& P, int b, Walk& w) {
-  set_seq<R, UNIT>(P, b, P.cu[b], P.cu[b + 1], P.lens[b], w);
+  set_seq<W>(P, b, P.cu[b], P.cu[b + 1], P.lens[b], w);
 }
 __device__ __forceinline__ void load_ahead(const AttnParams& P, Walk& w) {
   w.len1 = P.lens[min(w.b + 1, P.B - 1)];
   w.past1 = P.cu[min(w.b + 2, P.B)];
 }
-__device__ __forceinline__ long long seq_units(const AttnParams& P, const Walk& w) {
-  return static_cast<long long>(w.rts) * P.hkv * w.nu;
+template <class W>
+__device__ __forceinline__ long long item_cost(const Walk& w) {
+  return static_cast<long long>(w.nu) * w.wt + W::kOver;
 }
-template <int R, int UNIT>
+template <class W>
 __device__ __forceinline__ void next_item(const AttnParams& P, Walk& w) {
   w.base += w.nu;
+  w.cost += item_cost<W>(w);
   if (++w.rt < w.rts) return;
   w.rt = 0;
   if (++w.h < P.hkv) return;
@@ -65,7 +74,7 @@ __device__ __forceinline__ void next_item(const AttnParams& P, Walk& w) {
       w.nu = 1 << 30;  // nothing follows
       return;
     }
-    set_seq<R, UNIT>(P, b, w.past, w.past1, w.len1, w);
+    set_seq<W>(P, b, w.past, w.past1, w.len1, w);
     load_ahead(P, w);
   } while (w.n == 0);
 }
@@ -129,69 +138,97 @@ __device__ __forceinline__ void finish(const AttnParams& P, const Walk& w, int t
   if (d == 0) store_lse(P, at, M, L);
 }
 
-// This CTA's run of the call's units. run: first unit, past the last, all units, CTAs that have any.
+// This CTA's run of the call's units: first unit, past the last, the cost of all, CTAs that share it.
 struct Run {
-  long long u0, u1, U, ctas;
+  long long u0, u1, all, ctas;
 };
 
+// The CTA that has the unit which starts at this cost: the last one whose share starts there or before.
+__device__ __forceinline__ int cta_of(const Run& run, long long cost) {
+  return static_cast<int>(divide((cost + 1) * run.ctas + run.all - 1, run.all)) - 1;
+}
+
 // Finds the run and the item that holds its first unit; false if there is none for this CTA. Every
-// thread calls it; `least` units a CTA at least. Ends with a barrier.
-template <int THREADS, int R, int UNIT>
-__device__ __forceinline__ bool find_run(const AttnParams& P, int least, long long* scan, Run* run,
-                                         Walk* first) {
+// thread calls it. A CTA's share costs as much as kLeast of the dearest units at least, so that an
+// item's pieces lie with neighbours. Ends with a barrier.
+template <int THREADS, class W>
+__device__ __forceinline__ bool find_run(const AttnParams& P, longlong2* scan, Run* run, Walk* first) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Walk w;
   const int per = (P.B + THREADS - 1) / THREADS;
   const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
-  long long mine = 0;
+  longlong2 mine = make_longlong2(0, 0);  // cost, units
   for (int b = b0; b < b1; ++b) {
-    load_seq<R, UNIT>(P, b, w);
-    mine += seq_units(P, w);
+    load_seq<W>(P, b, w);
+    const long long items = static_cast<long long>(w.rts) * P.hkv;
+    mine.x += items * item_cost<W>(w);
+    mine.y += items * w.nu;
   }
-  long long x = mine;
+  longlong2 x = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) scan[warp] = x;
-  __syncthreads();
-  long long before = 0, U = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) {
-    const long long n = scan[i];
-    if (i < warp) before += n;
-    U += n;
-  }
-  before += x - mine;
-  const long long ctas = min(static_cast<long long>(gridDim.x), divide(U + least - 1, least));
-  if (blockIdx.x >= ctas) return false;
-  const long long u0 = divide(U * blockIdx.x, ctas);
-  if (u0 >= before && u0 < before + mine) {
-    for (int b = b0; b < b1; ++b) {
-      load_seq<R, UNIT>(P, b, w);
-      const long long n = seq_units(P, w);
-      if (u0 < before + n) {
-        const long long item = divide(u0 - before, w.nu);
-        w.h = static_cast<int>(divide(item, w.rts));
-        w.rt = static_cast<int>(item - static_cast<long long>(w.h) * w.rts);
-        w.base = before + item * w.nu;
-        load_ahead(P, w);
-        *first = w;
-        run->u0 = u0;
-        run->u1 = divide(U * (blockIdx.x + 1), ctas);
-        run->U = U;
-        run->ctas = ctas;
-        break;
-      }
-      before += n;
+    const long long cost = __shfl_up_sync(0xFFFFFFFFu, x.x, d);
+    const long long units = __shfl_up_sync(0xFFFFFFFFu, x.y, d);
+    if (lane >= d) {
+      x.x += cost;
+      x.y += units;
     }
   }
+  if (lane == 31) scan[warp] = x;
+  if (tid == 0) run->u0 = run->u1 = 0;
   __syncthreads();
-  return true;
+  longlong2 before = make_longlong2(x.x - mine.x, x.y - mine.y), all = make_longlong2(0, 0);
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const longlong2 n = scan[i];
+    if (i < warp) {
+      before.x += n.x;
+      before.y += n.y;
+    }
+    all.x += n.x;
+    all.y += n.y;
+  }
+  constexpr int kShare = W::kLeast * W::kDearest;
+  const long long ctas = min(static_cast<long long>(gridDim.x), divide(all.x + kShare - 1, kShare));
+  if (blockIdx.x >= ctas) return false;
+  const long long c0 = divide(all.x * blockIdx.x, ctas), c1 = divide(all.x * (blockIdx.x + 1), ctas);
+  const bool has0 = c0 >= before.x && c0 < before.x + mine.x;
+  const bool has1 = c1 >= before.x && c1 < before.x + mine.x;
+  if (has0 || has1) {
+    for (int b = b0; b < b1; ++b) {
+      load_seq<W>(P, b, w);
+      const long long one = item_cost<W>(w), items = static_cast<long long>(w.rts) * P.hkv;
+      // the first unit that starts at c or later: past the item's last if c lies behind that
+      auto unit_at = [&](long long c, long long item) {
+        const long long i = divide(c - before.x - item * one + w.wt - 1, w.wt);
+        return before.y + item * w.nu + min(i, static_cast<long long>(w.nu));
+      };
+      if (c0 >= before.x && c0 < before.x + items * one) {
+        const long long item = divide(c0 - before.x, one);
+        run->u0 = unit_at(c0, item);
+        run->all = all.x;
+        run->ctas = ctas;
+        Walk at = w;
+        at.h = static_cast<int>(divide(item, w.rts));
+        at.rt = static_cast<int>(item - static_cast<long long>(at.h) * w.rts);
+        at.base = before.y + item * w.nu;
+        at.cost = before.x + item * one;
+        load_ahead(P, at);
+        if (run->u0 == at.base + at.nu) next_item<W>(P, at);
+        *first = at;
+      }
+      if (c1 >= before.x && c1 < before.x + items * one) run->u1 = unit_at(c1, divide(c1 - before.x, one));
+      before.x += items * one;
+      before.y += items * w.nu;
+    }
+  }
+  if (tid == 0 && blockIdx.x + 1 == ctas) run->u1 = all.y;
+  __syncthreads();
+  return run->u0 < run->u1;
 }
 
-// A piece of an item is written (R x D outputs, maxima, sums at P.part + slot * part_floats): counts
+// A CTA has two pieces of items at most, one that ends an item or goes on with it and one that
+// starts one, at P.part in this order (R x D outputs, maxima, sums). A piece is written: counts
 // it, and in the last CTA to arrive at the item joins its pieces, in their order. THREADS threads
 // call it, tid of them this one, with `sync` a barrier among them.
 template <int THREADS, int R, int D, int BATCH, class Sync>
@@ -199,17 +236,16 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const Walk& w, 
                                             int rows, int tid, int* s_last, Sync sync) {
   constexpr long long kPart = R * (D + 2);
   // pieces of this item lie with CTAs first .. last
-  const int first = static_cast<int>(divide((w.base + 1) * run.ctas + run.U - 1, run.U)) - 1;
-  const int last = static_cast<int>(divide((w.base + w.nu) * run.ctas + run.U - 1, run.U)) - 1;
+  const int first = cta_of(run, w.cost);
+  const int last = cta_of(run, w.cost + static_cast<long long>(w.nu - 1) * w.wt);
   __threadfence();
   sync();
   if (tid == 0) *s_last = atomicAdd(&P.arrived[first], 1u) == static_cast<unsigned>(last - first);
   sync();
   if (!*s_last) return;
   __threadfence();
-  const int slot0 = 2 * first + (divide(run.U * first, run.ctas) >= w.base ? 0 : 1);
   auto part_of = [&](int k) {
-    return P.part + static_cast<long long>(k == first ? slot0 : 2 * k) * kPart;
+    return P.part + static_cast<long long>(2 * k + (k == first ? 1 : 0)) * kPart;
   };
   for (int i = tid; i < rows * (D / 4); i += THREADS) {
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
