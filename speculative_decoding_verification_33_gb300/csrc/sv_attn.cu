@@ -19,10 +19,16 @@
 // the weights through shared memory, and sums half of the D outputs over all of the unit's tokens.
 // Nothing is computed twice, and a warp holds half the accumulators that a warp alone would, so
 // that 16 warps fit on an SM, where 8 left half of the issue slots to waits (64 sequences of up to
-// 8192 tokens, 24 rows a head: 111 us, a warp alone 147 us).
+// 8192 tokens, 24 rows a head, before the work was cut by cost: 111 us, a warp alone 147 us).
 //
 // Each pair streams its units through a ring in shared memory with bulk copies that it issues
 // itself; no barrier spans the pairs until a head ends, and then the SM's other CTA streams on.
+//
+// What bounds it is instructions, not bytes: for D = 128 a block of 16 tokens takes 64 conversions,
+// 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax. 524301
+// tokens of 8 heads take 134 us with 4 rows (4.5 TB/s, 0.67 of the measured copy rate), 166 with 16,
+// 215 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 88 us (0.35); one request
+// of 4097 tokens 11 us, most of it the way from the lengths to the pages, the bytes and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -629,9 +635,9 @@ cudaError_t launch_tiles(const AttnParams& P, int sms, cudaStream_t stream) {
 }
 
 // Rows of a tile, at most. For D = 128 the kernel of sv_attn_tc.cu takes what has more: with 28 rows
-// a head it takes 156 us for 300001 tokens of 8 heads and 148 us for 64 sequences of up to 8192
-// tokens, this one 175 and 154; with 24 rows it takes 149 and 141 us, this one 134 and 111. It has
-// no form for D = 64.
+// a head it takes 241 us for 524301 tokens of 8 heads, 115 us for 64 sequences of up to 8192 tokens
+// and 23.5 us for 8 of 2000, this one 294, 109 and 28.2; with 24 rows it takes 230, 113 and 22.7 us,
+// this one 214, 89 and 20.2. It has no form for D = 64.
 template <int D>
 constexpr int kMaxRows = D == 128 ? 24 : 32;
 

@@ -14,10 +14,17 @@
 //
 // One CTA an SM, its warps specialised, two tiles in flight between any two of them: one copies
 // blocks in, one issues products, four unpack keys, four unpack values, sixteen take scores to
-// weights, each four of these a quarter of the rows. The first form, eight warps that did all of it in
-// turn behind barriers of the CTA, two CTAs an SM, took 363 us for 524301 tokens and 20 rows of 8
-// heads: its warps waited for the one that issued products. The work is cut and joined as in
-// sv_attn.cu, in units of 128 tokens.
+// weights, each four of these a quarter of the rows, and one walks through the heads ahead of all
+// others. The first form, eight warps that did all of it in turn behind barriers of the CTA, two CTAs
+// an SM, took 363 us for 524301 tokens and 20 rows of 8 heads: its warps waited for the one that
+// issued products. The work is cut and joined as in sv_attn.cu, in units of 128 tokens.
+//
+// What bounds it is the way of a tile through the weights' warps, from scores in tensor memory to
+// weights in shared memory (about 2300 cycles for 32 rows, 2600 for 64; the products take 1000, the
+// copies 700): leaving out the conversions of keys or values in an experiment changed nothing. 256
+// sequences of up to 8192 tokens, 63 rows on each of 4 heads, take 235 us (438 in the kernel of
+// register operands when that was measured), 0.27 of the measured copy rate; 524301 tokens of 8 heads
+// with 64 rows 279 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

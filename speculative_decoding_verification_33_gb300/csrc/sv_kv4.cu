@@ -7,6 +7,10 @@
 // bits of each byte with a pair of atomics on 32-bit words, which leaves the other token's bits
 // alone, whoever else writes the word. Bits of different tokens never meet, so the order of the
 // atomics does not matter.
+//
+// 65013 tokens of 8 heads of 128 in bf16 (608 MB read and written, the values as they are held
+// among them) take 119 us, 0.75 of the measured copy rate; the quantisation's instructions and the
+// scattered lines of 16 to 64 bytes share the rest. 384 tokens take 3.2 us, which is the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -100,7 +104,7 @@ __device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
 // is held at 448) they come from one division for the block and Markstein's correction for
 // each value: with y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y), two fused operations, is RN(x / s)
 // (P. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
-// 16 divisions made the kernel issue-bound: 65013 tokens of 8 heads took 149 us.
+// 16 divisions made the kernel issue-bound: 65013 tokens of 8 heads took 149 us instead of 119.
 __device__ __forceinline__ uint2 quantise(const float (&x)[16], float inv6g, float g, bool plain,
                                           uint32_t* scale_bits) {
   float m = fabsf(x[0]);
