@@ -16,6 +16,9 @@
  * Memory: every pointer is DEVICE memory owned by the caller. All calls are asynchronous on
  * `stream` (a cudaStream_t, NULL for the legacy default stream), do not synchronise and may be
  * captured into a graph (spec_kv4_attention after one call on the same stream outside capture).
+ * spec_kv4_attention keeps a workspace of fixed size for each device and stream; a captured call
+ * keeps that of the stream it was captured on, so its replays must not overlap other calls of
+ * that stream, or replays of other graphs captured on it.
  *
  * Errors: arguments are checked on the host before anything is launched, as in spec_verify.h.
  *
@@ -115,8 +118,8 @@ sv_status spec_qk_norm_rope(int T, int Hq, int Hkv, int D, int rot, int interlea
 /*
  * Keys and values of T tokens into the cache. For 16 neighbouring values x of a head:
  * scale = e4m3(max|x| * float32(1 / (6 g))), at most 448, and code = e2m1(x / (scale * g)), both to
- * nearest with ties to even, the quotient in float32 and held at +-6; g is k_scale or v_scale (finite, > 0). 16 values that hold
- * a NaN or an infinity get a NaN scale: they read as NaN.
+ * nearest with ties to even, the quotient in float32 and held at +-6; g is k_scale or v_scale
+ * (finite, > 0). 16 values that hold a NaN or an infinity get a NaN scale: they read as NaN.
  *   k, v [T][Hkv][D] of dtype, rows as in spec_qk_norm_rope, 16-byte aligned (pointers, strides)
  *   slots [T] int64: slot of each token; a token whose slot is outside 0..num_pages*page_size-1
  *      is not written. The slots of one call are distinct.
