@@ -146,24 +146,35 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const float2 (&v)[4]) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// Columns t and t + 32 and the seven after each: the row groups of this warp.
-__device__ __forceinline__ void tmem_ld_groups(uint32_t t, float2 (&v)[2][4]) {
-  uint32_t r[16];
+// Columns t and t + 32 and the seven after each, the row groups of this warp: asked for, and there
+// (nothing may be done with r in between).
+__device__ __forceinline__ void tmem_ld_start(uint32_t t, uint32_t (&r)[16]) {
   asm volatile(
-      "{\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
-      : "r"(t), "r"(t + 32)
+      : "r"(t), "r"(t + 32));
+}
+__device__ __forceinline__ void tmem_ld_finish(uint32_t (&r)[16], float2 (&v)[2][4]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15])
+      :
       : "memory");
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       v[k][j] = make_float2(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+}
+__device__ __forceinline__ void tmem_ld_groups(uint32_t t, float2 (&v)[2][4]) {
+  uint32_t r[16];
+  tmem_ld_start(t, r);
+  tmem_ld_finish(r, v);
 }
 
 // Two floats at a time
@@ -656,19 +667,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         const int b = t & 1, t0 = unit * kTcUnit;
         wait_warp(&S.s_full[b], t >> 1);
         tc_fence_after();
-        const uint32_t lost = S.lost[t & 15];
-        const bool masked = t0 + kTcUnit > all_see || lost;
-        if (past & 2u) poison |= nan_rows(t - 2, unit - 2);
-        past = (past << 1) | (masked ? 1u : 0u);
+        bool masked;
         // Scores less their rows' maxima. If one of them is too large they are read once more, and
         // the maxima are moved, as an item's first are in any case.
         float2 z[2][4];
         for (bool move = first;;) {
-          tmem_ld_groups(mine + kColS + 64 * b + 8 * hh, z);
+          // what they are multiplied with is read while they come
+          uint32_t raw[16];
+          tmem_ld_start(mine + kColS + 64 * b + 8 * hh, raw);
+          const uint32_t lost = S.lost[t & 15];
+          const float4 f[2][2] = {{qc4[0], qc4[1]}, {qc4[8], qc4[9]}};
+          tmem_ld_finish(raw, z);
+          masked = t0 + kTcUnit > all_see || lost;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             if (8 * (4 * k + hh) >= rows) break;
-            const float4 a = qc4[8 * k], c = qc4[8 * k + 1];
+            const float4 a = f[k][0], c = f[k][1];
             // rounded before the maximum is taken
             z[k][0] = mul2(z[k][0], make_float2(a.x, a.y));
             z[k][1] = mul2(z[k][1], make_float2(a.z, a.w));
@@ -747,6 +761,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
           if (move || !named_sync_or(1 + hh, 128, top > kSlack)) break;
           move = true;
         }
+        if (past & 2u) poison |= nan_rows(t - 2, unit - 2);
+        past = (past << 1) | (masked ? 1u : 0u);
         // the products that read this buffer last were issued before these scores'
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
