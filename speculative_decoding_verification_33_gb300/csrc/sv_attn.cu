@@ -2,7 +2,7 @@
 //
 // Everything that a sequence's rows (new tokens x query heads of one key/value head) need of the
 // cache is read once for all of them: a block of 16 tokens is 18 D bytes, its products with R
-// rows 64 D R operations. The unit of work is two blocks for one tile of R = 8 NT rows. All
+// rows 64 D R operations. The unit of work is two or four blocks for one tile of R = 8 NT rows. All
 // units of the call, sequence after sequence, are cut into equal runs, one per persistent CTA, so
 // that the load is even whatever the lengths are; a head that is cut has its pieces joined by the
 // last CTA that finishes one of them, in their order, so results do not depend on timing.
@@ -26,7 +26,7 @@
 //
 // What bounds it is instructions, not bytes: for D = 128 a block of 16 tokens takes 64 conversions,
 // 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax. 524301
-// tokens of 8 heads take 134 us with 4 rows (4.5 TB/s, 0.67 of the measured copy rate), 166 with 16,
+// tokens of 8 heads take 122 us with 4 rows (4.9 TB/s, 0.73 of the measured copy rate), 168 with 16,
 // 215 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 88 us (0.35); one request
 // of 4097 tokens 11 us, most of it the way from the lengths to the pages, the bytes and the join.
 #include <cuda_bf16.h>
@@ -52,25 +52,30 @@ struct AttnShape {
   static constexpr int kThreads = 64 * kPairs;
   static constexpr int kPerSm = 2;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kUnit = 32;  // tokens: a block for each warp of a pair
+  // Blocks of a unit for each warp of a pair. With one tile of rows there are registers for two: half
+  // the barriers, 122 us instead of 135 for 524301 tokens of 8 heads and 4 rows, 58 instead of 61 for
+  // 64 sequences of up to 8192. With two tiles that takes 160 instead of 168 us and 75 instead of
+  // 72.5, and for 256 sequences of up to 1024 tokens 78 instead of 68.
+  static constexpr int kOwn = NT == 1 ? 2 : 1;
+  static constexpr int kUnit = 32 * kOwn;  // tokens
   // Work as it is cut: 524301 tokens of 8 heads take 134, 166, 215 and 280 us with 1 to 4 tiles. With
   // an item's start and end for nothing, 64 sequences of up to 8192 tokens, 24 rows a head, take
   // 113 us and 256 of up to 1024 tokens 135 us; for 96, 88 and 86 us.
-  static constexpr int kDearest = NT == 1 ? 5 : NT == 2 ? 6 : NT == 3 ? 8 : 10;
+  static constexpr int kDearest = kOwn * (NT == 1 ? 5 : NT == 2 ? 6 : NT == 3 ? 8 : 10);
   static constexpr int kOver = 96;
   // Every pair of a CTA gets three units or so at least: with one, more pieces are to be joined, and
   // one request of 4000 tokens, 24 rows a head, takes 21.9 us instead of 17.6
-  static constexpr int kLeast = 3 * kPairs;
+  static constexpr int kLeast = 3 * kPairs / kOwn;
   static __device__ __forceinline__ int weight(int rows) {
     const int tiles = NT == 1 ? 1 : max((rows + 7) >> 3, NT - 1 > 2 ? 2 : NT - 1);
-    return tiles <= 1 ? 5 : tiles == 2 ? 6 : tiles == 3 ? 8 : 10;
+    return kOwn * (tiles <= 1 ? 5 : tiles == 2 ? 6 : tiles == 3 ? 8 : 10);
   }
   static constexpr int kBlock = KvBlock<D>::kBytes;
-  static constexpr int kStage = 2 * kBlock;
-  static constexpr int kStages = 3 * (128 / D);
+  static constexpr int kStage = 2 * kOwn * kBlock;
+  static constexpr int kStages = (kOwn == 1 ? 3 : 2) * (128 / D);
   static constexpr int kRing = kPairs * kStages * kStage;
   static constexpr int kQ = NT * (D / 16) * 32 * 8;
-  static constexpr int kP = kPairs * 2 * NT * 32 * 8;
+  static constexpr int kP = kPairs * 2 * kOwn * NT * 32 * 8;
   static constexpr int kOutStride = D + 4;  // floats of a row of a joining buffer
   static constexpr int kOut = kPairs * 8 * kOutStride * 4;
   // the first joining buffer lies over the queries and weights, which are spent by then
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     attn_kernel(AttnParams P) {
   using S = AttnShape<D, NT>;
   constexpr int NP = S::kPairs, NS = S::kStages, R = S::kRows, KS = D / 16, MH = D / 32;
-  constexpr int NB = 2, UNIT = S::kUnit;
+  constexpr int OWN = S::kOwn, NB = 2 * OWN, UNIT = S::kUnit;
   constexpr int QV = D / 8;  // 16-byte vectors of a query row
   constexpr int QPER = (R * QV + S::kThreads - 1) / S::kThreads;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -295,12 +300,19 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       } else {
         mbar_arrive_expect_tx(&my_bar[stage], n * S::kBlock);
         unsigned char* to = my_ring + stage * S::kStage;
-        if (!lost && off[NB - 1] == off[0] + (NB - 1) * S::kBlock) {  // one run of bytes
-          bulk_g2s(to, P.cache + off[0], S::kStage, &my_bar[stage]);
-        } else {
+        auto together = [&] { bulk_g2s(to, P.cache + off[0], S::kStage, &my_bar[stage]); };
+        auto apart = [&] {
 #pragma unroll
           for (int i = 0; i < NB; ++i)
             if (off[i] >= 0) bulk_g2s(to + i * S::kBlock, P.cache + off[i], S::kBlock, &my_bar[stage]);
+        };
+        // one run of bytes, or not; a condition for both sizes costs those of two blocks 2 % (the
+        // compiler's schedule of what follows changes)
+        if constexpr (NB == 2) {
+          if (!lost && off[NB - 1] == off[0] + (NB - 1) * S::kBlock) together(); else apart();
+        } else {
+          if (!lost && off[1] - off[0] == S::kBlock && off[2] - off[1] == S::kBlock &&
+              off[3] - off[2] == S::kBlock) together(); else apart();
         }
       }
     }
@@ -405,13 +417,14 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         const uint32_t lost = my_lost[stage];
         const bool masked = t0 + UNIT > all_see || lost;
 
-        // scores of this warp's block and the tile's rows
-        float s[TN][4];
-        {
-          KeyCodes<D> kc;
-          kc.load(sb + h * S::kBlock, g, c);
+        // scores of this warp's blocks and the tile's rows
+        float s[OWN][TN][4];
 #pragma unroll
-          for (int t = 0; t < TN; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+        for (int o = 0; o < OWN; ++o) {
+          KeyCodes<D> kc;
+          kc.load(sb + (h * OWN + o) * S::kBlock, g, c);
+#pragma unroll
+          for (int t = 0; t < TN; ++t) s[o][t][0] = s[o][t][1] = s[o][t][2] = s[o][t][3] = 0.f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t kf[2][4];
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
 #pragma unroll
               for (int n = 0; n < 2; ++n) {
                 const uint2 q = sq[(t * KS + 2 * i + n) * 32 + lane];
-                mma16816(s[t], kf[n][0], kf[n][1], kf[n][2], kf[n][3], q.x, q.y);
+                mma16816(s[o][t], kf[n][0], kf[n][1], kf[n][2], kf[n][3], q.x, q.y);
               }
           }
         }
@@ -430,25 +443,33 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         for (int t = 0; t < TN; ++t) {
           const float2 qc = *reinterpret_cast<const float2*>(sqc + 8 * t + 2 * c);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[t][k] = __fmul_rn(s[t][k], k & 1 ? qc.y : qc.x);
+          for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[o][t][k] = __fmul_rn(s[o][t][k], k & 1 ? qc.y : qc.x);
         }
         if (masked) {
-          const int tb = t0 + 16 * h + g;
 #pragma unroll
-          for (int t = 0; t < TN; ++t)
+          for (int o = 0; o < OWN; ++o) {
+            const int tb = t0 + 16 * (h * OWN + o) + g;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (tb + 8 * (k >> 1) >= svis[8 * t + 2 * c + (k & 1)])
-                s[t][k] = -INFINITY;
-              else if ((lost >> h) & 1u)
-                s[t][k] = NAN;
-            }
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (tb + 8 * (k >> 1) >= svis[8 * t + 2 * c + (k & 1)])
+                  s[o][t][k] = -INFINITY;
+                else if ((lost >> (h * OWN + o)) & 1u)
+                  s[o][t][k] = NAN;
+              }
+          }
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < TN; ++t)
+        for (int o = 0; o < OWN; ++o)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) top = fmaxf(top, fmaxf(s[t][e], s[t][e + 2]) - m[t][e]);
+          for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              top = fmaxf(top, fmaxf(s[o][t][e], s[o][t][e + 2]) - m[t][e]);
         const bool move = named_sync_or(1 + pair, 64, top > kSlack);
         // both warps are past the last unit
         if (h == 0 && spent >= 0) issue(spent);
@@ -458,7 +479,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           for (int t = 0; t < TN; ++t) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y = fmaxf(s[t][e], s[t][e + 2]);
+              float y = fmaxf(s[0][t][e], s[0][t][e + 2]);
+              if (OWN == 2) y = fmaxf(y, fmaxf(s[OWN - 1][t][e], s[OWN - 1][t][e + 2]));
               y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
               y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
               y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
@@ -483,16 +505,18 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
             }
         }
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          float x[4];
+        for (int o = 0; o < OWN; ++o)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = ex2_fast(s[t][k] - m[t][k & 1]);
-            l[t][k & 1] += x[k];
+          for (int t = 0; t < TN; ++t) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = ex2_fast(s[o][t][k] - m[t][k & 1]);
+              l[t][k & 1] += x[k];
+            }
+            my_p[((h * OWN + o) * NT + t) * 32 + lane] =
+                make_uint2(transpose8x8(pack_f16(x[0], x[1])), transpose8x8(pack_f16(x[2], x[3])));
           }
-          my_p[(h * NT + t) * 32 + lane] =
-              make_uint2(transpose8x8(pack_f16(x[0], x[1])), transpose8x8(pack_f16(x[2], x[3])));
-        }
         ValueCodes<D> vc[NB];  // read ahead of the barrier
 #pragma unroll
         for (int b = 0; b < NB; ++b) vc[b].load(sb + b * S::kBlock, g, c, h);

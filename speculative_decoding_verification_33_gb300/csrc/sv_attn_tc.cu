@@ -56,7 +56,7 @@ constexpr int kTcUnit = 128;   // tokens
 // as much as four tiles: 256 sequences of up to 8192 tokens, 63 rows a head, take 258 us if they are
 // not counted, 235 us if they are, and 256 of up to 1024 tokens, 32 rows, 172 and 129 us.
 struct TcWork {
-  static constexpr int kRows = kTcMaxRows, kUnit = kTcUnit, kDearest = 4, kOver = 16, kLeast = 2;
+  static constexpr int kRows = kTcMaxRows, kUnit = kTcUnit, kDearest = 4, kOver = 12, kLeast = 2;
   static __device__ __forceinline__ int weight(int) { return 4; }
 };
 constexpr int kTcStages = 4;   // tiles of the cache's bytes on their way
