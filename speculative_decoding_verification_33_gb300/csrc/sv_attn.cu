@@ -27,7 +27,7 @@
 // What bounds it is instructions, not bytes: for D = 128 a block of 16 tokens takes 64 conversions,
 // 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax. 524301
 // tokens of 8 heads take 122 us with 4 rows (4.9 TB/s, 0.73 of the measured copy rate), 168 with 16,
-// 215 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 88 us (0.35); one request
+// 215 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 89 us (0.35); one request
 // of 4097 tokens 11 us, most of it the way from the lengths to the pages, the bytes and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -58,9 +58,9 @@ struct AttnShape {
   // 72.5, and for 256 sequences of up to 1024 tokens 78 instead of 68.
   static constexpr int kOwn = NT == 1 ? 2 : 1;
   static constexpr int kUnit = 32 * kOwn;  // tokens
-  // Work as it is cut: 524301 tokens of 8 heads take 134, 166, 215 and 280 us with 1 to 4 tiles. With
-  // an item's start and end for nothing, 64 sequences of up to 8192 tokens, 24 rows a head, take
-  // 113 us and 256 of up to 1024 tokens 135 us; for 96, 88 and 86 us.
+  // Work as it is cut: 524301 tokens of 8 heads take 135, 168, 215 and 287 us with 1 to 4 tiles and
+  // one block a warp. With an item's start and end for nothing, 64 sequences of up to 8192 tokens, 24
+  // rows a head, take 113 us and 256 of up to 1024 tokens 135 us; for 96, 89 and 86 us.
   static constexpr int kDearest = kOwn * (NT == 1 ? 5 : NT == 2 ? 6 : NT == 3 ? 8 : 10);
   static constexpr int kOver = 96;
   // Every pair of a CTA gets three units or so at least: with one, more pieces are to be joined, and
@@ -659,9 +659,9 @@ cudaError_t launch_tiles(const AttnParams& P, int sms, cudaStream_t stream) {
 }
 
 // Rows of a tile, at most. For D = 128 the kernel of sv_attn_tc.cu takes what has more: with 28 rows
-// a head it takes 241 us for 524301 tokens of 8 heads, 115 us for 64 sequences of up to 8192 tokens
-// and 23.5 us for 8 of 2000, this one 294, 109 and 28.2; with 24 rows it takes 230, 113 and 22.7 us,
-// this one 214, 89 and 20.2. It has no form for D = 64.
+// a head it takes 231 us for 524301 tokens of 8 heads, 106 us for 64 sequences of up to 8192 tokens
+// and 23.5 us for 8 of 2000, this one 296, 109 and 28.3; with 24 rows it takes 219, 103 and 22.5 us,
+// this one 215, 89 and 20.2. It has no form for D = 64.
 template <int D>
 constexpr int kMaxRows = D == 128 ? 24 : 32;
 

@@ -20,11 +20,11 @@
 // issued products. The work is cut and joined as in sv_attn.cu, in units of 128 tokens.
 //
 // What bounds it is the way of a tile through the weights' warps, from scores in tensor memory to
-// weights in shared memory (about 2300 cycles for 32 rows, 2600 for 64; the products take 1000, the
+// weights in shared memory (about 2050 cycles for 32 rows, 2400 for 64; the products take 1000, the
 // copies 700): leaving out the conversions of keys or values in an experiment changed nothing. 256
-// sequences of up to 8192 tokens, 63 rows on each of 4 heads, take 235 us (438 in the kernel of
-// register operands when that was measured), 0.27 of the measured copy rate; 524301 tokens of 8 heads
-// with 64 rows 279 us.
+// sequences of up to 8192 tokens, 63 rows on each of 4 heads, take 219 us (438 in the kernel of
+// register operands when that was measured), 0.29 of the measured copy rate; 524301 tokens of 8 heads
+// with 64 rows 270 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,8 +53,8 @@ constexpr int kTcWThreads = 32 * (kWarpItems - kWarpWeights);
 constexpr int kTcThreads = 32 * kTcWarps;
 constexpr int kTcUnit = 128;   // tokens
 // Work as it is cut. A tile costs much the same for 32 rows and for 64. An item's start and end cost
-// as much as four tiles: 256 sequences of up to 8192 tokens, 63 rows a head, take 258 us if they are
-// not counted, 235 us if they are, and 256 of up to 1024 tokens, 32 rows, 172 and 129 us.
+// as much as three tiles: counted so, 256 sequences of up to 8192 tokens, 63 rows a head, take 219 us
+// (222 counted as four, 225 as five), and not counting them cost 23 us more than counting four.
 struct TcWork {
   static constexpr int kRows = kTcMaxRows, kUnit = kTcUnit, kDearest = 4, kOver = 12, kLeast = 2;
   static __device__ __forceinline__ int weight(int) { return 4; }
