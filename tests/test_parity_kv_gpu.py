@@ -4,6 +4,7 @@ Integers and 4-bit codes are equal. Tolerances count roundings: half a step of t
 (2^-8 of a bf16 value, 2^-24 of a float32 one) and, scaled by the magnitudes that enter a sum, those of
 the arithmetic in between; each test says which.
 """
+import itertools
 import math
 
 import numpy as np
@@ -462,6 +463,27 @@ def test_attention_tiles(ps, hq, hk):
     """The kernel for many rows, with few and many of them, lengths around its tiles of 128."""
     _check_attention([127, 128, 129, 255, 260, 1, 16], [1, 2, 3, 9, 5, 1, 4], hq, hk, 128, ps,
                      max_new=64)
+
+
+@HINTS
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_every_order_of_four_pages(D, hint):
+    """Blocks that are fetched together, side by side in the cache or not, in every order."""
+    orders = list(itertools.permutations(range(4)))
+
+    def edit(cache, table, q):
+        table[:] = [[4 * b + i for i in order] for b, order in enumerate(orders)]
+    _check_attention([64] * len(orders), [1] * len(orders), 4, 1, D, 16, edit=edit, max_new=hint)
+
+
+@HINTS
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 32)])
+def test_attention_uneven_batches(D, ps, hint):
+    """Sequences that cost very different amounts: empty ones, single tokens, many rows, long ones."""
+    r = np.random.default_rng(D)
+    lens, news = r.integers(1, 300, 60), r.choice([0, 0, 1, 1, 2, 7, 12], 60)
+    lens[::9], lens[4], lens[30] = r.integers(0, 20, 7), 2500, 1800
+    _check_attention(lens, news, 8, 2, D, ps, max_new=hint)
 
 
 def wide_cache(B, L, H, D, ps, seed):
