@@ -850,8 +850,8 @@ sv_status spec_verify_device_error(void* stream) {
   const sv_status a = ws ? take_error(&ws->error) : SV_OK;
   const sv_status b = fixed ? take_error(&static_cast<Workspace*>(fixed)->error) : SV_OK;
   const sv_status c = att ? take_error(att) : SV_OK;
-  // a call that gave up may have left arrivals at its cut items
-  if (c == SV_ERR_DEVICE_TIMEOUT && cudaMemset(att, 0, sv::kAttnHeader) != cudaSuccess)
+  // a call that gave up may have left arrivals at its cut items: zero before this stream's next call
+  if (c == SV_ERR_DEVICE_TIMEOUT && cudaMemsetAsync(att, 0, sv::kAttnHeader, s) != cudaSuccess)
     return SV_ERR_CUDA;
   if (a == SV_ERR_CUDA || b == SV_ERR_CUDA || c == SV_ERR_CUDA) return SV_ERR_CUDA;
   return (a == SV_ERR_DEVICE_TIMEOUT || b == SV_ERR_DEVICE_TIMEOUT || c == SV_ERR_DEVICE_TIMEOUT)
@@ -1151,9 +1151,11 @@ sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size
       cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
       if (cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
         return SV_ERR_UNSUPPORTED;  // the workspace must exist before capture
-      const size_t need = sv::attention_workspace_bytes(sms);
+      // The header starts at zero, set in this stream's order: the default stream's may lie behind
+      // work that this one does not wait for. Pieces are written before they are read.
       void* w = nullptr;
-      if (cudaMalloc(&w, need) != cudaSuccess || cudaMemset(w, 0, need) != cudaSuccess) {
+      if (cudaMalloc(&w, sv::attention_workspace_bytes(sms)) != cudaSuccess ||
+          cudaMemsetAsync(w, 0, sv::kAttnHeader, s) != cudaSuccess) {
         if (w) cudaFree(w);
         return SV_ERR_CUDA;
       }

@@ -62,7 +62,7 @@ constexpr int kAttnMaxCtas = (4096 - 256) / 4;
 constexpr int kTcMaxRows = 64;  // rows of a tile of the tcgen05 kernel (sv_attn_tc.cu), D = 128
 cudaError_t launch_attention_tc(const AttnParams& P, int sms, cudaStream_t stream);
 
-// Bytes of the attention workspace on a device with `sms` multiprocessors; zeroed once.
+// Bytes of the attention workspace on a device with `sms` multiprocessors; its header is zeroed once.
 size_t attention_workspace_bytes(int sms);
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream);
