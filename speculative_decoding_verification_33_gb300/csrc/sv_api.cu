@@ -71,14 +71,18 @@ sv_status noalloc_array(int dev, bool create, void** ws) {
   return SV_OK;
 }
 
-// Reads a workspace's error word (after the caller synchronised its stream) and clears it.
+// Reads a workspace's error word once its stream's work is done, and clears it, all in that stream's
+// order: the word is clear before the stream's next call and when this returns.
 // Returns SV_ERR_DEVICE_TIMEOUT if it was raised.
-sv_status take_error(unsigned int* word) {
+sv_status take_error(unsigned int* word, cudaStream_t s) {
   unsigned int err = 0;
-  if (cudaMemcpy(&err, word, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpyAsync(&err, word, sizeof(err), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
     return SV_ERR_CUDA;
   if (!err) return SV_OK;
-  if (cudaMemset(word, 0, sizeof(err)) != cudaSuccess) return SV_ERR_CUDA;
+  if (cudaMemsetAsync(word, 0, sizeof(err), s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return SV_ERR_CUDA;
   return SV_ERR_DEVICE_TIMEOUT;
 }
 
@@ -163,7 +167,9 @@ StreamRes* resources(int dev, cudaStream_t s, size_t need, sv_status* st) {
       r.ws_bytes = 0;
     }
     void* w = nullptr;
-    if (cudaMalloc(&w, need) != cudaSuccess || cudaMemset(w, 0, need) != cudaSuccess) {
+    // zeroed in this stream's order: the default stream's may lie behind work that this one does not
+    // wait for
+    if (cudaMalloc(&w, need) != cudaSuccess || cudaMemsetAsync(w, 0, need, s) != cudaSuccess) {
       if (w) cudaFree(w);
       *st = SV_ERR_CUDA;
       return nullptr;
@@ -543,7 +549,8 @@ sv_status run(const sv_problem* p, const void* tgt, const void* dft, const int32
         r.dd = nullptr;
         r.dd_cap = 0;
       }
-      if (cudaMalloc(&r.dd, need) != cudaSuccess || cudaMemset(r.dd, 0, need) != cudaSuccess) {
+      if (cudaMalloc(&r.dd, need) != cudaSuccess ||
+          cudaMemsetAsync(r.dd, 0, need, stream) != cudaSuccess) {
         if (r.dd) cudaFree(r.dd);
         r.dd = nullptr;
         return SV_ERR_CUDA;
@@ -847,9 +854,9 @@ sv_status spec_verify_device_error(void* stream) {
   }
   if (cudaStreamSynchronize(s) != cudaSuccess) return SV_ERR_CUDA;
   // every word is read and cleared, so one report covers them all
-  const sv_status a = ws ? take_error(&ws->error) : SV_OK;
-  const sv_status b = fixed ? take_error(&static_cast<Workspace*>(fixed)->error) : SV_OK;
-  const sv_status c = att ? take_error(att) : SV_OK;
+  const sv_status a = ws ? take_error(&ws->error, s) : SV_OK;
+  const sv_status b = fixed ? take_error(&static_cast<Workspace*>(fixed)->error, s) : SV_OK;
+  const sv_status c = att ? take_error(att, s) : SV_OK;
   // a call that gave up may have left arrivals at its cut items: zero before this stream's next call
   if (c == SV_ERR_DEVICE_TIMEOUT && cudaMemsetAsync(att, 0, sv::kAttnHeader, s) != cudaSuccess)
     return SV_ERR_CUDA;
@@ -861,9 +868,7 @@ sv_status spec_verify_device_error(void* stream) {
 
 sv_status spec_verify_workspace_error(void* workspace, void* stream) {
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return SV_ERR_INVALID_ARG;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return SV_ERR_CUDA;
-  return take_error(&static_cast<Workspace*>(workspace)->error);
+  return take_error(&static_cast<Workspace*>(workspace)->error, static_cast<cudaStream_t>(stream));
 }
 
 // ---------------------------------------------------------------------------------------------

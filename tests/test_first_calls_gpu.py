@@ -59,3 +59,37 @@ def test_attention(max_new):
     def call():
         return sv.kv4_attention(q, cache, table, lens, cu, page_size=ps, max_new=max_new, out=next(out))
     first_calls(call, call())
+
+
+@pytest.mark.parametrize("B,K,V,mode,beta", [
+    (64, 8, 152064, "stochastic", 1.0),   # the walk, its draws deferred to two more launches
+    (64, 8, 152064, "stochastic", 0.5),   # the walk behind its prepass
+    (64, 8, 152064, "greedy", 1.0),       # the greedy walk
+    (8, 5, 32000, "stochastic", 1.0),     # every row at once
+    (8, 5, 32000, "greedy", 1.0)])
+def test_verify(B, K, V, mode, beta):
+    g = torch.Generator("cuda").manual_seed(B + K)
+    tgt = torch.randn(B, K + 1, V, device="cuda", generator=g).mul_(2).to(BF16)
+    dft = (tgt[:, :K].float() + torch.randn(B, K, V, device="cuda", generator=g) * 0.3).to(BF16)
+    tokens = dft.argmax(-1).int()
+    uniforms = torch.rand(B, K + 1, device="cuda", generator=g)
+
+    def call():
+        return sv.verify(tgt, None if mode == "greedy" else dft, tokens, None,
+                         None if mode == "greedy" else uniforms, mode=mode, beta=beta,
+                         bias_k=4 if beta < 1 else 0)
+    first_calls(call, call())
+
+
+def test_rows():
+    """The row steps' queues."""
+    B, K, V = 40, 6, 32000
+    g = torch.Generator("cuda").manual_seed(1)
+    tgt = torch.randn(B, K + 1, V, device="cuda", generator=g).to(BF16)
+    dft = torch.randn(B, K, V, device="cuda", generator=g).to(BF16)
+    uniforms = torch.rand(B * K, device="cuda", generator=g)
+
+    def call():
+        return {**sv.draft_sample(dft.view(B * K, V), uniforms, beta=0.5, bias_k=4),
+                **sv.residual_topf(tgt, dft, None, [4] * K)}
+    first_calls(call, call())
