@@ -227,6 +227,13 @@ struct TcItem {
   bool whole;
 };
 
+// Tiles whose tokens with a NaN scale are kept. The values' warps note those of tile t, over those of
+// tile t - kNanTiles, once the products of tile t - 3 are done, so once the weights of tile t - 3 are
+// there; the weights' warps read those of tile i before they hand over the weights of tile i + 2, or, of
+// an item's last two tiles, those of the next item's first one, i + 1 or i + 2. So any number above 4
+// keeps what is still to be read; a power of two makes the place cheap.
+constexpr int kNanTiles = 8;
+
 // What the roles share. Tile t uses buffer t & 1 of everything that is held twice.
 struct TcShared {
   uint64_t raw_full[kTcStages], raw_empty[kTcStages];  // the cache's bytes
@@ -250,8 +257,8 @@ struct TcShared {
   alignas(16) float down[kTcMaxRows];
   float part[4][kTcMaxRows];      // per quarter of a tile's tokens: maxima, sums
   alignas(16) int at[4][kTcMaxRows];  // its row of the output, from the item's first (of four items)
-  uint32_t nan[4][8][4];          // per tile modulo 4 and 16 values: tokens with a NaN scale
-  int nans[4];                    // the tile that this speaks of, plus one
+  uint32_t nan[kNanTiles][8][4];  // per tile modulo kNanTiles and 16 values: tokens with a NaN scale
+  int nans[kNanTiles];            // the tile that this speaks of, plus one
   int last;
 };
 
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       S.items[i].end = S.items[i].rows = 1;
     }
     fence_mbar_init();
-    for (int i = 0; i < 4; ++i) S.nans[i] = 0;
+    for (int i = 0; i < kNanTiles; ++i) S.nans[i] = 0;
   }
   if (!find_run<kTcThreads, TcWork>(P, S.scan, &S.run, &S.first)) return;
   if (warp == 1) tmem_alloc(&S.tmem, kTcCols);
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         arrive_warp(&S.raw_empty[stage]);
         if (t0 + kTcUnit > all_see || lost) {
           // see sv_attn.cu: what some row does not see must not reach it as 0 * NaN
-          if (vid < 32) S.nan[t & 3][vid >> 2][vid & 3] = 0;
+          if (vid < 32) S.nan[t & (kNanTiles - 1)][vid >> 2][vid & 3] = 0;
           named_sync(5, 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -564,8 +571,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
                 sc[i] &= ~(0xFFu << sh);
               } else if (bad && t0 + k >= all_see) {
                 sc[i] &= ~(0xFFu << sh);
-                atomicOr(&S.nan[t & 3][vg][k >> 5], 1u << (k & 31));
-                S.nans[t & 3] = t + 1;
+                atomicOr(&S.nan[t & (kNanTiles - 1)][vg][k >> 5], 1u << (k & 31));
+                S.nans[t & (kNanTiles - 1)] = t + 1;
               }
             }
         }
@@ -640,10 +647,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       const float4* nm4 = reinterpret_cast<const float4*>(S.nm + 8 * hh);
       // Rows that see a NaN value get NaN in its 16 values at the item's end: of tile i (unit u of the
       // item), a bit a row. What the values' warps left for it is there once its products are done,
-      // and stays until four tiles later.
+      // and stays until it has been read (see kNanTiles).
       auto nan_rows = [&](int i, int u) {
         uint32_t hits = 0;
-        if (S.nans[i & 3] != i + 1) return hits;
+        if (S.nans[i & (kNanTiles - 1)] != i + 1) return hits;
         for (int k = 0; k < 16; ++k) {
           const int r = 8 * (4 * (k >> 3) + hh) + (k & 7);
           if (r >= rows) break;
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
           for (int n = 0; n < 4; ++n) {
             const int here = seen - 32 * n;
             const uint32_t sees = here >= 32 ? 0xFFFFFFFFu : here > 0 ? (1u << here) - 1u : 0u;
-            if (S.nan[i & 3][tok >> 4][n] & sees) hits |= 1u << k;
+            if (S.nan[i & (kNanTiles - 1)][tok >> 4][n] & sees) hits |= 1u << k;
           }
         }
         return hits;

@@ -1,0 +1,65 @@
+"""Cache operators at the edges of their definitions: NaN values in prompts of many tiles."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines too
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
+from tests.test_parity_kv_gpu import BF16, dev  # noqa: E402
+
+
+@pytest.mark.parametrize("news", [[2500, 2300], [250, 640, 129, 510, 700, 384, 260, 255] * 4])
+def test_attention_nan_values_in_prompts_of_many_tiles(news):
+    """Prompts whose tiles of tokens are nearly all masked for some row, dozens of them in a CTA's run, with
+    NaN values in several: the rows that see one are NaN in its 16 values, all others are what they are
+    without it, and every call says the same."""
+    H, G, D, ps = 2, 2, 128, 32
+    g = torch.Generator("cuda").manual_seed(len(news))
+    r = np.random.default_rng(len(news))
+    T, B, blocks = sum(news), len(news), -(-max(news) // ps)
+    table = torch.randperm(B * blocks, device="cuda", generator=g).view(B, blocks)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    seq = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(news, device="cuda"))
+    at = torch.arange(T, device="cuda") - dev(cu)[seq]
+    slots = table[seq, at // ps] * ps + at % ps
+    k, v = (torch.randn(T, H, D, device="cuda", generator=g).to(BF16) for _ in "kv")
+    cache, clean = (sv.kv4_cache(B * blocks, H, D, ps) for _ in range(2))
+    sv.kv4_append(k, v, slots, clean, page_size=ps)
+    want = torch.zeros(T, H, D // 16, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        for _ in range(12):
+            t, h, s = int(r.integers(0, news[b])), int(r.integers(H)), int(r.integers(D // 16))
+            v[cu[b] + t, h, 16 * s + int(r.integers(16))] = math.nan
+            want[cu[b] + t:cu[b + 1], h, s] = True
+    sv.kv4_append(k, v, slots, cache, page_size=ps)
+    want = want.repeat_interleave(G, 1).repeat_interleave(16, 2)
+    assert 0.1 < float(want.float().mean()) < 0.9
+    q = torch.randn(T, H * G, D, device="cuda", generator=g).to(BF16)
+    lens, cu, table = dev(np.array(news)), dev(cu), table.int()
+
+    def call(c):
+        return sv.kv4_attention(q, c, table, lens, cu, page_size=ps, max_new=max(news))
+    ref = call(clean)
+    for _ in range(20):
+        o = call(cache)
+        assert torch.equal(o["out"].isnan(), want)
+        assert torch.equal(o["out"][~want], ref["out"][~want]) and torch.equal(o["lse"], ref["lse"])
+    # the clean call against float64, a few rows of each sequence
+    for b in range(min(B, 8)):
+        n, c0 = news[b], int(cu[b])
+        out = sv.kv4_append(k[c0:c0 + n], v[c0:c0 + n].nan_to_num(0.0), slots[c0:c0 + n],
+                            torch.empty_like(clean), page_size=ps, values=True)
+        for i in sorted({0, n - 1, *r.integers(0, n, 6).tolist()}):
+            for h in range(H * G):
+                K, V = out["k"][:i + 1, h // G].double(), out["v"][:i + 1, h // G].double()
+                fine = ~want[c0 + i, h]
+                p = (K @ q[c0 + i, h].double() * D ** -0.5).softmax(0)
+                y = p @ V
+                tol = 2.0 ** -8 * y.abs() + (p @ V.abs()) * 2.0 ** -9 + 2.0 ** -32 * V.abs().sum(0)
+                assert ((ref["out"][c0 + i, h].double() - y).abs() <= tol)[fine].all()
