@@ -98,12 +98,18 @@ __device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t (&r)[4]) {
       : "r"(w));
 }
 
-// 16 values -> 8 bytes of codes (value 2j low, 2j + 1 high, in byte j) and the scale's bits. The
-// quotients x / s are those of IEEE division. Where nothing can overflow (`plain`: the tensor scale is
-// within 2^+-60, so the scale s = e4m3 * g and 1 / s are normal, and |x| <= 7 s unless the block's scale
-// is held at 448) they come from one division for the block and Markstein's correction for
-// each value: with y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y), two fused operations, is RN(x / s)
-// (P. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
+// 16 values -> 8 bytes of codes (value 2j low, 2j + 1 high, in byte j) and the scale's bits. The codes
+// are those of the quotients x / s of IEEE division. Where nothing can overflow (`plain`: the tensor scale
+// is within 2^+-60, so the scale s = e4m3 * g and 1 / s are normal, and |x| < 9 s, the bound of the smallest
+// scale, unless the block's scale is held at 448) they come from one division for the block and
+// Markstein's correction for each value: with y = RN(1 / s) and q = RN(x y), RN(q + (x - q s) y), two
+// fused operations, is RN(x / s) if q is within a unit in the last place of x / s (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990). At the thresholds
+// between codes, whose mantissas are at most 1.75, x y is off by less than 0.9 units: where x / s lies next
+// to the middle of two floats, q is one of these two and the theorem holds. Elsewhere q may be off by 1.5
+// units and the corrected sum by 3 * 2^-24 units before its rounding, which reaches no middle. The sum is
+// written as q - (q s - x) y: it keeps the sign of a zero, as x / s does, where q + (x - q s) y gives +0
+// for x = -0.
 // 16 divisions made the kernel issue-bound: 65013 tokens of 8 heads took 149 us instead of 119.
 __device__ __forceinline__ uint2 quantise(const float (&x)[16], float inv6g, float g, bool plain,
                                           uint32_t* scale_bits) {
@@ -121,7 +127,7 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[16], float inv6g, flo
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float q = x[i] * y;
-        t[i] = fmaf(fmaf(-q, s, x[i]), y, q);
+        t[i] = fmaf(-fmaf(q, s, -x[i]), y, q);
       }
     } else {
 #pragma unroll

@@ -1,4 +1,5 @@
-"""Cache operators at the edges of their definitions: NaN values in prompts of many tiles."""
+"""Cache operators at the edges of their definitions: NaN values in prompts of many tiles, signed zeros
+and the smallest scales."""
 import math
 
 import numpy as np
@@ -11,7 +12,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines t
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
-from tests.test_parity_kv_gpu import BF16, dev  # noqa: E402
+from tests.test_parity_kv_gpu import BF16, F32, _check_append, dev  # noqa: E402
 
 
 @pytest.mark.parametrize("news", [[2500, 2300], [250, 640, 129, 510, 700, 384, 260, 255] * 4])
@@ -63,3 +64,38 @@ def test_attention_nan_values_in_prompts_of_many_tiles(news):
                 y = p @ V
                 tol = 2.0 ** -8 * y.abs() + (p @ V.abs()) * 2.0 ** -9 + 2.0 ** -32 * V.abs().sum(0)
                 assert ((ref["out"][c0 + i, h].double() - y).abs() <= tol)[fine].all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_keeps_the_sign_of_zero(dtype, D):
+    """-0.0 beside other values has the code of -0, as the quotient -0 / scale has: in pairs of tokens and
+    alone, with scales in and out of the range of the quotient's short form, and held at 448."""
+    def edit(k, v):
+        k[:, :, 1::3] = -0.0
+        v[:, :, ::2] = -0.0
+        v[:, :, 1::4] = 0.0
+        v[5, 0] *= 1e6  # scales held at 448
+    slots = [0, 1, 2, 5, 8, 9, 31]
+    for gk, gv in ((1.0, 0.5), (2.0 ** -70, 2.0 ** 70)):
+        _check_append(len(slots), 2, D, 16, dtype, slots, gk=gk, gv=gv, edit=edit)
+    k = torch.full((1, 1, D), -0.0, device="cuda", dtype=dtype)
+    k[..., ::16] = 3.0
+    out = sv.kv4_append(k, -k, dev([0], torch.int64), sv.kv4_cache(1, 1, D, 16), page_size=16, values=True)
+    for n, x in (("k", k), ("v", -k)):
+        assert torch.equal(out[n].float(), x.float()) and torch.equal(out[n].signbit(), x.signbit())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_append_smallest_scales(dtype):
+    """Blocks whose scale is one of the smallest, 2^-9 to 2^-6: there the largest value may be almost nine
+    times the scale, or nothing is left of the block."""
+    r = np.random.default_rng(4)
+    most = 6 * 2.0 ** -9 * np.array([0.4, 0.499, 0.501, 0.9, 1.2, 1.49, 1.51, 2.49, 2.51, 3.5, 7.4, 7.9])
+
+    def edit(k, v):
+        for x in (k, v):
+            y = r.uniform(-1, 1, (len(most), 1, 4, 16)) * most[:, None, None, None]
+            y[..., 3] = most[:, None, None]
+            x[:] = torch.from_numpy(y.reshape(len(most), 1, 64)).to(x)
+    _check_append(len(most), 1, 64, 16, dtype, np.arange(len(most)) + 1, gk=1.0, gv=1.0, edit=edit)
