@@ -105,7 +105,7 @@ sv_status spec_block_tables(int B, int page_size, int max_blocks, int max_tokens
  *   out_q, out_k: dtype, with token strides of their own; out_q == q and out_k == k (with the
  *      same strides) work in place, any other overlap does not
  * D is even and at most 512. The norm is held in float32; the angle is reduced as a 64-bit
- * fraction of a turn, exact to 2^-32 turns at any position.
+ * fraction of a turn, exact to 2^-32 turns at any position (|inv_freq| of 2^54 and more counts as 0).
  */
 sv_status spec_qk_norm_rope(int T, int Hq, int Hkv, int D, int rot, int interleaved,
                             sv_dtype dtype, const void* q, long long q_token_stride,

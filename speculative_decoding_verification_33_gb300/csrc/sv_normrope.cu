@@ -5,15 +5,15 @@
 // that both halves of each rotated pair are its own: vectors j and j + rot/2 for halves, two
 // neighbours for interleaved pairs. D / 16 bf16 threads share a head's sum of squares by
 // shuffles. A CTA takes a few tokens, computes their sines and cosines once, and runs through the
-// heads. 32767 tokens of 28 + 4 heads of 128 in bf16 take 98 us, 5.5 TB/s or 0.80 of the measured
+// heads. 32767 tokens of 28 + 4 heads of 128 in bf16 take 97 us, 5.5 TB/s or 0.81 of the measured
 // copy rate; 8 tokens 2.8 us, which is the launch; 1153 tokens of 16 + 2 heads of 64 in float32,
-// interleaved, 5.3 us (1.6 us of bytes: all of them fit the L2, the launch and one wave bound it).
+// interleaved, 5.4 us (1.6 us of bytes: all of them fit the L2, the launch and one wave bound it).
 //
 // The angle position * inv_freq needs more bits than float32 has (2^-24 of a position of 10^6 is
-// a twentieth of a turn) but only its fraction of a turn matters: inv_freq / 2 pi is held as a
-// 64-bit fixed-point fraction, whose product with the position, modulo 2^64, is that fraction,
-// exact to position * 2^-65 turns. The nearest quarter turn goes into signs, the rest, at most
-// an eighth, through sincospif.
+// a twentieth of a turn) but only its fraction of a turn matters: inv_freq / 2 pi is held as a 64-bit
+// fixed-point fraction of a turn, to nearest. Its product with the position, modulo 2^64, is the angle's
+// fraction, off by position * 2^-65 turns at most. The nearest quarter turn goes into signs, the rest, at
+// most an eighth and rounded to 2^-32 turns, through sincospif.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,11 +41,26 @@ struct NormRopeParams {
   int splits;   // CTAs that share a token group's heads
 };
 
-// Fraction of a turn per position, times 2^64.
+// Fraction of a turn per position, times 2^64, to nearest; 0 for |freq| >= 2^54. In integers: the 53 bits
+// of freq times the first 128 of 2 / pi (a quarter turn is pi / 2), of which 64 are taken from where freq's
+// exponent has them. In double the product's rounding, some 2^-56 turns for a frequency of 1, would be
+// 2^-25 turns at position 2^31, and with its error carried along 1153 tokens take 6.0 us instead of 5.4:
+// double arithmetic is slow here.
 __device__ __forceinline__ unsigned long long turn_fraction(double freq) {
-  double t = freq * 0.15915494309189533577;  // 1 / 2 pi
-  t -= rint(t);                              // whole turns a position do not matter; |t| <= 1/2
-  return static_cast<unsigned long long>(__double2ll_rn(t * 9223372036854775808.0)) << 1;
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(freq));
+  const int exponent = static_cast<int>(bits >> 52) & 0x7FF;  // freq = m 2^(exponent - 1075)
+  const unsigned long long m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+  const unsigned long long high = 0xA2F9836E4E441529ull, low = 0xFC2757D1F534DDC0ull;  // 2 / pi 2^128
+  const int at = 1140 - exponent;  // the result's bits of m * 2 / pi * 2^128, and one for rounding
+  if (at < 64 || at >= 192) return 0;
+  // bits 64 to 127 and 128 to 191
+  const unsigned long long p1 = m * high + __umul64hi(m, low);
+  const unsigned long long p2 = __umul64hi(m, high) + (p1 < m * high);
+  const unsigned long long a = at < 128 ? p1 : p2, b = at < 128 ? p2 : 0;
+  const int off = at & 63;
+  const unsigned long long g = (a >> off) | ((b << 1) << (63 - off));
+  const unsigned long long f = ((g >> 1) | ((b >> off) << 63)) + (g & 1);
+  return bits >> 63 ? 0 - f : f;
 }
 
 __device__ __forceinline__ float2 cos_sin(unsigned long long fraction, int pos) {

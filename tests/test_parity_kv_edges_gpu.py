@@ -1,5 +1,5 @@
 """Cache operators at the edges of their definitions: NaN values in prompts of many tiles, signed zeros
-and the smallest scales."""
+and the smallest scales, angles of far positions."""
 import math
 
 import numpy as np
@@ -12,7 +12,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines t
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
-from tests.test_parity_kv_gpu import BF16, F32, _check_append, dev  # noqa: E402
+from tests.test_parity_kv_gpu import BF16, F32, _check_append, dev, host  # noqa: E402
 
 
 @pytest.mark.parametrize("news", [[2500, 2300], [250, 640, 129, 510, 700, 384, 260, 255] * 4])
@@ -99,3 +99,51 @@ def test_append_smallest_scales(dtype):
             y[..., 3] = most[:, None, None]
             x[:] = torch.from_numpy(y.reshape(len(most), 1, 64)).to(x)
     _check_append(len(most), 1, 64, 16, dtype, np.arange(len(most)) + 1, gk=1.0, gv=1.0, edit=edit)
+
+
+def _inverse_of_two_pi(bits):
+    """1 / (2 pi) * 2^bits, from pi = 16 atan(1/5) - 4 atan(1/239) in integers."""
+    one = 1 << (bits + 64)
+
+    def atan(n):
+        total = term = one // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+    return (one << bits) // (2 * (16 * atan(5) - 4 * atan(239)))
+
+
+def _exact_turns(position, freq, bits=256):
+    """position * freq / (2 pi), less the nearest whole number of turns."""
+    n, d = float(freq).as_integer_ratio()
+    x = position * n * _INVERSE // d % (1 << bits)
+    return (x - (1 << bits) if x >> (bits - 1) else x) / 2 ** bits
+
+
+_INVERSE = _inverse_of_two_pi(256)
+
+
+@pytest.mark.parametrize("offset", [0, 1])  # 1: rows that are not 16-byte aligned, the general kernel
+@pytest.mark.parametrize("far", [1 << 16, 1 << 24, (1 << 31) - 1])
+def test_angles_of_far_positions(far, offset):
+    """Sines next to their zeros show the angle itself: off by at most 2^-32 turns at every position, with
+    frequencies above one too."""
+    r = np.random.default_rng(far % 1000 + offset)
+    T, half, D = 4096, 32, 64
+    pos = r.integers(-far, far + 1, T)
+    pos[:4] = [far, -far, far - 1, 1]
+    freq = np.array([10000.0 ** (-j / 28) for j in range(28)] + [3.7, 123.456, 1e5 / 3, 7e8])
+    base = torch.zeros(T, D + offset, device="cuda")
+    base[:, offset:offset + half] = 1.0
+    q = base[:, offset:].unflatten(1, (1, D))
+    o = host(sv.qk_norm_rope(q, None, dev(pos), torch.from_numpy(freq).cuda(), eps=0.0)["q"])[:, 0]
+    turns = np.array([[_exact_turns(int(p), f) for f in freq] for p in pos])
+    y = math.sqrt(2)
+    for x, want in ((o[:, :half], y * np.cos(2 * math.pi * turns)), (o[:, half:], y * np.sin(2 * math.pi * turns))):
+        # the norm and the rotation's own roundings as in test_norm_rope; 2^-32 turns of the angle
+        tol = np.abs(want) * ((D / 2 + 8) * 2.0 ** -24 + 2.0 ** -23) + y * 2 * math.pi * 2.0 ** -32
+        assert (np.abs(x - want) <= tol).all(), (np.abs(x - want) / tol).max()
+    assert (np.abs(turns) < 2.0 ** -12).sum() > 10  # places where the sine tells
