@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   const uint32_t tmem = S.tmem;
   const int tiles = static_cast<int>(S.run.u1 - S.run.u0);
   // Every wait has a limit. A role that met it waits no more and runs through to its end, so that
-  // nobody waits for it for good; what comes out is not used.
+  // nobody waits for it for good; what comes out is not used. It hands on nothing that somebody may still
+  // use: no stage whose copy may be on its way (raw_empty), no place of an item that is read.
   int tries = kWaitTries;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const uint32_t at = smem_u32(bar), p = parity & 1u;
@@ -324,6 +325,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
   auto arrive_warp = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
+  };
+  auto give_back = [&](int stage) {
+    __syncwarp();
+    if (lane == 0 && tries > 0) mbar_arrive(&S.raw_empty[stage]);
   };
 
   if (warp == 0) {
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
         for (int i = 0; i < 4; ++i)
           x[i] = *reinterpret_cast<const uint4*>(blk + (tok & 15) * 64 + 16 * (i ^ turn));
         const uint2 sc = *reinterpret_cast<const uint2*>(blk + KvBlock<D>::kKeyScales + (tok & 15) * 8);
-        arrive_warp(&S.raw_empty[stage]);
+        give_back(stage);
         auto swap = [&](uint4& a, uint4& c, bool s) {
           const uint4 y = a;
           a = make_uint4(s ? c.x : a.x, s ? c.y : a.y, s ? c.z : a.z, s ? c.w : a.w);
@@ -556,7 +561,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
           sc[i] = *reinterpret_cast<const uint16_t*>(src + scale_at + 16 * i);
         }
         const uint32_t lost = S.lost[t & 15];
-        arrive_warp(&S.raw_empty[stage]);
+        give_back(stage);
         if (t0 + kTcUnit > all_see || lost) {
           // see sv_attn.cu: what some row does not see must not reach it as 0 * NaN
           if (vid < 32) S.nan[t & (kNanTiles - 1)][vid >> 2][vid & 3] = 0;
@@ -610,17 +615,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(AttnParams P) {
       int unit = static_cast<int>(S.run.u0 - w.base), t = 0;
       for (int item = 0;; ++item) {
         if (item >= 2) wait(&S.q_empty[item & 1], (item >> 1) - 1);
-        TcItem& it = S.items[item & 3];
-        it.w = w;
-        it.unit = unit;
-        it.end = static_cast<int>(min(static_cast<long long>(w.nu), S.run.u1 - w.base));
-        it.rows = min(R, w.n * P.group - w.rt * R);
-        const int i0 = w.rt * R / P.group;
-        it.all_see = w.len - w.n + i0 + 1;
-        it.out0 = static_cast<long long>(w.r0 + i0) * P.hq + w.h * P.group;
-        it.whole = w.base >= S.run.u0 && it.end == w.nu;
+        const int end = static_cast<int>(min(static_cast<long long>(w.nu), S.run.u1 - w.base));
+        if (tries > 0) {
+          TcItem& it = S.items[item & 3];
+          it.w = w;
+          it.unit = unit;
+          it.end = end;
+          it.rows = min(R, w.n * P.group - w.rt * R);
+          const int i0 = w.rt * R / P.group;
+          it.all_see = w.len - w.n + i0 + 1;
+          it.out0 = static_cast<long long>(w.r0 + i0) * P.hq + w.h * P.group;
+          it.whole = w.base >= S.run.u0 && end == w.nu;
+        }
         mbar_arrive(&S.item_full[item & 3]);
-        t += it.end - unit;
+        t += end - unit;
         if (t >= tiles) break;
         next_item<TcWork>(P, w);
         unit = 0;
