@@ -26,8 +26,8 @@
 //
 // What bounds it is instructions, not bytes: for D = 128 a block of 16 tokens takes 64 conversions,
 // 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax. 524301
-// tokens of 8 heads take 115 us with 4 rows (5.3 TB/s, 0.78 of the measured copy rate), 168 with 16,
-// 218 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 90 us (0.34); one request
+// tokens of 8 heads take 114 us with 4 rows (5.3 TB/s, 0.78 of the measured copy rate), 169 with 16,
+// 216 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 88 us (0.35); one request
 // of 4097 tokens 11 us, most of it the way from the lengths to the pages, the bytes and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   uint32_t* my_lost = slost + pair * NS;
   long long (*my_queue)[NB] = s_queue[pair];
   int queued = 0;  // units of the queue that are copied
-  // Tries that are left to a wait. Once one has run out (<= 0), the thread waits no longer and issues no
-  // copies; -tries then is the parity, by stage, of the copies that were on their way.
+  int issued = 0;  // by this thread
+  // Tries that a wait has. Once one has run out, the thread waits no longer and issues no copies.
   int tries = kWaitTries;
   auto look_up = [&]() {
     const int bpp_log = 31 - __clz(P.ps >> 4);  // blocks of a page: a power of two
@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   auto issue = [&](int stage) {  // copy the next unit into the stage
     if (queued == 32) look_up();
     if (lane == 0 && tries > 0) {
+      ++issued;
       long long off[NB];
       uint32_t lost = 0;
       int n = 0;
@@ -410,8 +411,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           const uint32_t bar = smem_u32(&my_bar[stage]), parity = (phase >> stage) & 1u;
           for (int left = tries; !mbar_try(bar, parity);)
             if (--left <= 0) {  // a copy that never came: its rows are not used
-              // the spent stage's copy is done and the next one is not issued
-              if (tries > 0) tries = -static_cast<int>(spent < 0 ? phase : phase ^ (1u << spent));
+              tries = 0;
               break;
             }
           __syncwarp();
@@ -643,9 +643,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   }
   if (tries <= 0) {
     // no copy into this CTA's memory outlives it
-    if (h == 0 && lane == 0)
-      for (int i = 0; i < NS; ++i)
-        mbar_wait_bounded(&my_bar[i], (static_cast<uint32_t>(-tries) >> i) & 1u, kWaitCycles);
+    for (int i = max(0, issued - NS); i < issued; ++i)
+      mbar_wait_bounded(&my_bar[i % NS], (i / NS) & 1, kWaitCycles);
     atomicOr(P.err, 1u);
   }
 }
