@@ -83,7 +83,8 @@ size_t spec_kv4_page_bytes(int page_size, int D);
  *                      position and sequence of each token; -1, 0, -1 past the last one
  * Integers are int32 where nothing else is said. The outputs of lengths, held and counters must
  * be other buffers than the inputs (two sets in turn serve a loop): a call on the same inputs
- * writes the same values again. max_blocks * page_size must stay below 2^31.
+ * writes the same values again. max_blocks * page_size must stay below 2^31, max_tokens and
+ * ring_size below 2^31 - 1.
  */
 sv_status spec_block_tables(int B, int page_size, int max_blocks, int max_tokens,
                             const int32_t* ctx_lens, const int32_t* accept_len,

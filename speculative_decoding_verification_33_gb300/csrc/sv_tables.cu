@@ -12,6 +12,7 @@
 // tokens (4.8 MB of positions, slots and owners: 0.7 us of HBM). A launch that does nothing is
 // about 2.5 us of that.
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "spec_kv.h"
@@ -57,7 +58,7 @@ __device__ __forceinline__ Seq load_seq(const TablesParams& P, int b) {
   return s;
 }
 
-// Sums held at 2^31 - 1: no limit that they are compared with (free pages, token places) is larger,
+// Sums held at 2^31 - 1: every limit that they are compared with (free pages, token places) is smaller,
 // so what is past it stays past it.
 constexpr uint32_t kMost = 0x7FFFFFFFu;
 __device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) { return min(a + b, kMost); }
@@ -340,6 +341,8 @@ extern "C" sv_status spec_block_tables(
   }
   if (max_tokens > 0 && (!out_slots || !out_positions || !out_seq_ids)) return SV_ERR_INVALID_ARG;
   if (B > sv::kTablesMaxB) return SV_ERR_UNSUPPORTED;
+  // a sum held at 2^31 - 1 must be past its limit
+  if (max_tokens == INT_MAX || ring_size == INT_MAX) return SV_ERR_UNSUPPORTED;
   sv::TablesParams P;
   P.B = B;
   P.ps_log = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
