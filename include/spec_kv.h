@@ -152,8 +152,11 @@ sv_status spec_kv4_append(int T, int Hkv, int D, int page_size, int num_pages, s
  *   out bfloat16 [T][Hq][D] contiguous; out_lse float32 [T][Hq]: natural log of the softmax's
  *       sum, or NULL. Rows of no sequence are not written.
  * Scores, softmax and sums are held in float32; products take float16 operands: keys and values
- * are exact in it, queries too (scaled by a power of two), the softmax's weights are rounded to
- * it (by up to 2^-11 of each, or 2^-32 of the row's largest where that is more).
+ * are exact in it, queries too (each row scaled by a power of two; what is below 2^-28 of its
+ * largest value, or below 2^-116, is rounded), the softmax's weights are rounded to it (by up to
+ * 2^-11 of each, or 2^-32 of the row's largest where that is more).
+ * A tile of rows reads all tokens of its sequence, also those that none of its rows sees: of a
+ * prompt with nothing before it, half of the work is on those.
  */
 sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
                              int max_blocks, const void* q, long long q_token_stride,

@@ -24,8 +24,11 @@
 // Each pair streams its units through a ring in shared memory with bulk copies that it issues
 // itself; no barrier spans the pairs until a head ends, and then the SM's other CTA streams on.
 //
-// What bounds it is instructions, not bytes: for D = 128 a block of 16 tokens takes 64 conversions,
-// 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax. 524301
+// What bounds it with more than 8 rows is latency: a block of 16 tokens (D = 128) takes 64 conversions,
+// 64 products with scales and 16 matrix instructions a tile of 8 rows, besides the softmax, and 16 warps
+// an SM, in pairs that wait for one another twice a unit, have too little of it that is independent. With
+// 20 rows 55 % of the issue slots, 42 % of the tensor pipe's cycles and 0.41 of the copy rate are used;
+// most stalls are fixed latencies and the pairs' barriers. With 4 rows the bytes are near: 0.78. 524301
 // tokens of 8 heads take 114 us with 4 rows (5.3 TB/s, 0.78 of the measured copy rate), 169 with 16,
 // 216 with 20 (0.41); 64 sequences of up to 8192 tokens with 4 to 24 rows 88 us (0.35); one request
 // of 4097 tokens 11 us, most of it the way from the lengths to the pages, the bytes and the join.
@@ -53,7 +56,7 @@ struct AttnShape {
   static constexpr int kPerSm = 2;
   static constexpr int kRows = 8 * NT;
   // Blocks of a unit for each warp of a pair. With one tile of rows there are registers for two: half
-  // the barriers, 122 us instead of 135 for 524301 tokens of 8 heads and 4 rows, 58 instead of 61 for
+  // the barriers, 122 us (now 114) instead of 135 for 524301 tokens of 8 heads and 4 rows, 58 instead of 61 for
   // 64 sequences of up to 8192. With two tiles that takes 160 instead of 168 us and 75 instead of
   // 72.5, and for 256 sequences of up to 1024 tokens 78 instead of 68.
   static constexpr int kOwn = NT == 1 ? 2 : 1;

@@ -5,7 +5,7 @@
 // that both halves of each rotated pair are its own: vectors j and j + rot/2 for halves, two
 // neighbours for interleaved pairs. D / 16 bf16 threads share a head's sum of squares by
 // shuffles. A CTA takes a few tokens, computes their sines and cosines once, and runs through the
-// heads. 32767 tokens of 28 + 4 heads of 128 in bf16 take 97 us, 5.5 TB/s or 0.81 of the measured
+// heads. 32767 tokens of 28 + 4 heads of 128 in bf16 take 97 us, 5.5 TB/s or 0.82 of the measured
 // copy rate; 8 tokens 2.8 us, which is the launch; 1153 tokens of 16 + 2 heads of 64 in float32,
 // interleaved, 5.4 us (1.6 us of bytes: all of them fit the L2, the launch and one wave bound it).
 //

@@ -7,7 +7,7 @@
 // writes its share of the tokens and pages. Pages that this call puts back are never taken by
 // it, so no CTA reads a ring entry or a table entry that another one writes.
 //
-// On the device: 3.3 us for 8 sequences, 8.0 us for 1024 (their lengths are read by every CTA, in
+// On the device: 3.3 us for 8 sequences, 7.3 us for 1024 (their lengths are read by every CTA, in
 // chains of loads and scans that nothing shortens), 5.9 us for 256 with prompts of up to 16384
 // tokens (4.8 MB of positions, slots and owners: 0.7 us of HBM). A launch that does nothing is
 // about 2.5 us of that.
