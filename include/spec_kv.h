@@ -20,7 +20,9 @@
  * keeps that of the stream it was captured on, so its replays must not overlap other calls of
  * that stream, or replays of other graphs captured on it.
  *
- * Errors: arguments are checked on the host before anything is launched, as in spec_verify.h.
+ * Errors: arguments are checked on the host before anything is launched, as in spec_verify.h. A
+ * copy that spec_kv4_attention waits for in vain raises the stream's error word; what that call and
+ * later ones on the stream wrote is not valid until spec_verify_device_error has reported it.
  *
  * The cache. uint8 [num_pages][Hkv][page_size * (D + D/8)], 16-byte aligned: a page holds
  * page_size tokens (16, 32, 64 or 128) of every key/value head, D = 64 or 128 values a head, as
