@@ -9,7 +9,9 @@
  *   spec_block_tables   accepted lengths and new lengths -> pages, slots and positions;
  *   spec_qk_norm_rope   norms of queries and keys per head, and the position rotation;
  *   spec_kv4_append     keys and values of the new tokens into the cache, in 4 bits;
- *   spec_kv4_attention  causal attention of the new tokens over the cache.
+ *   spec_kv4_attention  causal attention of the new tokens over the cache;
+ *   spec_kv8_append, spec_kv8_attention   the same over a cache in 8 bits;
+ *   spec_prompt_attention  causal attention over whole prompts, from their keys and values.
  * The hidden states that follow go to spec_verify_hidden (or their logits to spec_verify), whose
  * out_accept_len is the accept_len of the next round's spec_block_tables.
  *
@@ -36,6 +38,19 @@
  *                                         and g ^ (4 (p / 2 % 2)) when D = 64;
  *   value scales  [8 token pairs][D/16][2 tokens].
  * A token's slot is page * page_size + its place in the page.
+ *
+ * The 8-bit cache. uint8 [num_pages][Hkv][page_size * (2 D + 1)], 16-byte aligned, with the same page
+ * sizes, D and slots. A value is code * 2^e, codes from -127 to 127, with one exponent e, of -60 to 121,
+ * for the keys and one for the values of a block of 16 tokens of a head: a power of two, so that
+ * products with it are exact, and every stored value is a bfloat16.
+ * A block is 32 D + 16 bytes, in this order,
+ *   key codes     [16 tokens][D]      a byte a value, code + 128; the D bytes of token i are chunks of
+ *                                     16, for D = 128 chunk j at place j ^ (i % 2);
+ *   value codes   [8 token pairs][D][2 tokens]  a byte a value, code + 128; the 2 D bytes of pair p are
+ *                                     chunks of 16, chunk j at place j ^ (2 (p % 4));
+ *   head          int8 e of the keys, int8 e of the values, 2 bytes, uint16 marks of the keys, uint16
+ *                 marks of the values, 8 bytes. Bit i of the marks: the key (or value) of token i held a
+ *                 NaN or an infinity and reads as NaN in all its D values.
  */
 #ifndef SPEC_KV_H
 #define SPEC_KV_H
@@ -166,6 +181,69 @@ sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size
                              const int32_t* kv_lens, const int32_t* cu_new, float scale,
                              float k_scale, float v_scale, int max_new, void* out,
                              float* out_lse, void* stream);
+
+/* Bytes of one page of one head of the 8-bit cache: page_size * (2 D + 1); 0 if not supported. */
+size_t spec_kv8_page_bytes(int page_size, int D);
+
+/*
+ * Keys and values of T tokens into the 8-bit cache. Keys and values are treated alike, each with its
+ * exponent and marks. For each block of 16 tokens and head that the call writes to, with a the largest
+ * magnitude among the values it brings (those of marked tokens left out),
+ *   need = the smallest e in -60..121 with a <= 127 * 2^e, or 121
+ *   e = need if the call writes the block's place 0 (a block afresh: places that the call does not
+ *       write get code 0 and no mark), else max(need, the block's e)
+ *   code = x * 2^-e, to nearest with ties to even, held at +-127; 0 for a marked token.
+ * Where e grows, the codes that the block holds at other places are rounded again:
+ * code * 2^(old e - e), to nearest with ties to even. So a block has to be begun at its place 0, as a
+ * sequence does; what a rolled-back token left behind is overwritten in place, and may leave e larger
+ * than the tokens that are kept would need.
+ *   k, v [T][Hkv][D] of dtype, rows as in spec_qk_norm_rope, 16-byte aligned (pointers, strides)
+ *   slots [T] int64: slot of each token; a token whose slot is outside 0..num_pages*page_size-1
+ *      is not written. The slots of one call are distinct, and the tokens of one block lie within 32
+ *      neighbouring ones, in any order among them, with none of another block between them (as in
+ *      out_slots of spec_block_tables); else the blocks in question hold any values.
+ *   out_k, out_v: NULL, or bfloat16 [T][Hkv][D], 16-byte aligned: the values that the cache now
+ *      stands for, written for every token; a token that is not written stands for a block of its own
+ */
+sv_status spec_kv8_append(int T, int Hkv, int D, int page_size, int num_pages, sv_dtype dtype,
+                          const void* k, long long k_token_stride, const void* v,
+                          long long v_token_stride, const int64_t* slots, void* cache, void* out_k,
+                          void* out_v, void* stream);
+
+/*
+ * Causal attention of each sequence's new tokens over the 8-bit cache: spec_kv4_attention with that
+ * cache and no tensor scales. A row that sees a token with a marked key is NaN, its log-sum too; one that
+ * sees a token with a marked value is NaN. Scores, softmax and sums are held in float32; products take
+ * float16 operands: codes are exact in it, queries as in spec_kv4_attention; the weights times 2^e of
+ * the values' block are rounded to it (by up to 2^-11 of each, or 2^-32 of the row's largest where that is
+ * more). The exponents of the blocks of values that a row sees should lie within 100 of one another; past
+ * that the weights of the small ones may count as 0 in its sum.
+ */
+sv_status spec_kv8_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
+                             int max_blocks, const void* q, long long q_token_stride,
+                             const void* cache, const int32_t* block_table,
+                             const int32_t* kv_lens, const int32_t* cu_new, float scale,
+                             int max_new, void* out, float* out_lse, void* stream);
+
+/*
+ * Causal attention over whole prompts, packed one behind the other: sequence b has the rows
+ * cu[b] .. cu[b+1] - 1 of q, k and v, and row i of it sees its rows 0 .. i.
+ * out = softmax(scale * q k^T) v over the tokens seen; tokens that a row does not see have no part in
+ * it, whatever they hold.
+ *   q   bfloat16 [T][Hq][D], k, v bfloat16 [T][Hkv][D], rows as in spec_qk_norm_rope, 16-byte aligned
+ *       (pointers, strides); Hq a multiple of Hkv, query head h reads key/value head h / (Hq / Hkv)
+ *   cu  [B+1] int32, ascending; entries are held to 0..T
+ *   scale: finite
+ *   out bfloat16 [T][Hq][D] contiguous, 16-byte aligned, no part of the inputs; out_lse float32 [T][Hq]:
+ *       natural log of the softmax's sum, or NULL. Rows of no sequence are not written.
+ * D is 64 or 128, Hq / Hkv at most 128. Products take bfloat16 operands, the softmax's weights rounded to
+ * it (by up to 2^-8 of each); scores, sums and outputs are held in float32. Like spec_kv4_attention it
+ * needs one call on the stream before a capture, and reports waits that ran out the same way.
+ */
+sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void* q,
+                                long long q_token_stride, const void* k, long long k_token_stride,
+                                const void* v, long long v_token_stride, const int32_t* cu,
+                                float scale, void* out, float* out_lse, void* stream);
 
 #ifdef __cplusplus
 }

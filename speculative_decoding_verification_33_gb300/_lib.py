@@ -22,7 +22,8 @@ EXPORTS = ("spec_verify", "spec_verify_workspace_bytes", "spec_verify_ws", "spec
            "spec_lmhead_stats", "spec_verify_hidden", "sv_hbm_read_probe", "sv_wait_probe",
            "spec_verify_workspace_error", "sv_wait_probe_at",
            "spec_block_tables", "spec_qk_norm_rope", "spec_kv4_page_bytes", "spec_kv4_append",
-           "spec_kv4_attention")
+           "spec_kv4_attention", "spec_kv8_page_bytes", "spec_kv8_append", "spec_kv8_attention",
+           "spec_prompt_attention")
 SV_PROBE_NOALLOC, SV_PROBE_WORKSPACE = 1, 2
 
 
@@ -90,9 +91,14 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
         lib.spec_kv4_append.argtypes = [_I] * 6 + [_P, _LL, _P, _LL, _P, _F, _F, _P, _P, _P, _P]
         lib.spec_kv4_attention.argtypes = [_I] * 8 + [_P, _LL, _P, _P, _P, _P, _F, _F, _F, _I, _P,
                                                       _P, _P]
+        lib.spec_kv8_page_bytes.argtypes = [_I, _I]
+        lib.spec_kv8_page_bytes.restype = _SZ
+        lib.spec_kv8_append.argtypes = [_I] * 6 + [_P, _LL, _P, _LL, _P, _P, _P, _P, _P]
+        lib.spec_kv8_attention.argtypes = [_I] * 8 + [_P, _LL, _P, _P, _P, _P, _F, _I, _P, _P, _P]
+        lib.spec_prompt_attention.argtypes = [_I] * 5 + [_P, _LL, _P, _LL, _P, _LL, _P, _F, _P, _P, _P]
         for name in EXPORTS:
             if name not in ("spec_verify_workspace_bytes", "spec_verify_status_string",
-                            "spec_kv4_page_bytes"):
+                            "spec_kv4_page_bytes", "spec_kv8_page_bytes"):
                 getattr(lib, name).restype = _I
         _lib = lib
         return lib

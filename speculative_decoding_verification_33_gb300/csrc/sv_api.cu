@@ -882,6 +882,87 @@ bool aligned16(const void* p, long long stride, size_t elt) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * static_cast<long long>(elt)) % 16 == 0;
 }
 
+// Arguments of attention over a paged cache, checked; B == 0 or T == 0 leaves the rest unset.
+sv_status cache_attention_params(sv::AttnParams* out_params, int B, int T, int Hq, int Hkv, int D, int page_size,
+                                 int num_pages, int max_blocks, const void* q, long long q_token_stride,
+                                 const void* cache, const int32_t* block_table, const int32_t* kv_lens,
+                                 const int32_t* cu_new, float scale, float k_scale, float v_scale,
+                                 int max_new, void* out, float* out_lse) {
+  if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || num_pages < 1 ||
+      max_blocks < 1 || max_new < 0)
+    return SV_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return SV_ERR_INVALID_ARG;
+  if (!sv::kv_page_size_ok(page_size) || !sv::kv_head_dim_ok(D)) return SV_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks) * page_size >= (1LL << 31)) return SV_ERR_INVALID_ARG;
+  if (q_token_stride < static_cast<long long>(Hq) * D) return SV_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return SV_OK;
+  if (!q || !cache || !block_table || !kv_lens || !cu_new || !out) return SV_ERR_INVALID_ARG;
+  if (!aligned16(q, q_token_stride, 2) || !aligned16(cache, 0, 1) || !aligned16(out, 0, 1))
+    return SV_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq >= (1LL << 31)) return SV_ERR_UNSUPPORTED;
+  sv::AttnParams& P = *out_params;
+  P.B = B;
+  P.T = T;
+  P.hq = Hq;
+  P.hkv = Hkv;
+  P.group = Hq / Hkv;
+  P.ps = page_size;
+  P.num_pages = num_pages;
+  P.max_blocks = max_blocks;
+  P.qs = q_token_stride;
+  P.q = q;
+  P.cache = static_cast<const unsigned char*>(cache);
+  P.table = block_table;
+  P.lens = kv_lens;
+  P.cu = cu_new;
+  P.c = static_cast<float>(static_cast<double>(scale) * static_cast<double>(k_scale) *
+                           1.4426950408889634);
+  P.vs = v_scale;
+  P.out = out;
+  P.lse = out_lse;
+  return SV_OK;
+}
+
+void set_workspace(sv::AttnParams* P, void* at) {
+  unsigned char* base = static_cast<unsigned char*>(at);
+  P->err = reinterpret_cast<unsigned*>(base);
+  P->arrived = reinterpret_cast<unsigned*>(base + 256);
+  P->part = reinterpret_cast<float*>(base + sv::kAttnHeader);
+}
+
+// launch(workspace, multiprocessors, stream) with the stream's attention workspace, which the first call
+// makes.
+template <class F>
+sv_status with_attention_workspace(void* stream, F launch) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
+    const int sms = sm_count(dev);
+    if (sms <= 0 || 2 * sms > sv::kAttnMaxCtas) return SV_ERR_CUDA;
+    StreamRes& r = g_res[{dev, s}];
+    if (!r.att) {  // one size for every call: a captured call's workspace never moves
+      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+      if (cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
+        return SV_ERR_UNSUPPORTED;  // the workspace must exist before capture
+      // The header starts at zero, set in this stream's order: the default stream's may lie behind
+      // work that this one does not wait for. Pieces are written before they are read.
+      void* w = nullptr;
+      if (cudaMalloc(&w, sv::attention_workspace_bytes(sms)) != cudaSuccess ||
+          cudaMemsetAsync(w, 0, sv::kAttnHeader, s) != cudaSuccess) {
+        if (w) cudaFree(w);
+        return SV_ERR_CUDA;
+      }
+      r.att = w;
+    }
+    return launch(r.att, sms, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  } catch (...) {
+    return SV_ERR_CUDA;  // no memory for the host's table
+  }
+}
+
 // Launch one row kernel over `units` rows / pairs with persistent CTAs (as many as fit on the
 // device, at most one per unit), on the stream's workspace (queue counters and error word). The
 // ring gets the most stages that still let two CTAs share an SM (at least 3); failing that, one
@@ -1111,69 +1192,69 @@ sv_status spec_kv4_attention(int B, int T, int Hq, int Hkv, int D, int page_size
                              const int32_t* kv_lens, const int32_t* cu_new, float scale,
                              float k_scale, float v_scale, int max_new, void* out,
                              float* out_lse, void* stream) {
-  if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || num_pages < 1 ||
-      max_blocks < 1 || max_new < 0)
+  sv::AttnParams P;
+  const sv_status st =
+      cache_attention_params(&P, B, T, Hq, Hkv, D, page_size, num_pages, max_blocks, q, q_token_stride, cache,
+                             block_table, kv_lens, cu_new, scale, k_scale, v_scale, max_new, out, out_lse);
+  if (st != SV_OK || B == 0 || T == 0) return st;
+  return with_attention_workspace(stream, [&](void* base, int sms, cudaStream_t s) {
+    set_workspace(&P, base);
+    return sv::launch_attention(P, D, max_new, sms, s);
+  });
+}
+
+sv_status spec_kv8_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
+                             int max_blocks, const void* q, long long q_token_stride,
+                             const void* cache, const int32_t* block_table,
+                             const int32_t* kv_lens, const int32_t* cu_new, float scale,
+                             int max_new, void* out, float* out_lse, void* stream) {
+  sv::AttnParams P;
+  const sv_status st =
+      cache_attention_params(&P, B, T, Hq, Hkv, D, page_size, num_pages, max_blocks, q, q_token_stride, cache,
+                             block_table, kv_lens, cu_new, scale, 1.f, 1.f, max_new, out, out_lse);
+  if (st != SV_OK || B == 0 || T == 0) return st;
+  return with_attention_workspace(stream, [&](void* base, int sms, cudaStream_t s) {
+    set_workspace(&P, base);
+    return sv::launch_attention8(P, D, max_new, sms, s);
+  });
+}
+
+sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void* q,
+                                long long q_token_stride, const void* k, long long k_token_stride,
+                                const void* v, long long v_token_stride, const int32_t* cu,
+                                float scale, void* out, float* out_lse, void* stream) {
+  if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return SV_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+  if (!sv::kv_head_dim_ok(D) || Hq / Hkv > 128) return SV_ERR_UNSUPPORTED;
+  const long long row = static_cast<long long>(Hkv) * D;
+  if (q_token_stride < static_cast<long long>(Hq) * D || k_token_stride < row || v_token_stride < row)
     return SV_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
-    return SV_ERR_INVALID_ARG;
-  if (!sv::kv_page_size_ok(page_size) || !sv::kv_head_dim_ok(D)) return SV_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_blocks) * page_size >= (1LL << 31)) return SV_ERR_INVALID_ARG;
-  if (q_token_stride < static_cast<long long>(Hq) * D) return SV_ERR_INVALID_ARG;
   if (B == 0 || T == 0) return SV_OK;
-  if (!q || !cache || !block_table || !kv_lens || !cu_new || !out) return SV_ERR_INVALID_ARG;
-  if (!aligned16(q, q_token_stride, 2) || !aligned16(cache, 0, 1) || !aligned16(out, 0, 1))
+  if (!q || !k || !v || !cu || !out) return SV_ERR_INVALID_ARG;
+  if (!aligned16(q, q_token_stride, 2) || !aligned16(k, k_token_stride, 2) || !aligned16(v, v_token_stride, 2) ||
+      !aligned16(out, 0, 1))
     return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * Hq >= (1LL << 31)) return SV_ERR_UNSUPPORTED;
-  sv::AttnParams P;
+  sv::PromptParams P;
   P.B = B;
   P.T = T;
   P.hq = Hq;
   P.hkv = Hkv;
   P.group = Hq / Hkv;
-  P.ps = page_size;
-  P.num_pages = num_pages;
-  P.max_blocks = max_blocks;
   P.qs = q_token_stride;
+  P.ks = k_token_stride;
+  P.vs = v_token_stride;
   P.q = q;
-  P.cache = static_cast<const unsigned char*>(cache);
-  P.table = block_table;
-  P.lens = kv_lens;
-  P.cu = cu_new;
-  P.c = static_cast<float>(static_cast<double>(scale) * static_cast<double>(k_scale) *
-                           1.4426950408889634);
-  P.vs = v_scale;
+  P.k = k;
+  P.v = v;
+  P.cu = cu;
+  P.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   P.out = out;
   P.lse = out_lse;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
-  try {
-    std::lock_guard<std::mutex> lock(g_mu);
-    const int sms = sm_count(dev);
-    if (sms <= 0 || 2 * sms > sv::kAttnMaxCtas) return SV_ERR_CUDA;
-    StreamRes& r = g_res[{dev, s}];
-    if (!r.att) {  // one size for every call: a captured call's workspace never moves
-      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(s, &cap) == cudaSuccess && cap != cudaStreamCaptureStatusNone)
-        return SV_ERR_UNSUPPORTED;  // the workspace must exist before capture
-      // The header starts at zero, set in this stream's order: the default stream's may lie behind
-      // work that this one does not wait for. Pieces are written before they are read.
-      void* w = nullptr;
-      if (cudaMalloc(&w, sv::attention_workspace_bytes(sms)) != cudaSuccess ||
-          cudaMemsetAsync(w, 0, sv::kAttnHeader, s) != cudaSuccess) {
-        if (w) cudaFree(w);
-        return SV_ERR_CUDA;
-      }
-      r.att = w;
-    }
-    unsigned char* base = static_cast<unsigned char*>(r.att);
-    P.err = reinterpret_cast<unsigned*>(base);
-    P.arrived = reinterpret_cast<unsigned*>(base + 256);
-    P.part = reinterpret_cast<float*>(base + sv::kAttnHeader);
-    return sv::launch_attention(P, D, max_new, sms, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
-  } catch (...) {
-    return SV_ERR_CUDA;  // no memory for the host's table
-  }
+  return with_attention_workspace(stream, [&](void* base, int sms, cudaStream_t s) {
+    P.err = static_cast<unsigned*>(base);
+    return sv::launch_prompt(P, D, sms, s);
+  });
 }
 
 const char* spec_verify_status_string(sv_status status) {

@@ -1,5 +1,5 @@
-// Shared by the cache operators (sv_tables.cu, sv_normrope.cu, sv_kv4.cu, sv_attn.cu): the layout of the
-// 4-bit cache and the host-side interface of the attention kernels.
+// Shared by the cache operators (sv_tables.cu, sv_normrope.cu, sv_kv4.cu, sv_kv8.cu, sv_attn.cu, ...): the
+// layouts of the 4-bit and the 8-bit cache and the host-side interface of the attention kernels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -28,6 +28,19 @@ struct KvBlock {
     return D == 128 ? g ^ ((p & 3) << 1) : g ^ (((p >> 1) & 1) << 2);
   }
 };
+
+// The same of the 8-bit cache.
+template <int D>
+struct Kv8Block {
+  static constexpr int kKeyCodes = 0;
+  static constexpr int kValCodes = 16 * D;
+  static constexpr int kHead = 32 * D;  // int8 exponents of keys and values; at 4 and 6 uint16 marks
+  static constexpr int kBytes = 32 * D + 16;
+  // place of 16-byte chunk j of token i's key codes, and of token pair p's value codes
+  static __host__ __device__ constexpr int key_place(int i, int j) { return D == 128 ? j ^ (i & 1) : j; }
+  static __host__ __device__ constexpr int val_place(int p, int j) { return j ^ ((p & 3) << 1); }
+};
+constexpr int kKv8Low = -60, kKv8High = 121;  // exponents
 
 #ifdef __CUDACC__
 // a / b for a >= 0, b > 0: the 64-bit division takes some hundred instructions, few calls need it
@@ -66,5 +79,20 @@ cudaError_t launch_attention_tc(const AttnParams& P, int sms, cudaStream_t strea
 size_t attention_workspace_bytes(int sms);
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream);
+// The same over the 8-bit cache (sv_attn8.cu); k_scale and v_scale count as 1.
+cudaError_t launch_attention8(const AttnParams& P, int D, int max_new, int sms, cudaStream_t stream);
+
+// Causal attention over whole prompts (sv_prompt.cu).
+struct PromptParams {
+  int B, T, hq, hkv, group;
+  long long qs, ks, vs;  // token strides in elements
+  const void *q, *k, *v;
+  const int32_t* cu;
+  float c;  // scale * log2(e)
+  void* out;
+  float* lse;
+  unsigned* err;
+};
+cudaError_t launch_prompt(const PromptParams& P, int D, int sms, cudaStream_t stream);
 
 }  // namespace sv

@@ -5,7 +5,9 @@ dtypes and strides are read from the tensors, which lie on the current device, o
 unless ``out`` supplies them.
 A round is ``block_tables`` -> (projections) -> ``qk_norm_rope`` -> ``kv4_append`` ->
 ``kv4_attention`` -> (the rest of the layer, the head) -> ``verify`` / ``verify_hidden``, whose
-``accept_len`` goes into the next round's ``block_tables``.
+``accept_len`` goes into the next round's ``block_tables``. ``kv8_append`` and ``kv8_attention`` take
+the places of the 4-bit pair over a cache in 8 bits; ``prompt_attention`` is a prompt's own attention,
+from its keys and values as they are, or as the cache holds them.
 """
 from __future__ import annotations
 
@@ -175,9 +177,10 @@ def kv4_cache(num_pages: int, heads: int, D: int, page_size: int, device="cuda")
     return torch.zeros(num_pages, heads, nbytes, dtype=torch.uint8, device=device)
 
 
-def _cache(cache: torch.Tensor, heads: int, D: int, page_size: int, at: Optional[int]) -> int:
+def _cache(cache: torch.Tensor, heads: int, D: int, page_size: int, at: Optional[int],
+           token_bytes: Optional[int] = None) -> int:
     if cache.dim() != 3 or cache.shape[1] != heads or \
-            cache.shape[2] != page_size * (D + D // 8):
+            cache.shape[2] != page_size * (token_bytes or D + D // 8):
         raise ValueError(f"cache {tuple(cache.shape)} is not [pages, {heads}, page bytes] for "
                          f"page_size {page_size}, D {D}")
     return _dev(cache, torch.uint8, cache.shape, "cache", at)
@@ -239,4 +242,101 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         _dev(out["out"], torch.bfloat16, (T, hq, D), "out", at),
         0 if lse is None else _dev(lse, torch.float32, (T, hq), "lse", at), _stream(stream, at))
     _lib._check(st, "spec_kv4_attention")
+    return out
+
+
+def kv8_page_bytes(page_size: int, D: int) -> int:
+    """Bytes of one page of one head of the 8-bit cache; 0 where the sizes are not supported."""
+    return int(_lib.load().spec_kv8_page_bytes(int(page_size), int(D)))
+
+
+def kv8_cache(num_pages: int, heads: int, D: int, page_size: int, device="cuda") -> torch.Tensor:
+    """An empty 8-bit cache: uint8 [num_pages, heads, kv8_page_bytes(page_size, D)]."""
+    nbytes = kv8_page_bytes(page_size, D)
+    if not nbytes:
+        raise ValueError("page_size must be 16, 32, 64 or 128 and D 64 or 128")
+    return torch.zeros(num_pages, heads, nbytes, dtype=torch.uint8, device=device)
+
+
+def kv8_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, *,
+               page_size: int, out: Optional[dict] = None, values: bool = False,
+               stream=None) -> dict:
+    """Write the keys and values of T tokens into the 8-bit cache at ``slots`` (``spec_kv8_append``).
+    ``k``, ``v`` [T, Hkv, D] bf16 or f32; ``slots`` [T] int64, -1 for a token that is not written;
+    tokens of one block of 16 lie together, as ``block_tables`` gives them. Returns {}, or with
+    ``values`` (or ``out``) {"k", "v"}: bf16, what the cache now stands for."""
+    T, H, D = k.shape
+    at = _device(k, "k")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must share shape and dtype")
+    if out is None:
+        out = {n: torch.empty((T, H, D), dtype=torch.bfloat16, device=k.device)
+               for n in ("k", "v")} if values else {}
+    kp, ks = _rows(k, "k", at)
+    vp, vs = _rows(v, "v", at)
+    st = _lib.load().spec_kv8_append(
+        T, H, D, page_size, cache.shape[0], _float_code(k, "k"), kp, ks, vp, vs,
+        _vec(slots, torch.int64, T, "slots", at), _cache(cache, H, D, page_size, at, 2 * D + 1),
+        _dev(out["k"], torch.bfloat16, (T, H, D), "out k", at) if out else 0,
+        _dev(out["v"], torch.bfloat16, (T, H, D), "out v", at) if out else 0, _stream(stream, at))
+    _lib._check(st, "spec_kv8_append")
+    return out
+
+
+def kv8_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                  kv_lens: torch.Tensor, cu_new: torch.Tensor, *, page_size: int,
+                  scale: Optional[float] = None, max_new: int = 1, out: Optional[dict] = None,
+                  stream=None) -> dict:
+    """Causal attention of the new tokens over the 8-bit cache (``spec_kv8_attention``); arguments
+    and results as in ``kv4_attention``, without tensor scales."""
+    T, hq, D = q.shape
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    at, B = _device(q, "q"), kv_lens.shape[0]
+    if block_table.dim() != 2 or cache.dim() != 3:
+        raise ValueError("block_table must be [B, max_blocks] and cache [pages, Hkv, page bytes]")
+    H = cache.shape[1]
+    if out is None:
+        out = {"out": torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device),
+               "lse": torch.empty((T, hq), dtype=torch.float32, device=q.device)}
+    qp, qs = _rows(q, "q", at)
+    lse = out.get("lse")
+    st = _lib.load().spec_kv8_attention(
+        B, T, hq, H, D, page_size, cache.shape[0], block_table.shape[1], qp, qs,
+        _cache(cache, H, D, page_size, at, 2 * D + 1),
+        _dev(block_table, torch.int32, (B, block_table.shape[1]), "block_table", at),
+        _vec(kv_lens, torch.int32, B, "kv_lens", at), _vec(cu_new, torch.int32, B + 1, "cu_new", at),
+        D ** -0.5 if scale is None else scale, max_new,
+        _dev(out["out"], torch.bfloat16, (T, hq, D), "out", at),
+        0 if lse is None else _dev(lse, torch.float32, (T, hq), "lse", at), _stream(stream, at))
+    _lib._check(st, "spec_kv8_attention")
+    return out
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, *,
+                     scale: Optional[float] = None, out: Optional[dict] = None,
+                     stream=None) -> dict:
+    """Causal attention over whole prompts, packed (``spec_prompt_attention``). ``q`` [T, Hq, D],
+    ``k``, ``v`` [T, Hkv, D] bf16, heads contiguous in a token; ``cu`` [B + 1] int32, where each
+    sequence's rows begin. ``scale`` defaults to 1 / sqrt(D). Returns {"out" [T, Hq, D] bf16,
+    "lse" [T, Hq] f32}; rows of no sequence are left as they are."""
+    T, hq, D = q.shape
+    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError(f"q, k and v must be bfloat16, got {q.dtype}, {k.dtype}, {v.dtype}")
+    at = _device(q, "q")
+    if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{T}, Hkv, {D}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    if out is None:
+        out = {"out": torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device),
+               "lse": torch.empty((T, hq), dtype=torch.float32, device=q.device)}
+    qp, qs = _rows(q, "q", at)
+    kp, ks = _rows(k, "k", at)
+    vp, vs = _rows(v, "v", at)
+    lse = out.get("lse")
+    st = _lib.load().spec_prompt_attention(
+        cu.numel() - 1, T, hq, k.shape[1], D, qp, qs, kp, ks, vp, vs,
+        _vec(cu, torch.int32, cu.numel(), "cu", at), D ** -0.5 if scale is None else scale,
+        _dev(out["out"], torch.bfloat16, (T, hq, D), "out", at),
+        0 if lse is None else _dev(lse, torch.float32, (T, hq), "lse", at), _stream(stream, at))
+    _lib._check(st, "spec_prompt_attention")
     return out
