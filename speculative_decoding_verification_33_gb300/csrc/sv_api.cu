@@ -1253,6 +1253,7 @@ sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void
   P.lse = out_lse;
   return with_attention_workspace(stream, [&](void* base, int sms, cudaStream_t s) {
     P.err = static_cast<unsigned*>(base);
+    P.queue = P.err + 16;
     return sv::launch_prompt(P, D, sms, s);
   });
 }

@@ -91,7 +91,8 @@ struct PromptParams {
   float c;  // scale * log2(e)
   void* out;
   float* lse;
-  unsigned* err;
+  // workspace: error word; counters of items fetched and of CTAs at their end (zero between calls)
+  unsigned *err, *queue;
 };
 cudaError_t launch_prompt(const PromptParams& P, int D, int sms, cudaStream_t stream);
 

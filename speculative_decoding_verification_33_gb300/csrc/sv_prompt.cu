@@ -1,25 +1,176 @@
-// Causal attention over whole prompts, packed (spec_prompt_attention).
+// Causal attention over whole prompts, packed (spec_prompt_attention), on the fifth-generation tensor cores.
 //
-// The row kernel: a warp takes one row of one query head and goes once over the tokens that the row sees,
-// 32 at a time, a lane a token for the scores and D / 32 values of the output, with the running maximum and
-// sum of the softmax.
+// A CTA takes two tiles of up to 128 rows (tokens x query heads of one key/value head, so that grouped heads
+// share what is loaded) and goes over the keys and values that they see, 128 tokens at a time:
+//   scores [128 rows x 128 tokens] = q [shared memory] k^T [shared memory]
+//   outputs [128 rows x D] += weights [tensor memory] v [shared memory]
+// with scores and outputs of both tiles in tensor memory. While the tensor cores work for one tile, the
+// softmax of the other runs: a thread a row, one pass with the running maximum and sum; the weights go back
+// over the scores as bfloat16. A row's maximum is moved only when a score exceeds it by 2^8, and only then
+// are outputs read back and scaled, by the row's own threads: the products before have ended by then, since
+// the next scores were issued behind them.
+//
+// One persistent CTA an SM, its warps specialised: eight take scores to weights, four take outputs to memory,
+// one issues products, one copies (TMA), one looks after values that no row may see, one fetches items. Items
+// come from a counter, in the order of their cost where that can be had, so that the last ones are short.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <mutex>
 
+#include "sv_attn.cuh"
 #include "sv_kv.h"
 #include "sv_ptx.cuh"
+#include "sv_tc.cuh"
 
 namespace sv {
 namespace {
 
-// Row `row` of the call, of query head `head`, whose sequence starts at r0; a warp calls it. q: the row as
-// float32 in shared memory, this warp's own.
+// ------------------------------------------------------------------------------------------
+// instructions
+// ------------------------------------------------------------------------------------------
+// 64 float32 columns of a thread's lane, from column t: asked for. They are there after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld64(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63"
+      "}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(t));
+}
+// (Nothing may be done with r in between.)
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+      :
+      : "memory");
+}
+// 32 columns of this warp's lanes from r, complete (for this thread) after tmem_wait_st.
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptors of shared-memory operands in the 128-byte swizzle, rows of 128 bytes in groups of eight, 1024
+// bytes apart. The high word is the same for all. The low word has the address, and the bytes between
+// slabs of 64 values (of an operand whose rows are the inner dimension, as the values').
+__device__ __forceinline__ uint32_t operand_lo(uint32_t saddr, uint32_t slab) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((slab >> 4) << 16);
+}
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// D[tmem] (+)= A[smem] B[smem]^T, one step of 16; issued by one thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kOperandHi)
+      : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kOperandHi)
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------------
+// rows for themselves
+// ------------------------------------------------------------------------------------------
+// A warp takes one row of one query head and goes once over the tokens that the row sees, 32 at a time, a lane
+// a token for the scores and D / 32 values of the output. Only rows next to values that are not finite and that
+// they must not see are taken so: a weight of 0 in a product does not keep these out.
+// Row `row` of the call, of query head `head`, whose sequence starts at r0. q: the row as float32 in shared
+// memory, this warp's own.
 template <int D>
-__device__ void prompt_row(const PromptParams& P, int r0, int row, int head, float* q) {
+__device__ __noinline__ void prompt_row(const PromptParams& P, int r0, int row, int head, float* q) {
   constexpr int V = D / 32;  // values of a lane
   const int lane = threadIdx.x & 31, hk = head / P.group;
   const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(P.q) + row * P.qs + static_cast<long long>(head) * D;
@@ -75,38 +226,647 @@ __device__ void prompt_row(const PromptParams& P, int r0, int row, int head, flo
   if (lane == 0 && P.lse) P.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// The first row of the sequence of row `row`, or -1 where it has none.
-__device__ int sequence_of(const PromptParams& P, int row) {
-  int lo = 0, hi = P.B;  // the first b with cu[b + 1] > row
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (P.cu[mid + 1] > row) hi = mid; else lo = mid + 1;
+
+// ------------------------------------------------------------------------------------------
+// the kernel
+// ------------------------------------------------------------------------------------------
+constexpr int kWarpOut = 8, kWarpMma = 12, kWarpCopy = 13, kWarpValues = 14;  // and items
+constexpr int kPromptThreads = 512;
+constexpr int kSeqs = 1024, kLevels = 1024;  // sequences and tiles of one that items are ordered for
+constexpr int kFixes = 64;
+
+template <int D>
+struct PromptShape {
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kSlab = 128 * 128;       // bytes of 128 rows of 64 values
+  static constexpr int kTile = kSlabs * kSlab;  // of queries, keys or values
+  static constexpr int kStages = 8 / kSlabs;    // of keys and values in turn: an even number
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+};
+
+// Two tiles of rows, a and b: tokens from `tok` of the sequence that starts at row r0; those of tile b follow.
+struct PromptItem {
+  int r0, n, head;  // sequence: first row, length; key/value head
+  int tok, last;    // first and last token of the item
+  int tiles[2];     // of keys, that a tile sees; 0: it has no rows
+  int end;          // no item: the last one
+};
+
+struct PromptShared {
+  uint64_t full[8], empty[8];                // keys and values
+  uint64_t q_full[2], q_free[2];             // queries of a tile
+  uint64_t s_full[2], p_full[2];             // scores; weights
+  uint64_t o_done[2], o_free[2];             // outputs of an item; read
+  uint64_t stat[2][2];                       // sums and maxima of a tile; tiles in turn use two
+  uint64_t item_full[4], item_free[4];
+  uint64_t clean[4];                         // an item's last values are fit for products
+  uint64_t end;
+  PromptItem items[4];
+  float sum[2][2][128], top[2][2][128];
+  float row[4][128];                         // a row's queries
+  int bad[4];                                // the last token of the item with a value that is not finite
+  int4 fix[kFixes];                          // rows to be taken for themselves
+  uint32_t tmem;
+  int fixes, levels, total;
+  int count[kLevels + 1], more[kLevels + 1], start[kLevels + 1], order[kSeqs];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ PromptParams P) {
+  using C = PromptShape<D>;
+  extern __shared__ unsigned char dsm[];
+  __shared__ __align__(16) PromptShared S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned char* sq = dsm + ((1024u - (smem_u32(dsm) & 1023u)) & 1023u);
+  unsigned char* ring = sq + 2 * C::kTile;
+  const int per = 128 / P.group;  // tokens of a tile
+
+  auto sequence = [&](int b, int& first, int& n) {
+    first = min(max(P.cu[b], 0), P.T);
+    n = min(max(P.cu[b + 1], first), P.T) - first;
+  };
+  auto tiles_of = [&](int b) {
+    int first, n;
+    sequence(b, first, n);
+    return (n + 2 * per - 1) / (2 * per);
+  };
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.empty[i], 1 + (i & 1));  // values: read by the warp that looks after them, too
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 1);
+      mbar_init(&S.q_free[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.o_done[i], 1);
+      mbar_init(&S.o_free[i], 4);
+      mbar_init(&S.stat[i][0], 4);
+      mbar_init(&S.stat[i][1], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.clean[i], 1);
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_free[i], 15);
+      S.items[i] = PromptItem{};
+      S.items[i].end = 1;  // what a role reads that gave up waiting
+    }
+    mbar_init(&S.end, 1);
+    fence_mbar_init();
+    S.fixes = 0;
+    S.levels = 0;
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
   }
-  if (lo == P.B) return -1;
-  const int first = max(P.cu[lo], 0);
-  return first <= row ? first : -1;
+  if (warp == kWarpMma) tmem_alloc(&S.tmem, 512);
+  for (int i = tid; i <= kLevels; i += kPromptThreads) S.count[i] = 0;
+  __syncthreads();
+
+  // ---- Items by cost: the tiles with most keys of all sequences first. Level t has the tile t of each
+  // sequence that has more than t of them; with the sequences in the order of their tiles, these are the
+  // first more[t], and start[t] is what levels above hold.
+  if (P.B <= kSeqs) {
+    for (int b = tid; b < P.B; b += kPromptThreads) {
+      const int t = tiles_of(b);
+      if (t > 0) atomicMax(&S.levels, t);
+      if (t > 0 && t <= kLevels) atomicAdd(&S.count[t], 1);
+    }
+    __syncthreads();
+    const int levels = S.levels;
+    if (levels <= kLevels && warp == 0) {
+      int seqs = 0, items = 0;  // with more tiles than the levels that are left
+      if (lane == 0) S.more[levels] = 0;
+      for (int t0 = levels - 1; t0 >= 0; t0 -= 32) {
+        const int t = t0 - lane;
+        int m = t >= 0 ? S.count[t + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int x = __shfl_up_sync(0xFFFFFFFFu, m, d);
+          if (lane >= d) m += x;
+        }
+        m = t >= 0 ? m + seqs : 0;
+        int i = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int x = __shfl_up_sync(0xFFFFFFFFu, i, d);
+          if (lane >= d) i += x;
+        }
+        if (t >= 0) {
+          S.more[t] = m;
+          S.start[t] = items + i - m;
+        }
+        seqs = __shfl_sync(0xFFFFFFFFu, m, min(31, t0));
+        items += __shfl_sync(0xFFFFFFFFu, i, 31);
+      }
+      if (lane == 0) S.total = items;
+      __syncwarp();
+      for (int t = lane; t <= levels; t += 32) S.count[t] = S.more[t];  // where the next of t tiles goes
+      __syncwarp();
+      for (int b0 = 0; b0 < P.B; b0 += 32) {
+        const int b = b0 + lane, t = b < P.B ? tiles_of(b) : 0;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, t);
+        const int at = S.count[t] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (t > 0) {
+          S.order[at] = b;
+          if ((same >> lane) == 1u) S.count[t] = at + 1;  // the last of them
+        }
+        __syncwarp();
+      }
+    }
+  }
+  const bool ordered = P.B <= kSeqs && S.levels <= kLevels;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  constexpr uint32_t kColO = 256;  // scores of the tiles at columns 0 and 128, outputs from here
+
+  // Every wait has a limit. A role that met it leaves; what comes out is not used.
+  int tries = kWaitTries;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const uint32_t at = smem_u32(bar), p = parity & 1u;
+    int left = tries;
+    while (!mbar_try(at, p))
+      if (--left <= 0) {
+        tries = 0;
+        break;
+      }
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    wait(bar, parity);
+    if (!__all_sync(0xFFFFFFFFu, tries > 0)) tries = 0;
+  };
+  auto arrive_warp = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  // The k-th item, or false at the end. `done` hands its place back.
+  auto item = [&](int k, PromptItem& it) {
+    wait_warp(&S.item_full[k & 3], k >> 2);
+    it = S.items[k & 3];
+    arrive_warp(&S.item_free[k & 3]);
+    return tries > 0 && !it.end;
+  };
+
+  if (warp < kWarpOut) {
+    // ---- scores to weights: a thread a row
+    more_registers<184>();
+    const int g = warp >> 2, row = tid & 127, i = row / P.group;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const uint32_t cols = tmem + lanes + 128 * g, outs = tmem + lanes + kColO + D * g;
+    const float c = P.c, fill = c < 0.f ? INFINITY : -INFINITY;
+    int phase = 0, use = 0;
+    PromptItem it;
+    for (int k = 0; item(k, it); ++k) {
+      const int first = it.tok + g * per, sees = min(first + i, it.last) + 1;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int j = 0; j < it.tiles[g] && tries > 0; ++j, ++phase) {
+        wait_warp(&S.s_full[g], phase);
+        tc_fence_after();
+        uint32_t r[128];
+        tmem_ld64(cols, r);
+        tmem_ld64(cols + 64, r + 64);
+        tmem_wait_ld(r);
+        tmem_wait_ld(r + 64);
+        if (128 * j + 127 > first) {  // some row does not see some of these
+          const int lim = sees - 128 * j;
+#pragma unroll
+          for (int n = 0; n < 128; ++n)
+            if (n >= lim) r[n] = __float_as_uint(fill);
+        }
+        float t;
+        if (c < 0.f) {
+          float x[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+          for (int n = 0; n < 128; n += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = min3(x[e], __uint_as_float(r[n + 2 * e]), __uint_as_float(r[n + 2 * e + 1]));
+          t = fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) * c;
+        } else {
+          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int n = 0; n < 128; n += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[e] = max3(x[e], __uint_as_float(r[n + 2 * e]), __uint_as_float(r[n + 2 * e + 1]));
+          t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
+        }
+        if (j == 0) {
+          m = t;
+        } else {
+          const bool move = t > m + 8.f;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            // the products before these scores are done: nobody else is at the outputs
+            const float down = move ? ex2_fast(m - t) : 1.f;
+            if (move) m = t;
+            l2.x *= down;
+            l2.y *= down;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              float o[32];
+              uint32_t w[32];
+              tmem_ld32(outs + d, o);
+#pragma unroll
+              for (int n = 0; n < 32; ++n) w[n] = __float_as_uint(o[n] * down);
+              tmem_st32(outs + d, w);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int n = 0; n < 32; ++n) {
+            const float2 z = make_float2(__uint_as_float(r[64 * h + 2 * n]), __uint_as_float(r[64 * h + 2 * n + 1]));
+            float2 p = fma2(z, c2, b2);
+            p.x = ex2_fast(p.x);
+            p.y = ex2_fast(p.y);
+            l2 = add2(l2, p);
+            w[n] = pack_bf16(p.x, p.y);
+          }
+          tmem_st32(cols + 32 * h, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive_warp(&S.p_full[g]);
+      }
+      if (it.tiles[g]) {
+        S.sum[use & 1][g][row] = l2.x + l2.y;
+        S.top[use & 1][g][row] = m;
+        arrive_warp(&S.stat[use & 1][g]);
+        ++use;
+      }
+    }
+  } else if (warp < kWarpMma) {
+    // ---- outputs to memory: a thread a row
+    fewer_registers<96>();
+    const int row = tid & 127, i = row / P.group;
+    const uint32_t outs = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
+    int use[2] = {0, 0};
+    for (int k = 0;; ++k) {
+      wait_warp(&S.item_full[k & 3], k >> 2);
+      const PromptItem it = S.items[k & 3];
+      if (tries <= 0 || it.end) break;
+      for (int g = 0; g < 2; ++g) {
+        if (!it.tiles[g]) continue;
+        const int u = use[g]++;
+        wait_warp(&S.stat[u & 1][g], u >> 1);
+        wait_warp(&S.o_done[g], u);
+        if (tries <= 0) break;
+        tc_fence_after();
+        const float l = S.sum[u & 1][g][row], m = S.top[u & 1][g][row];
+        const float inv = 1.f / l;
+        const int tok = it.tok + g * per + i, head = it.head * P.group + row - i * P.group;
+        const bool there = i < per && tok <= it.last;
+        const long long at = static_cast<long long>(it.r0 + tok) * P.hq + head;
+        __nv_bfloat16* to = static_cast<__nv_bfloat16*>(P.out) + at * D;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          float o[32];
+          tmem_ld32(outs + D * g + d, o);
+          if (d + 32 == D) {
+            tc_fence_before();
+            arrive_warp(&S.o_free[g]);
+          }
+          if (there) {
+#pragma unroll
+            for (int n = 0; n < 32; n += 8)
+              *reinterpret_cast<uint4*>(to + d + n) =
+                  make_uint4(pack_bf16(o[n] * inv, o[n + 1] * inv), pack_bf16(o[n + 2] * inv, o[n + 3] * inv),
+                             pack_bf16(o[n + 4] * inv, o[n + 5] * inv), pack_bf16(o[n + 6] * inv, o[n + 7] * inv));
+          }
+        }
+        if (there && P.lse) P.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+      }
+      wait_warp(&S.clean[k & 3], k >> 2);
+      if (tries <= 0) break;
+      const int bad = S.bad[k & 3];
+      arrive_warp(&S.item_free[k & 3]);  // and the places of that number elsewhere
+      if (bad > it.tok) {  // rows before that token
+        const int4 fix = make_int4(it.r0, it.tok, bad, it.head);
+        if (S.fixes < kFixes) {
+          named_sync(1, 128);
+          if (tid == 32 * kWarpOut) S.fix[S.fixes++] = fix;
+          named_sync(1, 128);
+        } else {
+          named_sync(1, 128);  // what these rows got from the products is written
+          for (int n = warp - kWarpOut; n < (bad - it.tok) * P.group; n += 4)
+            prompt_row<D>(P, it.r0, it.r0 + it.tok + n / P.group, it.head * P.group + n % P.group,
+                          S.row[warp - kWarpOut]);
+        }
+      }
+    }
+    if (tries > 0) {
+      named_sync(1, 128);
+      for (int f = 0; f < S.fixes; ++f) {
+        const int4 fix = S.fix[f];
+        for (int n = warp - kWarpOut; n < (fix.z - fix.y) * P.group; n += 4)
+          prompt_row<D>(P, fix.x, fix.x + fix.y + n / P.group, fix.w * P.group + n % P.group, S.row[warp - kWarpOut]);
+      }
+    }
+  } else {
+    fewer_registers<48>();
+    if (warp == kWarpMma) {
+      // ---- products, issued by an elected thread
+      constexpr uint32_t kScores = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
+      constexpr uint32_t kOutputs = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
+                                    (static_cast<uint32_t>(D / 8) << 17) | (8u << 24);
+      const uint32_t a_q = operand_lo(smem_u32(sq), 16), a_ring = operand_lo(smem_u32(ring), 16);
+      const uint32_t a_val = operand_lo(smem_u32(ring), C::kSlab);
+      int pos = 0, use[2] = {0, 0}, weights[2] = {0, 0};
+      auto scores = [&](int g, int p, bool last) {  // of the keys at place p of the ring
+        if (elect_one()) {
+          const uint32_t q = a_q + g * (C::kTile >> 4), k = a_ring + (p % C::kStages) * (C::kTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kSlab + 32 * (kk & 3)) >> 4;
+            mma_ss(tmem + 128 * g, q + off, k + off, kScores, kk > 0);
+          }
+          tc_commit(&S.s_full[g]);
+          if (last) tc_commit(&S.q_free[g]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](int p) {
+        if (elect_one()) tc_commit(&S.empty[p % C::kStages]);
+        __syncwarp();
+      };
+      auto wait_full = [&](int p) { wait_warp(&S.full[p % C::kStages], p / C::kStages); };
+      PromptItem it;
+      for (int k = 0; item(k, it); ++k) {
+        const int most = max(it.tiles[0], it.tiles[1]);
+        wait_full(pos);
+        for (int g = 0; g < 2; ++g) {
+          if (!it.tiles[g]) continue;
+          wait_warp(&S.q_full[g], use[g]);
+          if (tries <= 0) break;
+          tc_fence_after();
+          scores(g, pos, it.tiles[g] == 1);
+        }
+        if (tries <= 0) break;
+        release(pos);
+        for (int j = 0; j < most && tries > 0; ++j) {
+          const int keys = pos + 2 * j + 2, values = pos + 2 * j + 1;
+          for (int g = 0; g < 2; ++g) {
+            if (j >= it.tiles[g]) continue;
+            wait_full(values);
+            if (j == most - 1) wait_warp(&S.clean[k & 3], k >> 2);
+            wait_warp(&S.p_full[g], weights[g]++);
+            if (j == 0 && use[g] > 0) wait_warp(&S.o_free[g], use[g] - 1);
+            if (tries <= 0) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t v = a_val + (values % C::kStages) * (C::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts(tmem + kColO + D * g, tmem + 128 * g + 8 * kk, v + ((2048 * kk) >> 4), kOutputs, j > 0 || kk > 0);
+              if (j == it.tiles[g] - 1) tc_commit(&S.o_done[g]);
+            }
+            __syncwarp();
+            if (j + 1 < it.tiles[g]) {
+              wait_full(keys);
+              if (tries <= 0) break;
+              tc_fence_after();
+              scores(g, keys, j + 2 == it.tiles[g]);
+            }
+          }
+          if (tries <= 0) break;
+          release(values);
+          if (j + 1 < most) release(keys);
+        }
+        if (tries <= 0) break;
+        pos += 2 * most;
+        for (int g = 0; g < 2; ++g) use[g] += it.tiles[g] > 0;
+      }
+      // all products are done before the memory goes
+      if (elect_one()) tc_commit(&S.end);
+      __syncwarp();
+      if (!mbar_wait_bounded(&S.end, 0, kWaitCycles)) tries = 0;
+    } else if (warp == kWarpCopy) {
+      // ---- copies
+      int pos = 0, use[2] = {0, 0};
+      PromptItem it;
+      for (int k = 0; item(k, it); ++k) {
+        const int most = max(it.tiles[0], it.tiles[1]);
+        auto put = [&](const CUtensorMap* map, int z) {
+          const int stage = pos % C::kStages;
+          if (pos >= C::kStages) wait_warp(&S.empty[stage], pos / C::kStages - 1);
+          if (tries <= 0) return;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&S.full[stage], C::kTile);
+            for (int s = 0; s < C::kSlabs; ++s)
+              tma_load_3d(ring + stage * C::kTile + s * C::kSlab, map, 64 * s, it.head, z, &S.full[stage]);
+          }
+          __syncwarp();
+          ++pos;
+        };
+        auto queries = [&](int g) {
+          if (!it.tiles[g]) return;
+          if (use[g] > 0) wait_warp(&S.q_free[g], use[g] - 1);
+          if (tries <= 0) return;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&S.q_full[g], C::kSlabs * 128 * per * P.group);
+            for (int s = 0; s < C::kSlabs; ++s)
+              tma_load_3d(sq + g * C::kTile + s * C::kSlab, &mq, 64 * s, it.head * P.group, it.r0 + it.tok + g * per,
+                          &S.q_full[g]);
+          }
+          __syncwarp();
+          ++use[g];
+        };
+        put(&mk, it.r0);
+        queries(0);
+        queries(1);
+        put(&mv, it.r0);
+        for (int j = 1; j < most && tries > 0; ++j) {
+          put(&mk, it.r0 + 128 * j);
+          put(&mv, it.r0 + 128 * j);
+        }
+      }
+      // no copy is in flight when the CTA ends, whoever gave up
+      for (int p = max(0, pos - C::kStages); p < pos; ++p)
+        if (!mbar_wait_bounded(&S.full[p % C::kStages], (p / C::kStages) & 1, kWaitCycles)) tries = 0;
+      for (int g = 0; g < 2; ++g)
+        if (use[g] > 0 && !mbar_wait_bounded(&S.q_full[g], (use[g] - 1) & 1, kWaitCycles)) tries = 0;
+    } else if (warp == kWarpValues) {
+      // ---- values next to the rows' own tokens. Those behind the item's last token, which no row sees, are
+      // cleared; of those behind its first one the last that is not finite is noted.
+      int pos = 1;
+      PromptItem it;
+      for (int k = 0; item(k, it); ++k) {
+        const int most = max(it.tiles[0], it.tiles[1]);
+        int bad = -1;
+        for (int j = 0; j < most; ++j, pos += 2) {
+          const int stage = pos % C::kStages;
+          wait_warp(&S.full[stage], pos / C::kStages);
+          if (tries <= 0) break;
+          const int from = max(it.tok + 1 - 128 * j, 0), to = min(it.last + 1 - 128 * j, 128);
+          if (to > from || j == most - 1) {
+            unsigned char* tile = ring + stage * C::kTile + 16 * (lane & 7);
+            for (int r = (from & ~3) + (lane >> 3); r < 128; r += 4) {
+              uint32_t x = 0;
+#pragma unroll
+              for (int s = 0; s < C::kSlabs; ++s) {
+                uint4* at = reinterpret_cast<uint4*>(tile + s * C::kSlab + 128 * r);
+                if (r >= to) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  const uint4 w = *at;
+                  const uint32_t f = 0x7FFF7FFFu;
+                  x = __vmaxu2(x, __vmaxu2(__vmaxu2(w.x & f, w.y & f), __vmaxu2(w.z & f, w.w & f)));
+                }
+              }
+              if ((x & 0xFFFFu) >= 0x7F80u || (x >> 16) >= 0x7F80u)
+                if (r >= from) bad = max(bad, 128 * j + r);
+            }
+          }
+          if (j == most - 1) {
+            bad = __reduce_max_sync(0xFFFFFFFFu, bad);
+            if (lane == 0) S.bad[k & 3] = bad;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            arrive_warp(&S.clean[k & 3]);
+          }
+          arrive_warp(&S.empty[stage]);
+        }
+        if (tries <= 0) break;
+      }
+    } else {
+      // ---- items: the first one is this CTA's number, the others come from the counter
+      int b = 0, before = 0;  // without an order: sequences from b on, tiles of those before
+      for (int k = 0;; ++k) {
+        if (k >= 4) wait_warp(&S.item_free[k & 3], (k >> 2) - 1);
+        if (tries <= 0) break;
+        int i = blockIdx.x;
+        if (k > 0) {
+          if (lane == 0) i = gridDim.x + atomicAdd(&P.queue[0], 1u);
+          i = __shfl_sync(0xFFFFFFFFu, i, 0);
+        }
+        const int u = i / P.hkv;
+        int t = -1, seq = 0;  // tile of a sequence
+        if (ordered) {
+          if (u < S.total) {
+            int hi = S.levels - 1;  // the lowest level that starts at u or before; starts grow as levels fall
+            t = 0;
+            while (t < hi) {
+              const int mid = (t + hi) >> 1;
+              if (S.start[mid] <= u) hi = mid; else t = mid + 1;
+            }
+            seq = S.order[u - S.start[t]];
+          }
+        } else {
+          for (; b < P.B; b += 32) {
+            const int mine = b + lane < P.B ? tiles_of(b + lane) : 0;
+            int all = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const int x = __shfl_up_sync(0xFFFFFFFFu, all, d);
+              if (lane >= d) all += x;
+            }
+            const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + all > u);
+            if (past) {
+              const int at = __ffs(past) - 1;
+              seq = b + at;
+              t = before + __shfl_sync(0xFFFFFFFFu, all, at) - 1 - u;  // its last tile first
+              break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, all, 31);
+          }
+        }
+        if (lane == 0) {
+          PromptItem it{};
+          it.end = t < 0;
+          if (t >= 0) {
+            sequence(seq, it.r0, it.n);
+            it.head = i - u * P.hkv;
+            it.tok = 2 * per * t;
+            it.last = min(it.tok + 2 * per, it.n) - 1;
+            it.tiles[0] = min(it.tok + per - 1, it.last) / 128 + 1;
+            it.tiles[1] = it.tok + per <= it.last ? it.last / 128 + 1 : 0;
+          }
+          S.items[k & 3] = it;
+          mbar_arrive(&S.item_full[k & 3]);
+        }
+        __syncwarp();
+        if (t < 0) break;
+      }
+      // the last CTA to come here leaves the counter at zero
+      if (lane == 0 && atomicAdd(&P.queue[1], 1u) == gridDim.x - 1) {
+        P.queue[0] = 0;
+        P.queue[1] = 0;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (tries <= 0) atomicOr(P.err, 1u);
+}
+
+// A tensor [T][H][D] of bfloat16, read in boxes of 64 values, `heads` heads and `tokens` tokens.
+bool make_map3(CUtensorMap* m, const void* p, int T, int H, int D, long long stride, int heads, int tokens) {
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::once_flag once;
+  static EncodeFn encode = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<EncodeFn>(f);
+  });
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(PromptParams P) {
-  __shared__ float q[4][D];
-  const long long i = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (i >= static_cast<long long>(P.T) * P.hq) return;
-  const int row = static_cast<int>(i / P.hq), head = static_cast<int>(i % P.hq);
-  const int r0 = sequence_of(P, row);
-  if (r0 >= 0) prompt_row<D>(P, r0, row, head, q[threadIdx.x >> 5]);
+cudaError_t launch_prompt_dim(const PromptParams& P, int sms, cudaStream_t stream) {
+  using C = PromptShape<D>;
+  const int per = 128 / P.group;
+  CUtensorMap mq, mk, mv;
+  if (!make_map3(&mq, P.q, P.T, P.hq, D, P.qs, P.group, per) || !make_map3(&mk, P.k, P.T, P.hkv, D, P.ks, 1, 128) ||
+      !make_map3(&mv, P.v, P.T, P.hkv, D, P.vs, 1, 128))
+    return cudaErrorInvalidValue;
+  static bool ready[64] = {};  // per device: the attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  // no more items than full tiles and one more of each sequence
+  const long long items = (P.T / (2LL * per) + std::min(P.B, P.T)) * P.hkv;
+  const unsigned ctas = static_cast<unsigned>(std::min<long long>(sms, std::max(1LL, items)));
+  prompt_kernel<D><<<ctas, kPromptThreads, C::kSmem, stream>>>(mq, mk, mv, P);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptParams& P, int D, int, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(P.T) * P.hq;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (D == 64)
-    prompt_rows_kernel<64><<<grid, 128, 0, stream>>>(P);
-  else
-    prompt_rows_kernel<128><<<grid, 128, 0, stream>>>(P);
-  return cudaGetLastError();
+cudaError_t launch_prompt(const PromptParams& params, int D, int sms, cudaStream_t stream) {
+  PromptParams P = params;
+  if (P.c == 0.f) P.c = FLT_MIN;  // so that what is not seen stays so; scores count as nothing all the same
+  return D == 64 ? launch_prompt_dim<64>(P, sms, stream) : launch_prompt_dim<128>(P, sms, stream);
 }
 
 }  // namespace sv
