@@ -425,9 +425,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     PromptItem it;
     for (int k = 0; item(k, it); ++k) {
       const int first = it.tok + g * per, sees = min(first + i, it.last) + 1;
+      const int tiles = g ? it.tiles[1] : it.tiles[0];
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int j = 0; j < it.tiles[g] && tries > 0; ++j, ++phase) {
+      for (int j = 0; j < tiles && tries > 0; ++j, ++phase) {
         wait_warp(&S.s_full[g], phase);
         tc_fence_after();
         uint32_t r[128];
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_before();
         arrive_warp(&S.p_full[g]);
       }
-      if (it.tiles[g]) {
+      if (tiles) {
         S.sum[use & 1][g][row] = l2.x + l2.y;
         S.top[use & 1][g][row] = m;
         arrive_warp(&S.stat[use & 1][g]);
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else if (warp < kWarpMma) {
     // ---- outputs to memory: a thread a row
-    fewer_registers<96>();
+    fewer_registers<72>();
     const int row = tid & 127, i = row / P.group;
     const uint32_t outs = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
     int use[2] = {0, 0};
@@ -517,6 +518,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       wait_warp(&S.item_full[k & 3], k >> 2);
       const PromptItem it = S.items[k & 3];
       if (tries <= 0 || it.end) break;
+#pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (!it.tiles[g]) continue;
         const int u = use[g]++;
@@ -575,17 +577,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else {
-    fewer_registers<48>();
+    fewer_registers<72>();
     if (warp == kWarpMma) {
-      // ---- products, issued by an elected thread
+      // ---- products: one elected thread does it all. It is held up until nearly all products that it has
+      // issued are done, so that what it does between them leaves the tensor cores idle: waits that are over
+      // by then come first.
       constexpr uint32_t kScores = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
       constexpr uint32_t kOutputs = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
                                     (static_cast<uint32_t>(D / 8) << 17) | (8u << 24);
-      const uint32_t a_q = operand_lo(smem_u32(sq), 16), a_ring = operand_lo(smem_u32(ring), 16);
-      const uint32_t a_val = operand_lo(smem_u32(ring), C::kSlab);
-      int pos = 0, use[2] = {0, 0}, weights[2] = {0, 0};
-      auto scores = [&](int g, int p, bool last) {  // of the keys at place p of the ring
-        if (elect_one()) {
+      if (elect_one()) {
+        const uint32_t a_q = operand_lo(smem_u32(sq), 16), a_ring = operand_lo(smem_u32(ring), 16);
+        const uint32_t a_val = operand_lo(smem_u32(ring), C::kSlab);
+        uint32_t pos = 0, use[2] = {0, 0}, weights[2] = {0, 0};
+        auto scores = [&](int g, uint32_t p, bool last) {  // of the keys at place p of the ring
           const uint32_t q = a_q + g * (C::kTile >> 4), k = a_ring + (p % C::kStages) * (C::kTile >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -594,64 +598,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           tc_commit(&S.s_full[g]);
           if (last) tc_commit(&S.q_free[g]);
-        }
-        __syncwarp();
-      };
-      auto release = [&](int p) {
-        if (elect_one()) tc_commit(&S.empty[p % C::kStages]);
-        __syncwarp();
-      };
-      auto wait_full = [&](int p) { wait_warp(&S.full[p % C::kStages], p / C::kStages); };
-      PromptItem it;
-      for (int k = 0; item(k, it); ++k) {
-        const int most = max(it.tiles[0], it.tiles[1]);
-        wait_full(pos);
-        for (int g = 0; g < 2; ++g) {
-          if (!it.tiles[g]) continue;
-          wait_warp(&S.q_full[g], use[g]);
-          if (tries <= 0) break;
-          tc_fence_after();
-          scores(g, pos, it.tiles[g] == 1);
-        }
-        if (tries <= 0) break;
-        release(pos);
-        for (int j = 0; j < most && tries > 0; ++j) {
-          const int keys = pos + 2 * j + 2, values = pos + 2 * j + 1;
+        };
+        auto wait_full = [&](uint32_t p) { wait(&S.full[p % C::kStages], p / C::kStages); };
+        for (int k = 0;; ++k) {
+          wait(&S.item_full[k & 3], k >> 2);
+          const int tiles[2] = {S.items[k & 3].tiles[0], S.items[k & 3].tiles[1]}, end = S.items[k & 3].end;
+          mbar_arrive(&S.item_free[k & 3]);
+          if (end || tries <= 0) break;
+          const int most = max(tiles[0], tiles[1]);
+          wait_full(pos);
+#pragma unroll
           for (int g = 0; g < 2; ++g) {
-            if (j >= it.tiles[g]) continue;
-            wait_full(values);
-            if (j == most - 1) wait_warp(&S.clean[k & 3], k >> 2);
-            wait_warp(&S.p_full[g], weights[g]++);
-            if (j == 0 && use[g] > 0) wait_warp(&S.o_free[g], use[g] - 1);
+            if (!tiles[g]) continue;
+            wait(&S.q_full[g], use[g]);
             if (tries <= 0) break;
             tc_fence_after();
-            if (elect_one()) {
+            scores(g, pos, tiles[g] == 1);
+          }
+          if (tries <= 0) break;
+          tc_commit(&S.empty[pos % C::kStages]);
+          for (int j = 0; j < most; ++j) {
+            const uint32_t values = pos + 2 * j + 1, keys = values + 1;
+            wait_full(values);
+            if (j + 1 < most) wait_full(keys); else wait(&S.clean[k & 3], k >> 2);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              if (j >= tiles[g]) continue;
+              if (j == 0 && use[g] > 0) wait(&S.o_free[g], use[g] - 1);
+              wait(&S.p_full[g], weights[g]++);
+              if (tries <= 0) break;
+              tc_fence_after();
               const uint32_t v = a_val + (values % C::kStages) * (C::kTile >> 4);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 mma_ts(tmem + kColO + D * g, tmem + 128 * g + 8 * kk, v + ((2048 * kk) >> 4), kOutputs, j > 0 || kk > 0);
-              if (j == it.tiles[g] - 1) tc_commit(&S.o_done[g]);
+              if (j + 1 < tiles[g])
+                scores(g, keys, j + 2 == tiles[g]);
+              else
+                tc_commit(&S.o_done[g]);
             }
-            __syncwarp();
-            if (j + 1 < it.tiles[g]) {
-              wait_full(keys);
-              if (tries <= 0) break;
-              tc_fence_after();
-              scores(g, keys, j + 2 == it.tiles[g]);
-            }
+            if (tries <= 0) break;
+            tc_commit(&S.empty[values % C::kStages]);
+            if (j + 1 < most) tc_commit(&S.empty[keys % C::kStages]);
           }
           if (tries <= 0) break;
-          release(values);
-          if (j + 1 < most) release(keys);
+          pos += 2 * most;
+          use[0] += tiles[0] > 0;
+          use[1] += tiles[1] > 0;
         }
-        if (tries <= 0) break;
-        pos += 2 * most;
-        for (int g = 0; g < 2; ++g) use[g] += it.tiles[g] > 0;
+        // all products are done before the memory goes
+        tc_commit(&S.end);
+        if (!mbar_wait_bounded(&S.end, 0, kWaitCycles)) tries = 0;
       }
-      // all products are done before the memory goes
-      if (elect_one()) tc_commit(&S.end);
       __syncwarp();
-      if (!mbar_wait_bounded(&S.end, 0, kWaitCycles)) tries = 0;
     } else if (warp == kWarpCopy) {
       // ---- copies
       int pos = 0, use[2] = {0, 0};
