@@ -20,7 +20,7 @@ LIB_NAME = "libspecverify.so"
 SOURCES = ["sv_kernel.cu", "sv_api.cu", "sv_probe.cu", "sv_rows.cu", "sv_lmhead.cu",
            "sv_hverify.cu", "sv_greedy.cu", "sv_small.cu", "sv_tables.cu", "sv_normrope.cu",
            "sv_kv4.cu", "sv_attn.cu", "sv_attn_tc.cu", "sv_kv8.cu", "sv_attn8.cu",
-           "sv_prompt.cu"]
+           "sv_attn8_tc.cu", "sv_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -67,7 +67,8 @@ KERNEL_SOURCES = {
     "attention": ("sv_attn.cu", "sv_attn_mma.cuh", "sv_attn.cuh", "sv_kv.h", "sv_ptx.cuh"),
     "append8": ("sv_kv8.cu", "sv_kv.h", "sv_ptx.cuh"),
     "attention8": ("sv_attn8.cu", "sv_attn_mma.cuh", "sv_attn.cuh", "sv_kv.h", "sv_ptx.cuh"),
-    "prompt": ("sv_prompt.cu", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
+    "attention8_tc": ("sv_attn8_tc.cu", "sv_tc_attn.cuh", "sv_attn.cuh", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
+    "prompt": ("sv_prompt.cu", "sv_tc_attn.cuh", "sv_attn.cuh", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
     "attention_tc": ("sv_attn_tc.cu", "sv_attn.cuh", "sv_kv.h", "sv_tc.cuh", "sv_ptx.cuh"),
 }
 

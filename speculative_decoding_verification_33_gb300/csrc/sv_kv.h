@@ -81,6 +81,7 @@ cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream);
 // The same over the 8-bit cache (sv_attn8.cu); k_scale and v_scale count as 1.
 cudaError_t launch_attention8(const AttnParams& P, int D, int max_new, int sms, cudaStream_t stream);
+cudaError_t launch_attention8_tc(const AttnParams& P, int D, int sms, cudaStream_t stream);  // sv_attn8_tc.cu
 
 // Causal attention over whole prompts (sv_prompt.cu).
 struct PromptParams {
