@@ -23,6 +23,7 @@
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "spec_kv.h"
 #include "sv_attn.cuh"
@@ -94,6 +95,27 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   return r;
 }
 
+// Loads and stores at a register's address plus a constant
+template <int off>
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at), "n"(off));
+  return v;
+}
+template <int off>
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0+%1], {%2, %3, %4, %5};" ::"r"(at), "n"(off), "r"(a), "r"(b), "r"(c), "r"(d));
+}
+// f(0), ..., f(N - 1) with constants as arguments
+template <int... I, class F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N>
+using Upto = std::make_integer_sequence<int, N>;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_constant__ AttnParams P) {
   using C = Shape8<D>;
@@ -161,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
 
   if (warp < kWarpUnpack) {
     // ---- scores to weights: a thread a row, units of one stream
-    more_registers<168>();
+    more_registers<176>();
     const int g = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t cols = tmem + lanes + 128 * g, outs = tmem + lanes + kColO;
@@ -183,32 +205,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         wait_warp(&S.s_full[g], phase);
         if (tries <= 0) break;
         tc_fence_after();
-        uint32_t r[128];
-        tmem_ld64(cols, r);
-        tmem_ld64(cols + 64, r + 64);
         const float4* heads = S.heads[(unit0 + u) & 7];
         const int lim = sees - kUnit * (first_unit + u);
-        tmem_wait_ld(r);
-        tmem_wait_ld(r + 64);
+        const bool masked = kUnit * (first_unit + u + 1) > all_see;  // some row does not see some of these
+        // The row's factor of block b: held, so that a sum of 0 stays 0; what is past that decides the
+        // softmax by itself
+        auto factor = [&](float keys) { return fminf(fmaxf(qc * keys, -1.2676506e30f), 1.2676506e30f); };
+        // Once for the maximum, half of the columns at a time, and once for the weights: both halves at
+        // once, or read once, leave the compiler short of registers.
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         uint32_t marks = 0;
+        auto maxima = [&](int half, auto masked) {
+          uint32_t r[64];
+          tmem_ld64(cols + 64 * half, r);
+          float4 h[4];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float4 h = heads[b];
-          marks |= __float_as_uint(h.w);
-          // held, so that a sum of 0 stays 0; what is past that decides the softmax by itself
-          const float f = fminf(fmaxf(qc * h.x, -1.2676506e30f), 1.2676506e30f);
-          const float2 f2 = make_float2(f, f), e2 = make_float2(h.y, h.y);
+          for (int b = 0; b < 4; ++b) h[b] = heads[4 * half + b];
+          tmem_wait_ld(r);
 #pragma unroll
-          for (int n = 16 * b; n < 16 * b + 16; n += 2) {
-            const float2 z = fma2(make_float2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), f2, e2);
-            r[n] = __float_as_uint(z.x);
-            r[n + 1] = __float_as_uint(z.y);
+          for (int b = 0; b < 4; ++b) {
+            marks |= __float_as_uint(h[b].w);
+            const float f = factor(h[b].x);
+            const float2 f2 = make_float2(f, f), e2 = make_float2(h[b].y, h[b].y);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const int at = 16 * b + 2 * n;
+              float2 z = fma2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f2, e2);
+              if constexpr (masked) {
+                if (64 * half + at >= lim) z.x = -INFINITY;
+                if (64 * half + at + 1 >= lim) z.y = -INFINITY;
+              }
+              x[n & 3] = max3(x[n & 3], z.x, z.y);
+            }
           }
-        }
-        if (kUnit * (first_unit + u + 1) > all_see) {  // some row does not see some of these
-#pragma unroll
-          for (int n = 0; n < 128; ++n)
-            if (n >= lim) r[n] = 0xFF800000u;
+        };
+        if (masked) {
+          maxima(0, std::true_type());
+          maxima(1, std::true_type());
+        } else {
+          maxima(0, std::false_type());
+          maxima(1, std::false_type());
         }
         if (marks) {
           for (int b = 0; b < 8; ++b) {
@@ -219,12 +255,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
             if ((w >> 16) & seen) poison = NAN;
           }
         }
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < 128; n += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = max3(x[e], __uint_as_float(r[n + 2 * e]), __uint_as_float(r[n + 2 * e + 1]));
         const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         const bool move = top - m > kSlack;
         if (u < 2) {
@@ -245,26 +275,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
             tmem_st32(outs + D * g + d, w);
           }
         }
-        const float2 m2 = make_float2(-m, -m);
+        // Far from 0 the score that was rounded for the maximum is not the one that a fused operation has here.
+        const bool far = row < rows && fabsf(m) > 1048576.f && m > -FLT_MAX;
+        auto weights = [&](int half, auto masked, auto rounded) {
+          uint32_t r[64], w[32];
+          tmem_ld64(cols + 64 * half, r);
+          float4 h[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
+          for (int b = 0; b < 4; ++b) h[b] = heads[4 * half + b];
+          tmem_wait_ld(r);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const float undo = heads[4 * half + b].z;
+            const float f = factor(h[b].x), e = rounded && far ? h[b].y : h[b].y - m;
+            const float2 f2 = make_float2(f, f), e2 = make_float2(e, e);
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-              const int at = 64 * half + 16 * b + 2 * n;
-              float2 p = add2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), m2);
-              p.x = ex2_fast(p.x);
-              p.y = ex2_fast(p.y);
-              sum = add2(sum, p);
-              w[8 * b + n] = pack_f16x2(p.x, p.y);
+              const int at = 16 * b + 2 * n;
+              float2 z = fma2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f2, e2);
+              if constexpr (masked) {
+                if (64 * half + at >= lim) z.x = -INFINITY;
+                if (64 * half + at + 1 >= lim) z.y = -INFINITY;
+              }
+              if constexpr (rounded) z = add2(z, far ? make_float2(-m, -m) : make_float2(0.f, 0.f));
+              z.x = ex2_fast(z.x);
+              z.y = ex2_fast(z.y);
+              sum = add2(sum, z);
+              w[8 * b + n] = pack_f16x2(z.x, z.y);
             }
-            l2 = fma2(sum, make_float2(undo, undo), l2);
+            l2 = fma2(sum, make_float2(h[b].z, h[b].z), l2);
           }
           tmem_st32(cols + 32 * half, w);
+        };
+        if (__any_sync(0xFFFFFFFFu, far)) {
+          weights(0, std::true_type(), std::true_type());
+          weights(1, std::true_type(), std::true_type());
+        } else if (masked) {
+          weights(0, std::true_type(), std::false_type());
+          weights(1, std::true_type(), std::false_type());
+        } else {
+          weights(0, std::false_type(), std::false_type());
+          weights(1, std::false_type(), std::false_type());
         }
         tmem_wait_st();
         tc_fence_before();
@@ -340,8 +391,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
     }
   } else if (warp < kWarpMma) {
     // ---- codes (and queries) to operands
-    fewer_registers<104>();
+    fewer_registers<96>();
     const int wid = warp - kWarpUnpack;
+    // Where this thread's 16-byte chunks of codes lie, and what they become: D / 16 of keys (16 values of a token)
+    // and of values (8 of a pair of tokens), of the blocks 2 wid and 2 wid + 1. Eight lanes in a row keep the banks
+    // apart, of the bytes that they read and of the operands that they write. D = 128: what the places are
+    // exchanged with depends on a chunk's number by a bit.
+    constexpr int N = D / 16;
+    const uint32_t a_raw = smem_u32(raws), a_ring = smem_u32(ring);
+    uint32_t key_from, key_to, value_from, value_to;
+    {
+      const int row = D == 128 ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane >> 2;  // of 4 or 8 at a time
+      const int j = D == 128 ? (lane & 3) + 4 * (((lane >> 2) ^ (lane >> 3)) & 1) : lane & 3;
+      key_from = (32 * wid + row) * D + 16 * B::key_place(row, j);
+      key_to = (j >> 2) * C::kSlab + (32 * wid + row) * 128 + (((2 * (j & 3)) ^ row) << 4);
+      constexpr int PV = D / 8;  // chunks of a pair
+      const int pair = lane / PV, x = lane % PV;
+      value_from = (16 * wid + pair) * 2 * D + 16 * B::val_place(pair, x);
+      value_to = (x >> 3) * C::kSlab + (16 * wid + pair) * 256 + (((x & 7) ^ (2 * pair)) << 4);
+    }
     uint32_t raw = 0, pos = 0, unit0 = 0, used = 0;
     for (int k = 0;; ++k) {
       wait_warp(&S.item_full[k & 3], k >> 2);
@@ -394,84 +462,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         fence_async_shared();
         arrive_warp(&S.full[pos++ % C::kStages]);
       };
-      constexpr int N = D / 16;  // 16-byte chunks of a thread
       for (int u = 0; u <= units; ++u) {
         if (u < units) {
           begin();
           if (tries <= 0) break;
-          const unsigned char* src = raws + (raw % C::kRaws) * C::kRaw;
-          unsigned char* dst = ring + (pos % C::kStages) * C::kTile;
+          const uint32_t src = a_raw + (raw % C::kRaws) * C::kRaw, dst = a_ring + (pos % C::kStages) * C::kTile;
           const uint2 gone = S.absent[(unit0 + u) & 15];
-          const uint32_t none = gone.x | gone.y;
+          const uint32_t none = ((gone.x | gone.y) >> (2 * wid)) & 3u;
           if (lane < 2) {
-            const int b = 2 * wid + lane;
-            uint2 h = *reinterpret_cast<const uint2*>(src + 8 * 16 * D + 16 * b);
-            if ((none >> b) & 1u) h = make_uint2(0u, (gone.x >> b) & 1u ? 0xFFFFu : 0u);  // without a page: marked keys
+            uint2 h = *reinterpret_cast<const uint2*>(raws + (raw % C::kRaws) * C::kRaw + 8 * 16 * D + 16 * (2 * wid + lane));
+            if ((none >> lane) & 1u)  // without a page: marked keys
+              h = make_uint2(0u, (gone.x >> (2 * wid + lane)) & 1u ? 0xFFFFu : 0u);
             const int ek = static_cast<signed char>(h.x & 0xFFu), ev = static_cast<signed char>((h.x >> 8) & 0xFFu);
-            S.heads[(unit0 + u) & 7][b] = make_float4(__int_as_float((ek + 127) << 23), static_cast<float>(ev),
-                                                      __int_as_float((127 - ev) << 23), __uint_as_float(h.y));
+            S.heads[(unit0 + u) & 7][2 * wid + lane] =
+                make_float4(__int_as_float((ek + 127) << 23), static_cast<float>(ev), __int_as_float((127 - ev) << 23),
+                            __uint_as_float(h.y));
           }
           uint4 c[N];
-          int row[N], j;
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            // eight lanes in a row: keep the banks apart, of the bytes read and of the operands written
-            if (D == 128) {
-              row[n] = 32 * wid + 4 * n + 2 * (lane >> 4) + ((lane >> 2) & 1);
-              j = (lane & 3) + 4 * (((lane >> 2) ^ (lane >> 3)) & 1);
-            } else {
-              row[n] = 32 * wid + 8 * n + (lane >> 2);
-              j = lane & 3;
-            }
-            c[n] = *reinterpret_cast<const uint4*>(src + row[n] * D + 16 * B::key_place(row[n], j));
+          each(Upto<N>(), [&](auto n_) { c[n_] = ld_shared_v4<n_ * 512>(src + key_from); });
+          if (none) {
+            each(Upto<N>(), [&](auto n_) {
+              constexpr int n = n_;
+              if ((none >> (n >= N / 2)) & 1u) c[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+            });
           }
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            uint32_t f[8] = {code_pair<0x4140>(c[n].x), code_pair<0x4342>(c[n].x), code_pair<0x4140>(c[n].y),
-                             code_pair<0x4342>(c[n].y), code_pair<0x4140>(c[n].z), code_pair<0x4342>(c[n].z),
-                             code_pair<0x4140>(c[n].w), code_pair<0x4342>(c[n].w)};
-            if (none && ((none >> (row[n] >> 4)) & 1u)) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = 0u;
-            }
-            unsigned char* to = dst + (j >> 2) * C::kSlab + row[n] * 128;
-            const int p = ((2 * (j & 3)) ^ (row[n] & 7)) << 4;
-            *reinterpret_cast<uint4*>(to + p) = make_uint4(f[0], f[1], f[2], f[3]);
-            *reinterpret_cast<uint4*>(to + (p ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
-          }
+          each(Upto<N>(), [&](auto n_) {
+            constexpr int n = n_;
+            const uint32_t to = dst + (D == 128 && (n & 1) ? key_to ^ 64u : key_to);
+            constexpr int off = n * (D == 128 ? 512 : 1024);
+            st_shared_v4<off>(to, code_pair<0x4140>(c[n].x), code_pair<0x4342>(c[n].x), code_pair<0x4140>(c[n].y),
+                              code_pair<0x4342>(c[n].y));
+            st_shared_v4<off>(to ^ 16u, code_pair<0x4140>(c[n].z), code_pair<0x4342>(c[n].z),
+                              code_pair<0x4140>(c[n].w), code_pair<0x4342>(c[n].w));
+          });
           end();
         }
         if (u > 0) {
           begin();
           if (tries <= 0) break;
-          const unsigned char* src = raws + (raw % C::kRaws) * C::kRaw;
-          unsigned char* dst = ring + (pos % C::kStages) * C::kTile;
+          const uint32_t src = a_raw + (raw % C::kRaws) * C::kRaw, dst = a_ring + (pos % C::kStages) * C::kTile;
           const uint2 gone = S.absent[(unit0 + u - 1) & 15];
-          const uint32_t none = gone.x | gone.y;
-          constexpr int PV = D / 8;  // chunks of a pair
-          const int x = lane % PV;
+          const uint32_t none = ((gone.x | gone.y) >> (2 * wid)) & 3u;
           uint4 c[N];
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int pair = 16 * wid + 32 / PV * n + lane / PV;
-            c[n] = *reinterpret_cast<const uint4*>(src + pair * 2 * D + 16 * B::val_place(pair, x));
+          each(Upto<N>(), [&](auto n_) {
+            constexpr int n = n_;
+            c[n] = ld_shared_v4<n * 512>(src + (D == 128 && (n & 1) ? value_from ^ 64u : value_from));
+          });
+          if (none) {
+            each(Upto<N>(), [&](auto n_) {
+              constexpr int n = n_;
+              if ((none >> (n >= N / 2)) & 1u) c[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+            });
           }
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int pair = 16 * wid + 32 / PV * n + lane / PV;
-            uint32_t a[4] = {code_pair<0x4240>(c[n].x), code_pair<0x4240>(c[n].y), code_pair<0x4240>(c[n].z),
-                             code_pair<0x4240>(c[n].w)};
-            uint32_t b[4] = {code_pair<0x4341>(c[n].x), code_pair<0x4341>(c[n].y), code_pair<0x4341>(c[n].z),
-                             code_pair<0x4341>(c[n].w)};
-            if (none && ((none >> (pair >> 3)) & 1u)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) a[i] = b[i] = 0u;
-            }
-            unsigned char* to = dst + (x >> 3) * C::kSlab + 2 * pair * 128;
-            const int p = ((x & 7) ^ ((2 * pair) & 7)) << 4;
-            *reinterpret_cast<uint4*>(to + p) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4*>(to + 128 + (p ^ 16)) = make_uint4(b[0], b[1], b[2], b[3]);
-          }
+          each(Upto<N>(), [&](auto n_) {
+            constexpr int n = n_;
+            const uint32_t to = dst + (D == 128 && (n & 1) ? value_to ^ 64u : value_to);
+            constexpr int off = n * (D == 128 ? 512 : 1024);
+            st_shared_v4<off>(to, code_pair<0x4240>(c[n].x), code_pair<0x4240>(c[n].y), code_pair<0x4240>(c[n].z),
+                              code_pair<0x4240>(c[n].w));
+            st_shared_v4<off + 128>(to ^ 16u, code_pair<0x4341>(c[n].x), code_pair<0x4341>(c[n].y),
+                                    code_pair<0x4341>(c[n].z), code_pair<0x4341>(c[n].w));
+          });
           end();
         }
       }
@@ -480,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
       if (last) break;
     }
   } else {
-    fewer_registers<72>();
+    fewer_registers<64>();
     if (warp == kWarpMma) {
       // ---- products: one elected thread does it all (see sv_prompt.cu)
       constexpr uint32_t kScores = (1u << 4) | (16u << 17) | (8u << 24);  // float16 operands, float32 sums

@@ -22,6 +22,7 @@
 #include <cfloat>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "sv_attn.cuh"
 #include "sv_kv.h"
@@ -361,20 +362,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float base = m == -INFINITY ? 0.f : -m;
         const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
+        const bool far = fabsf(base) > 1048576.f;
+        auto weights = [&](auto rounded) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[32];
 #pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            const float2 z = make_float2(__uint_as_float(r[64 * h + 2 * n]), __uint_as_float(r[64 * h + 2 * n + 1]));
-            float2 p = fma2(z, c2, b2);
-            p.x = ex2_fast(p.x);
-            p.y = ex2_fast(p.y);
-            l2 = add2(l2, p);
-            w[n] = pack_bf16(p.x, p.y);
+            for (int n = 0; n < 32; ++n) {
+              float2 p = make_float2(__uint_as_float(r[64 * h + 2 * n]), __uint_as_float(r[64 * h + 2 * n + 1]));
+              if constexpr (rounded)
+                p = far ? make_float2(__fadd_rn(__fmul_rn(p.x, c), base), __fadd_rn(__fmul_rn(p.y, c), base))
+                        : fma2(p, c2, b2);
+              else
+                p = fma2(p, c2, b2);
+              p.x = ex2_fast(p.x);
+              p.y = ex2_fast(p.y);
+              l2 = add2(l2, p);
+              w[n] = pack_bf16(p.x, p.y);
+            }
+            tmem_st32(cols + 32 * h, w);
           }
-          tmem_st32(cols + 32 * h, w);
-        }
+        };
+        // Far from 0 the score that was rounded for the maximum is not the one that a fused operation has here
+        if (__any_sync(0xFFFFFFFFu, far))
+          weights(std::true_type());
+        else
+          weights(std::false_type());
         tmem_wait_st();
         tc_fence_before();
         arrive_warp(&S.p_full[g]);

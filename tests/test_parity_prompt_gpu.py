@@ -126,6 +126,18 @@ def test_sharp_flat_and_scaled(D):
 
 
 @DIMS
+def test_scores_far_from_zero(D):
+    """Scores of up to 1e31: the largest decides, in rows and tiles whose maxima differ by a lot."""
+    def edit(q, k, v):
+        q[3:200] *= 1e30
+        q[200:210] *= 1e7
+        q[210] *= -1e20
+        k[100] *= 3.0
+    _check([300, 40], 4, 2, D, edit=edit)
+    _check([300, 40], 4, 2, D, edit=edit, scale=-0.1)
+
+
+@DIMS
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("at", [0, 5, 31, 32, 127, 128, 200, 255, 256, 299])
 def test_values_that_rows_do_not_see(D, bad, at):
