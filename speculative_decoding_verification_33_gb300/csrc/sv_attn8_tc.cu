@@ -35,8 +35,8 @@
 namespace sv {
 namespace {
 
-constexpr int kWarpUnpack = 8, kWarpMma = 12, kWarpCopy = 13, kWarpItems = 14;
-constexpr int kThreads = 512, kSoftmaxThreads = 256;
+constexpr int kWarpUnpack = 8, kWarpMma = 16, kWarpCopy = 17, kWarpItems = 18;
+constexpr int kThreads = 640, kSoftmaxThreads = 256;
 constexpr int kR = 128, kUnit = 128;  // rows of a tile, tokens of a unit
 
 // Work as it is cut.
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
     mbar_init(&S.o_free, 8);
     mbar_init(&S.end, 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&S.q_full[i], 4);
+      mbar_init(&S.q_full[i], 8);
       mbar_init(&S.item_full[i], 1);
-      mbar_init(&S.item_free[i], 14);
+      mbar_init(&S.item_free[i], 18);
       S.items[i] = Item8{};
       S.items[i].last = 1;  // what a role reads that gave up waiting
     }
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
 
   if (warp < kWarpUnpack) {
     // ---- scores to weights: a thread a row, units of one stream
-    more_registers<176>();
+    more_registers<152>();
     const int g = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const uint32_t cols = tmem + lanes + 128 * g, outs = tmem + lanes + kColO;
@@ -391,26 +391,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
     }
   } else if (warp < kWarpMma) {
     // ---- codes (and queries) to operands
-    fewer_registers<96>();
-    const int wid = warp - kWarpUnpack;
+    fewer_registers<64>();
+    const int wid = warp & 3, which = (warp - kWarpUnpack) >> 2;  // keys, values
     // Where this thread's 16-byte chunks of codes lie, and what they become: D / 16 of keys (16 values of a token)
-    // and of values (8 of a pair of tokens), of the blocks 2 wid and 2 wid + 1. Eight lanes in a row keep the banks
+    // or of values (8 of a pair of tokens), of the blocks 2 wid and 2 wid + 1. Eight lanes in a row keep the banks
     // apart, of the bytes that they read and of the operands that they write. D = 128: what the places are
     // exchanged with depends on a chunk's number by a bit.
     constexpr int N = D / 16;
     const uint32_t a_raw = smem_u32(raws), a_ring = smem_u32(ring);
-    uint32_t key_from, key_to, value_from, value_to;
-    {
+    uint32_t from, to;
+    if (which == 0) {
       const int row = D == 128 ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane >> 2;  // of 4 or 8 at a time
       const int j = D == 128 ? (lane & 3) + 4 * (((lane >> 2) ^ (lane >> 3)) & 1) : lane & 3;
-      key_from = (32 * wid + row) * D + 16 * B::key_place(row, j);
-      key_to = (j >> 2) * C::kSlab + (32 * wid + row) * 128 + (((2 * (j & 3)) ^ row) << 4);
+      from = a_raw + (32 * wid + row) * D + 16 * B::key_place(row, j);
+      to = a_ring + (j >> 2) * C::kSlab + (32 * wid + row) * 128 + (((2 * (j & 3)) ^ row) << 4);
+    } else {
       constexpr int PV = D / 8;  // chunks of a pair
       const int pair = lane / PV, x = lane % PV;
-      value_from = (16 * wid + pair) * 2 * D + 16 * B::val_place(pair, x);
-      value_to = (x >> 3) * C::kSlab + (16 * wid + pair) * 256 + (((x & 7) ^ (2 * pair)) << 4);
+      from = a_raw + (16 * wid + pair) * 2 * D + 16 * B::val_place(pair, x);
+      to = a_ring + (x >> 3) * C::kSlab + (16 * wid + pair) * 256 + (((x & 7) ^ (2 * pair)) << 4);
     }
-    uint32_t raw = 0, pos = 0, unit0 = 0, used = 0;
+    uint32_t pos0 = 0, unit0 = 0, used = 0;
     for (int k = 0;; ++k) {
       wait_warp(&S.item_full[k & 3], k >> 2);
       if (tries <= 0) break;
@@ -419,11 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
       const int head0 = it.w.h * P.group;
       arrive_warp(&S.item_free[k & 3]);
       if (units > 0) {
-        constexpr int QV = D / 8, PASS = 128 / QV, N = kR / PASS;  // vectors of a row, rows at a time
-        const int j = lane % QV, rr = (32 * wid + lane) / QV;
-        uint4 x[N];
+        constexpr int QV = D / 8, PASS = 128 / QV, NQ = kR / PASS / 2;  // vectors of a row, rows at a time
+        const int j = lane % QV, rr = kR / 2 * which + (32 * wid + lane) / QV;  // half of the rows
+        uint4 x[NQ];
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
+        for (int n = 0; n < NQ; ++n) {
           const int row = row0 + PASS * n + rr, i = row / P.group;
           x[n] = make_uint4(0u, 0u, 0u, 0u);
           if (PASS * n + rr < rows)
@@ -434,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         if (tries <= 0) break;
         ++used;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (PASS * n >= rows) break;
+        for (int n = 0; n < NQ; ++n) {
+          if (kR / 2 * which + PASS * n >= rows) break;
           const int r = PASS * n + rr;
           unsigned most = largest_finite(x[n]);
 #pragma unroll
@@ -452,25 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
       }
       arrive_warp(&S.q_full[k & 3]);
 
-      // what a unit's bytes are waited for and handed on with
-      auto begin = [&]() {
-        wait_warp(&S.raw_full[raw % C::kRaws], raw / C::kRaws);
-        if (pos >= C::kStages) wait_warp(&S.empty[pos % C::kStages], pos / C::kStages - 1);
-      };
-      auto end = [&]() {
-        arrive_warp(&S.raw_empty[raw++ % C::kRaws]);
-        fence_async_shared();
-        arrive_warp(&S.full[pos++ % C::kStages]);
-      };
-      for (int u = 0; u <= units; ++u) {
-        if (u < units) {
-          begin();
-          if (tries <= 0) break;
-          const uint32_t src = a_raw + (raw % C::kRaws) * C::kRaw, dst = a_ring + (pos % C::kStages) * C::kTile;
-          const uint2 gone = S.absent[(unit0 + u) & 15];
-          const uint32_t none = ((gone.x | gone.y) >> (2 * wid)) & 3u;
+      for (int u = 0; u < units; ++u) {
+        // keys of an item's first two units come first, then values and keys in turn
+        const uint32_t pos = pos0 + (which == 0 ? max(2 * u - 1, 0) : min(2 * u + 2, 2 * units - 1));
+        const uint32_t raw = pos % C::kRaws, st = pos % C::kStages;
+        const uint32_t src = from + raw * C::kRaw, dst = to + st * C::kTile;
+        wait_warp(&S.raw_full[raw], pos / C::kRaws);
+        if (tries <= 0) break;
+        const uint2 gone = S.absent[(unit0 + u) & 15];
+        const uint32_t none = ((gone.x | gone.y) >> (2 * wid)) & 3u;
+        uint4 c[N];
+        if (which == 0) {
+          each(Upto<N>(), [&](auto n_) { c[n_] = ld_shared_v4<n_ * 512>(src); });
           if (lane < 2) {
-            uint2 h = *reinterpret_cast<const uint2*>(raws + (raw % C::kRaws) * C::kRaw + 8 * 16 * D + 16 * (2 * wid + lane));
+            uint2 h = *reinterpret_cast<const uint2*>(raws + raw * C::kRaw + 8 * 16 * D + 16 * (2 * wid + lane));
             if ((none >> lane) & 1u)  // without a page: marked keys
               h = make_uint2(0u, (gone.x >> (2 * wid + lane)) & 1u ? 0xFFFFu : 0u);
             const int ek = static_cast<signed char>(h.x & 0xFFu), ev = static_cast<signed char>((h.x >> 8) & 0xFFu);
@@ -478,60 +474,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
                 make_float4(__int_as_float((ek + 127) << 23), static_cast<float>(ev), __int_as_float((127 - ev) << 23),
                             __uint_as_float(h.y));
           }
-          uint4 c[N];
-          each(Upto<N>(), [&](auto n_) { c[n_] = ld_shared_v4<n_ * 512>(src + key_from); });
-          if (none) {
-            each(Upto<N>(), [&](auto n_) {
-              constexpr int n = n_;
-              if ((none >> (n >= N / 2)) & 1u) c[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-            });
-          }
+        } else {
           each(Upto<N>(), [&](auto n_) {
             constexpr int n = n_;
-            const uint32_t to = dst + (D == 128 && (n & 1) ? key_to ^ 64u : key_to);
-            constexpr int off = n * (D == 128 ? 512 : 1024);
-            st_shared_v4<off>(to, code_pair<0x4140>(c[n].x), code_pair<0x4342>(c[n].x), code_pair<0x4140>(c[n].y),
-                              code_pair<0x4342>(c[n].y));
-            st_shared_v4<off>(to ^ 16u, code_pair<0x4140>(c[n].z), code_pair<0x4342>(c[n].z),
-                              code_pair<0x4140>(c[n].w), code_pair<0x4342>(c[n].w));
+            c[n] = ld_shared_v4<n * 512>(D == 128 && (n & 1) ? src ^ 64u : src);
           });
-          end();
         }
-        if (u > 0) {
-          begin();
-          if (tries <= 0) break;
-          const uint32_t src = a_raw + (raw % C::kRaws) * C::kRaw, dst = a_ring + (pos % C::kStages) * C::kTile;
-          const uint2 gone = S.absent[(unit0 + u - 1) & 15];
-          const uint32_t none = ((gone.x | gone.y) >> (2 * wid)) & 3u;
-          uint4 c[N];
+        if (none) {
           each(Upto<N>(), [&](auto n_) {
             constexpr int n = n_;
-            c[n] = ld_shared_v4<n * 512>(src + (D == 128 && (n & 1) ? value_from ^ 64u : value_from));
+            if ((none >> (n >= N / 2)) & 1u) c[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
           });
-          if (none) {
-            each(Upto<N>(), [&](auto n_) {
-              constexpr int n = n_;
-              if ((none >> (n >= N / 2)) & 1u) c[n] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-            });
-          }
-          each(Upto<N>(), [&](auto n_) {
-            constexpr int n = n_;
-            const uint32_t to = dst + (D == 128 && (n & 1) ? value_to ^ 64u : value_to);
-            constexpr int off = n * (D == 128 ? 512 : 1024);
-            st_shared_v4<off>(to, code_pair<0x4240>(c[n].x), code_pair<0x4240>(c[n].y), code_pair<0x4240>(c[n].z),
+        }
+        if (pos >= C::kStages) wait_warp(&S.empty[st], pos / C::kStages - 1);
+        if (tries <= 0) break;
+        each(Upto<N>(), [&](auto n_) {
+          constexpr int n = n_;
+          const uint32_t at = D == 128 && (n & 1) ? dst ^ 64u : dst;
+          constexpr int off = n * (D == 128 ? 512 : 1024);
+          if (which == 0) {
+            st_shared_v4<off>(at, code_pair<0x4140>(c[n].x), code_pair<0x4342>(c[n].x), code_pair<0x4140>(c[n].y),
+                              code_pair<0x4342>(c[n].y));
+            st_shared_v4<off>(at ^ 16u, code_pair<0x4140>(c[n].z), code_pair<0x4342>(c[n].z), code_pair<0x4140>(c[n].w),
+                              code_pair<0x4342>(c[n].w));
+          } else {
+            st_shared_v4<off>(at, code_pair<0x4240>(c[n].x), code_pair<0x4240>(c[n].y), code_pair<0x4240>(c[n].z),
                               code_pair<0x4240>(c[n].w));
-            st_shared_v4<off + 128>(to ^ 16u, code_pair<0x4341>(c[n].x), code_pair<0x4341>(c[n].y),
+            st_shared_v4<off + 128>(at ^ 16u, code_pair<0x4341>(c[n].x), code_pair<0x4341>(c[n].y),
                                     code_pair<0x4341>(c[n].z), code_pair<0x4341>(c[n].w));
-          });
-          end();
+          }
+        });
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.raw_empty[raw]);
+          mbar_arrive(&S.full[st]);
         }
       }
+      pos0 += 2 * units;
       if (tries <= 0) break;
       unit0 += units;
       if (last) break;
     }
   } else {
-    fewer_registers<64>();
+    fewer_registers<48>();
     if (warp == kWarpMma) {
       // ---- products: one elected thread does it all (see sv_prompt.cu)
       constexpr uint32_t kScores = (1u << 4) | (16u << 17) | (8u << 24);  // float16 operands, float32 sums
