@@ -191,8 +191,8 @@ cudaError_t launch_dim(const AttnParams& P, long long all, int sms, cudaStream_t
 }  // namespace
 
 size_t attention_workspace_bytes(int sms) {
-  // two pieces a CTA, two CTAs an SM
-  return kAttnHeader + static_cast<size_t>(sms) * 4 * kTcMaxRows * (128 + 2) * sizeof(float);
+  // two pieces a CTA, of at most kPieceRows rows with one CTA an SM, half as many with two
+  return kAttnHeader + static_cast<size_t>(sms) * 2 * kPieceRows * (128 + 2) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,

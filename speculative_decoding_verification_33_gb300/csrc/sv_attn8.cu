@@ -140,7 +140,7 @@ cudaError_t launch_dim8(const AttnParams& P, long long all, int sms, cudaStream_
 
 cudaError_t launch_attention8(const AttnParams& P, int D, int max_new, int sms, cudaStream_t stream) {
   const long long all = std::max(1LL, static_cast<long long>(max_new) * P.group);
-  if (all > kMaxRows8<128>) return launch_attention8_tc(P, D, sms, stream);
+  if (all > (D == 64 ? kMaxRows8<64> : kMaxRows8<128>)) return launch_attention8_tc(P, D, all, sms, stream);
   return D == 64 ? launch_dim8<64>(P, all, sms, stream) : launch_dim8<128>(P, all, sms, stream);
 }
 

@@ -72,6 +72,7 @@ struct AttnParams {
 constexpr size_t kAttnHeader = 4096;  // bytes before the pieces: error word at 0, arrivals from 256
 constexpr int kAttnMaxCtas = (4096 - 256) / 4;
 
+constexpr int kPieceRows = 256;
 constexpr int kTcMaxRows = 64;  // rows of a tile of the tcgen05 kernel (sv_attn_tc.cu), D = 128
 cudaError_t launch_attention_tc(const AttnParams& P, int sms, cudaStream_t stream);
 
@@ -81,7 +82,8 @@ cudaError_t launch_attention(const AttnParams& P, int D, int max_new, int sms,
                              cudaStream_t stream);
 // The same over the 8-bit cache (sv_attn8.cu); k_scale and v_scale count as 1.
 cudaError_t launch_attention8(const AttnParams& P, int D, int max_new, int sms, cudaStream_t stream);
-cudaError_t launch_attention8_tc(const AttnParams& P, int D, int sms, cudaStream_t stream);  // sv_attn8_tc.cu
+// ... for `rows` rows a head or so, many of them (sv_attn8_tc.cu)
+cudaError_t launch_attention8_tc(const AttnParams& P, int D, long long rows, int sms, cudaStream_t stream);
 
 // Causal attention over whole prompts (sv_prompt.cu).
 struct PromptParams {
