@@ -128,6 +128,7 @@ struct PromptItem {
   int r0, n, head;  // sequence: first row, length; key/value head
   int tok, last;    // first and last token of the item
   int tiles[2];     // of keys, that a tile sees; 0: it has no rows
+  int half[2];      // its rows see the first half alone of the last of these
   int end;          // no item: the last one
 };
 
@@ -137,13 +138,13 @@ struct PromptShared {
   uint64_t s_full[2], p_full[2];             // scores; weights
   uint64_t o_done[2], o_free[2];             // outputs of an item; read
   uint64_t stat[2][2];                       // sums and maxima of a tile; tiles in turn use two
-  uint64_t item_full[4], item_free[4];
-  uint64_t clean[4];                         // an item's last values are fit for products
+  uint64_t item_full[2], item_free[2];
+  uint64_t clean[2];                         // an item's last values are fit for products
   uint64_t end;
-  PromptItem items[4];
+  PromptItem items[2];
   float sum[2][2][128], top[2][2][128];
   float row[4][128];                         // a row's queries
-  int bad[4];                                // the last token of the item with a value that is not finite
+  int bad[2];                                // the last token of the item with a value that is not finite
   int4 fix[kFixes];                          // rows to be taken for themselves
   uint32_t tmem;
   int fixes, levels, total;
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&S.stat[i][0], 4);
       mbar_init(&S.stat[i][1], 4);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&S.clean[i], 1);
       mbar_init(&S.item_full[i], 1);
       mbar_init(&S.item_free[i], 15);
@@ -287,9 +288,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
   // The k-th item, or false at the end. `done` hands its place back.
   auto item = [&](int k, PromptItem& it) {
-    wait_warp(&S.item_full[k & 3], k >> 2);
-    it = S.items[k & 3];
-    arrive_warp(&S.item_free[k & 3]);
+    wait_warp(&S.item_full[k & 1], k >> 1);
+    it = S.items[k & 1];
+    arrive_warp(&S.item_free[k & 1]);
     return tries > 0 && !it.end;
   };
 
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     PromptItem it;
     for (int k = 0; item(k, it); ++k) {
       const int first = it.tok + g * per, sees = min(first + i, it.last) + 1;
-      const int tiles = g ? it.tiles[1] : it.tiles[0];
+      const int tiles = g ? it.tiles[1] : it.tiles[0], half = g ? it.half[1] : it.half[0];
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int j = 0; j < tiles && tries > 0; ++j, ++phase) {
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               w[n] = pack_bf16(p.x, p.y);
             }
             tmem_st32(cols + 32 * h, w);
+            if (half && j + 1 == tiles) break;
           }
         };
         // Far from 0 the score that was rounded for the maximum is not the one that a fused operation has here
@@ -404,10 +406,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     fewer_registers<72>();
     const int row = tid & 127, i = row / P.group;
     const uint32_t outs = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
+    const bool wide = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;  // whole sectors
     int use[2] = {0, 0};
     for (int k = 0;; ++k) {
-      wait_warp(&S.item_full[k & 3], k >> 2);
-      const PromptItem it = S.items[k & 3];
+      wait_warp(&S.item_full[k & 1], k >> 1);
+      const PromptItem it = S.items[k & 1];
       if (tries <= 0 || it.end) break;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -431,20 +434,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tc_fence_before();
             arrive_warp(&S.o_free[g]);
           }
-          if (there) {
+          uint32_t w[16];
 #pragma unroll
-            for (int n = 0; n < 32; n += 8)
-              *reinterpret_cast<uint4*>(to + d + n) =
-                  make_uint4(pack_bf16(o[n] * inv, o[n + 1] * inv), pack_bf16(o[n + 2] * inv, o[n + 3] * inv),
-                             pack_bf16(o[n + 4] * inv, o[n + 5] * inv), pack_bf16(o[n + 6] * inv, o[n + 7] * inv));
+          for (int n = 0; n < 16; ++n) w[n] = pack_bf16(o[2 * n] * inv, o[2 * n + 1] * inv);
+          if (there) {
+            if (wide) {
+#pragma unroll
+              for (int n = 0; n < 16; n += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + d + 2 * n), "r"(w[n]),
+                             "r"(w[n + 1]), "r"(w[n + 2]), "r"(w[n + 3]), "r"(w[n + 4]), "r"(w[n + 5]), "r"(w[n + 6]),
+                             "r"(w[n + 7])
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int n = 0; n < 16; n += 4)
+                *reinterpret_cast<uint4*>(to + d + 2 * n) = make_uint4(w[n], w[n + 1], w[n + 2], w[n + 3]);
+            }
           }
         }
         if (there && P.lse) P.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
       }
-      wait_warp(&S.clean[k & 3], k >> 2);
+      wait_warp(&S.clean[k & 1], k >> 1);
       if (tries <= 0) break;
-      const int bad = S.bad[k & 3];
-      arrive_warp(&S.item_free[k & 3]);  // and the places of that number elsewhere
+      const int bad = S.bad[k & 1];
+      arrive_warp(&S.item_free[k & 1]);  // and the places of that number elsewhere
       if (bad > it.tok) {  // rows before that token
         const int4 fix = make_int4(it.r0, it.tok, bad, it.head);
         if (S.fixes < kFixes) {
@@ -492,9 +505,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         auto wait_full = [&](uint32_t p) { wait(&S.full[p % C::kStages], p / C::kStages); };
         for (int k = 0;; ++k) {
-          wait(&S.item_full[k & 3], k >> 2);
-          const int tiles[2] = {S.items[k & 3].tiles[0], S.items[k & 3].tiles[1]}, end = S.items[k & 3].end;
-          mbar_arrive(&S.item_free[k & 3]);
+          wait(&S.item_full[k & 1], k >> 1);
+          const int tiles[2] = {S.items[k & 1].tiles[0], S.items[k & 1].tiles[1]}, end = S.items[k & 1].end;
+          const int half[2] = {S.items[k & 1].half[0], S.items[k & 1].half[1]};
+          mbar_arrive(&S.item_free[k & 1]);
           if (end || tries <= 0) break;
           const int most = max(tiles[0], tiles[1]);
           wait_full(pos);
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int j = 0; j < most; ++j) {
             const uint32_t values = pos + 2 * j + 1, keys = values + 1;
             wait_full(values);
-            if (j + 1 < most) wait_full(keys); else wait(&S.clean[k & 3], k >> 2);
+            if (j + 1 < most) wait_full(keys); else wait(&S.clean[k & 1], k >> 1);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (j >= tiles[g]) continue;
@@ -522,7 +536,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               const uint32_t v = a_val + (values % C::kStages) * (C::kTile >> 4);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tmem + kColO + D * g, tmem + 128 * g + 8 * kk, v + ((2048 * kk) >> 4), kOutputs, j > 0 || kk > 0);
+                if (kk < 4 || j + 1 < tiles[g] || !half[g])
+                  mma_ts(tmem + kColO + D * g, tmem + 128 * g + 8 * kk, v + ((2048 * kk) >> 4), kOutputs, j > 0 || kk > 0);
               if (j + 1 < tiles[g])
                 scores(g, keys, j + 2 == tiles[g]);
               else
@@ -602,28 +617,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int from = max(it.tok + 1 - 128 * j, 0), to = min(it.last + 1 - 128 * j, 128);
           if (to > from || j == most - 1) {
             unsigned char* tile = ring + stage * C::kTile + 16 * (lane & 7);
-            for (int r = (from & ~3) + (lane >> 3); r < 128; r += 4) {
-              uint32_t x = 0;
+#pragma unroll 1
+            for (int r0 = (from & ~15) + (lane >> 3); r0 < 128; r0 += 16) {  // 16 rows at a time, all read at once
+              uint4 w[4][C::kSlabs];
 #pragma unroll
-              for (int s = 0; s < C::kSlabs; ++s) {
-                uint4* at = reinterpret_cast<uint4*>(tile + s * C::kSlab + 128 * r);
-                if (r >= to) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  const uint4 w = *at;
-                  const uint32_t f = 0x7FFF7FFFu;
-                  x = __vmaxu2(x, __vmaxu2(__vmaxu2(w.x & f, w.y & f), __vmaxu2(w.z & f, w.w & f)));
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int s = 0; s < C::kSlabs; ++s)
+                  w[u][s] = *reinterpret_cast<const uint4*>(tile + s * C::kSlab + 128 * (r0 + 4 * u));
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int r = r0 + 4 * u;
+                const uint32_t f = 0x7FFF7FFFu;
+                uint32_t x = 0;
+#pragma unroll
+                for (int s = 0; s < C::kSlabs; ++s) {
+                  x = __vmaxu2(x, __vmaxu2(__vmaxu2(w[u][s].x & f, w[u][s].y & f), __vmaxu2(w[u][s].z & f, w[u][s].w & f)));
+                  if (r >= to) *reinterpret_cast<uint4*>(tile + s * C::kSlab + 128 * r) = make_uint4(0u, 0u, 0u, 0u);
                 }
+                if (r >= from && r < to && ((x & 0xFFFFu) >= 0x7F80u || (x >> 16) >= 0x7F80u)) bad = max(bad, 128 * j + r);
               }
-              if ((x & 0xFFFFu) >= 0x7F80u || (x >> 16) >= 0x7F80u)
-                if (r >= from) bad = max(bad, 128 * j + r);
             }
           }
           if (j == most - 1) {
             bad = __reduce_max_sync(0xFFFFFFFFu, bad);
-            if (lane == 0) S.bad[k & 3] = bad;
+            if (lane == 0) S.bad[k & 1] = bad;
             fence_async_shared();
-            arrive_warp(&S.clean[k & 3]);
+            arrive_warp(&S.clean[k & 1]);
           }
           arrive_warp(&S.empty[stage]);
         }
@@ -633,7 +653,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // ---- items: the first one is this CTA's number, the others come from the counter
       int b = 0, before = 0;  // without an order: sequences from b on, tiles of those before
       for (int k = 0;; ++k) {
-        if (k >= 4) wait_warp(&S.item_free[k & 3], (k >> 2) - 1);
+        if (k >= 2) wait_warp(&S.item_free[k & 1], (k >> 1) - 1);
         if (tries <= 0) break;
         int i = blockIdx.x;
         if (k > 0) {
@@ -679,11 +699,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             it.head = i - u * P.hkv;
             it.tok = 2 * per * t;
             it.last = min(it.tok + 2 * per, it.n) - 1;
-            it.tiles[0] = min(it.tok + per - 1, it.last) / 128 + 1;
-            it.tiles[1] = it.tok + per <= it.last ? it.last / 128 + 1 : 0;
+            const int last0 = min(it.tok + per - 1, it.last);
+            it.tiles[0] = last0 / 128 + 1;
+            it.tiles[1] = last0 < it.last ? it.last / 128 + 1 : 0;
+            it.half[0] = last0 % 128 < 64;
+            it.half[1] = it.last % 128 < 64;
           }
-          S.items[k & 3] = it;
-          mbar_arrive(&S.item_full[k & 3]);
+          S.items[k & 1] = it;
+          mbar_arrive(&S.item_full[k & 1]);
         }
         __syncwarp();
         if (t < 0) break;
