@@ -21,7 +21,7 @@
 namespace sv {
 namespace {
 
-constexpr int kThreads8 = 256;
+constexpr int kThreads8 = 128;
 constexpr float kMagic = 12582912.f + 128.f;  // 1.5 * 2^23: its unit in the last place is 1
 
 struct Append8Params {
@@ -98,7 +98,7 @@ __device__ __forceinline__ uint2 interleave(uint32_t a, uint32_t b) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads8) append8_kernel(Append8Params P) {
+__global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_kernel(Append8Params P) {
   using B = Kv8Block<D>;
   constexpr int LP = D / 8;    // lanes of a token
   constexpr int TP = 32 / LP;  // tokens at a time
@@ -117,9 +117,11 @@ __global__ void __launch_bounds__(kThreads8) append8_kernel(Append8Params P) {
   // The tokens of this group that are the first of a block: the last token before it that is written, of the
   // 32 before, is of another block. Tokens that are not written stand for themselves.
   uint32_t starts = 0;
+  const long long slot0 = t0 + lane < P.T ? P.slots[t0 + lane] : -1;  // of 64 tokens
+  const long long slot1 = P.group_log && t0 + 32 + lane < P.T ? P.slots[t0 + 32 + lane] : -1;
   {
     const long long t = t0 + lane;
-    const long long now = t < P.T ? block_no(P.slots[t]) : -1;
+    const long long now = block_no(slot0);
     const long long before = t >= 32 ? block_no(P.slots[t - 32]) : -1;
     const uint32_t is_now = __ballot_sync(0xFFFFFFFFu, now >= 0), is_before = __ballot_sync(0xFFFFFFFFu, before >= 0);
     const uint32_t lower = (1u << lane) - 1u;
@@ -136,10 +138,13 @@ __global__ void __launch_bounds__(kThreads8) append8_kernel(Append8Params P) {
 
   while (starts) {
     __syncwarp();  // `from` is read
-    const long long t = t0 + __ffs(starts) - 1;
+    const int off = __ffs(starts) - 1;  // below 2^group_log
+    const long long t = t0 + off;
     starts &= starts - 1;
     // lane i: the token t + i, if it is of the same block and no token of another one comes before
-    const long long slot = t + lane < P.T ? P.slots[t + lane] : -1;
+    const long long near = __shfl_sync(0xFFFFFFFFu, slot0, (off + lane) & 31);
+    const long long far = __shfl_sync(0xFFFFFFFFu, slot1, (off + lane) & 31);
+    const long long slot = off + lane < 32 ? near : far;
     const long long no = block_no(slot), blk = __shfl_sync(0xFFFFFFFFu, no, 0);
     const uint32_t ends = __ballot_sync(0xFFFFFFFFu, no >= 0 && no != blk);
     const bool mine = blk < 0 ? lane == 0 : no == blk && !(ends & ((1u << lane) - 1u));
@@ -184,10 +189,28 @@ __global__ void __launch_bounds__(kThreads8) append8_kernel(Append8Params P) {
     const int e = fresh ? need : max(need, had);
     const bool again = !fresh && e > had;  // the other places' codes are rounded again
     const float scale = two_to(-e), step = two_to(e);
+    if (again) {  // all codes that are there, for the tokens of this call are written after them
+      const float down = two_to(max(had - e, -126));
+      unsigned char* codes = to + (is_v ? B::kValCodes : B::kKeyCodes) + 16 * lane;
+#pragma unroll 1
+      for (int at = 0; at < 16 * D; at += 512) {
+        uint4 w = *reinterpret_cast<const uint4*>(codes + at);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y[4];
+          codes_of((&w.x)[q], y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = fmaxf(y[i] * down, -127.f) + kMagic;
+          (&w.x)[q] = low_bytes(y);
+        }
+        *reinterpret_cast<uint4*>(codes + at) = w;
+      }
+      __syncwarp();
+    }
 
     // codes plus 128, eight a lane; `known`: places whose bytes are to be written
     uint2 c[N];
-    const uint32_t known = fresh || again ? 0xFFFFu : there;
+    const uint32_t known = fresh ? 0xFFFFu : there;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int p = TP * j + j0;
@@ -197,24 +220,6 @@ __global__ void __launch_bounds__(kThreads8) append8_kernel(Append8Params P) {
         float v = x[j].get(i) * scale;
         if (e == kKv8High) v = fminf(fmaxf(v, -127.f), 127.f);
         y[i] = v + kMagic;
-      }
-      if (again && !((there >> p) & 1u)) {
-        float old[8];
-        if (!is_v) {
-          const uint2 w = *reinterpret_cast<const uint2*>(to + B::kKeyCodes + p * D +
-                                                          16 * B::key_place(p, l >> 1) + 8 * (l & 1));
-          codes_of(w.x, old);
-          codes_of(w.y, old + 4);
-        } else {
-          const uint4 w = *reinterpret_cast<const uint4*>(to + B::kValCodes + (p >> 1) * 2 * D +
-                                                          16 * B::val_place(p >> 1, l));
-          const uint32_t sel = p & 1 ? 0x7531u : 0x6420u;
-          codes_of(__byte_perm(w.x, w.y, sel), old);
-          codes_of(__byte_perm(w.z, w.w, sel), old + 4);
-        }
-        const float down = two_to(max(had - e, -126));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaxf(old[i] * down, -127.f) + kMagic;
       }
       c[j] = make_uint2(low_bytes(y), low_bytes(y + 4));
       if (out && ((there >> p) & 1u)) {
