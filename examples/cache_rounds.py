@@ -1,13 +1,15 @@
-"""Rounds of greedy self-speculative decoding over the 4-bit paged cache, end to end.
+"""Rounds of greedy self-speculative decoding over the 4-bit or the 8-bit paged cache, end to end.
 
 A small decoder with random weights drafts with its first layers and the shared head (an early
 exit) and verifies with all of them (LayerSkip guide, "Verification Phase"): each round is one
 ``block_tables`` call, the drafts' single-token passes through the first layers, one pass of all
 layers over every sequence's last token and drafts (``qk_norm_rope``, ``kv4_append``,
 ``kv4_attention``), and ``verify_hidden``, whose accepted lengths roll the cache back in the next
-round's ``block_tables``. Projections are plain matrix products.
+round's ``block_tables``. With 8 bits (``kv8_append``, ``kv8_attention``) the prompts' pass runs
+``prompt_attention`` over the keys and values as the cache holds them, without reading it. Projections
+are plain matrix products.
 
-    python examples/cache_rounds.py [rounds] [draft length]
+    python examples/cache_rounds.py [rounds] [draft length] [bits]
 """
 import os
 import sys
@@ -45,9 +47,9 @@ class Decoder:
         return (y * torch.rsqrt((y * y).mean(-1, keepdim=True) + 1e-6)).to(BF16)
 
     def forward(self, tokens, positions, slots, caches, table, kv_lens, cu_new, max_new, page_size,
-                layers):
+                layers, bits=4, prompts=False):
         """Hidden states [T, d] of ``tokens`` after the first ``layers`` layers; their keys and values
-        go into ``caches`` at ``slots``."""
+        go into ``caches`` at ``slots``. ``prompts``: nothing is cached before these tokens."""
         x = self.embed[tokens.long()]
         T, qw, kw = x.shape[0], self.hq * self.head, self.hkv * self.head
         for w, cache in zip(self.layers[:layers], caches):
@@ -57,8 +59,15 @@ class Decoder:
             v = qkv[:, qw + kw:].unflatten(1, (self.hkv, self.head))
             sv.qk_norm_rope(q, k, positions, self.freq, q_weight=w["qn"], k_weight=w["kn"],
                             out={"q": q, "k": k})
-            sv.kv4_append(k, v, slots, cache, page_size=page_size)
-            a = sv.kv4_attention(q, cache, table, kv_lens, cu_new, page_size=page_size, max_new=max_new)
+            if bits == 8:
+                held = sv.kv8_append(k, v, slots, cache, page_size=page_size, values=prompts)
+            else:
+                sv.kv4_append(k, v, slots, cache, page_size=page_size)
+            if bits == 8 and prompts:
+                a = sv.prompt_attention(q, held["k"], held["v"], cu_new)
+            else:
+                attend = sv.kv8_attention if bits == 8 else sv.kv4_attention
+                a = attend(q, cache, table, kv_lens, cu_new, page_size=page_size, max_new=max_new)
             x = x + a["out"].view(T, qw) @ w["o"].T
             y = self.norm(x)
             x = x + (torch.nn.functional.silu(y @ w["gate"].T) * (y @ w["up"].T)) @ w["down"].T
@@ -71,10 +80,11 @@ class Decoder:
 class Session:
     """Sequences that decode together: their lengths, pages and caches."""
 
-    def __init__(self, model, prompts, page_size=16, pages=512, max_blocks=64):
-        self.m, self.ps, B = model, page_size, len(prompts)
+    def __init__(self, model, prompts, page_size=16, pages=512, max_blocks=64, bits=4):
+        self.m, self.ps, self.bits, B = model, page_size, bits, len(prompts)
         i32 = {"dtype": torch.int32, "device": "cuda"}
-        self.caches = [sv.kv4_cache(pages, model.hkv, model.head, page_size) for _ in model.layers]
+        empty = sv.kv8_cache if bits == 8 else sv.kv4_cache
+        self.caches = [empty(pages, model.hkv, model.head, page_size) for _ in model.layers]
         self.table = torch.full((B, max_blocks), -1, **i32)
         self.ring = torch.arange(pages, **i32)
         self.ctx, self.held = torch.zeros(B, **i32), torch.zeros(B, **i32)
@@ -85,7 +95,7 @@ class Session:
         r = self.tables(new, int(new.sum()))
         tokens = torch.tensor([t for p in prompts for t in p], **i32)
         h = model.forward(tokens, r["positions"], r["slots"], self.caches, self.table, r["kv_lens"],
-                          r["cu_new"], int(new.max()), self.ps, len(model.layers))
+                          r["cu_new"], int(new.max()), self.ps, len(model.layers), bits, prompts=True)
         self.last = model.next_token(h[(r["cu_new"][1:] - 1).long()])
         self.accept = new - 1
         self.out = [[int(t)] for t in self.last]
@@ -108,10 +118,11 @@ class Session:
         one = torch.arange(B + 1, dtype=torch.int32, device="cuda")
         for j in range(K):  # drafts: the first layers, a token at a time
             h = m.forward(tokens[:, j], positions[:, j].contiguous(), slots[:, j].contiguous(),
-                          self.caches, self.table, positions[:, j] + 1, one, 1, self.ps, m.exit)
+                          self.caches, self.table, positions[:, j] + 1, one, 1, self.ps, m.exit,
+                          self.bits)
             tokens[:, j + 1] = m.next_token(h)
         h = m.forward(tokens.view(-1), r["positions"], r["slots"], self.caches, self.table,
-                      r["kv_lens"], r["cu_new"], K + 1, self.ps, len(m.layers))
+                      r["kv_lens"], r["cu_new"], K + 1, self.ps, len(m.layers), self.bits)
         if K == 0:
             self.last, self.accept = m.next_token(h), torch.zeros_like(self.last)
             for b, t in enumerate(self.last.tolist()):
@@ -126,11 +137,11 @@ class Session:
         return self.accept
 
 
-def main(rounds=12, K=4):
+def main(rounds=12, K=4, bits=4):
     model = Decoder()
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 2000, (n,), generator=g).tolist() for n in (1, 7, 16, 33, 90, 127)]
-    s = Session(model, prompts)
+    s = Session(model, prompts, bits=bits)
     accepted = torch.stack([s.round(K) for _ in range(rounds)]).float()
     torch.cuda.synchronize()
     assert sv.device_error() == 0
@@ -138,7 +149,7 @@ def main(rounds=12, K=4):
 
 
 if __name__ == "__main__":
-    args = [int(a) for a in sys.argv[1:3]]
+    args = [int(a) for a in sys.argv[1:4]]
     session, acc = main(*args)
     print(f"{acc.shape[0]} rounds, {acc.mean():.2f} drafts accepted a round and sequence")
     for b, toks in enumerate(session.out):

@@ -248,3 +248,30 @@ def test_without_log_sums_and_nothing_to_do():
     assert torch.equal(sv.prompt_attention(q, q, q, dev([0, 5]), out=out)["out"], full["out"])
     assert sv.prompt_attention(q[:0], q[:0], q[:0], dev([0, 0]))["out"].shape == (0, 2, 64)
     assert sv.prompt_attention(q, q, q, dev([3]))["out"].shape == (5, 2, 64)  # no sequence
+
+
+@DIMS
+def test_output_at_half_a_sector(D):
+    """An output that begins 16 bytes behind a line: the same values, and nothing beside them."""
+    T, hq, hk = 150, 4, 2
+    q, k, v = (torch.randn(T, h, D, device="cuda").to(BF16) for h in (hq, hk, hk))
+    cu = dev(np.array([0, 130, 150]))
+    want = sv.prompt_attention(q, k, v, cu)
+    room = torch.full((T * hq * D + 16,), 7.0, device="cuda", dtype=BF16)
+    o = {"out": room[8:-8].view(T, hq, D), "lse": torch.empty((T, hq), device="cuda")}
+    sv.prompt_attention(q, k, v, cu, out=o)
+    assert torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"])
+    assert bool((room[:8] == 7).all()) and bool((room[-8:] == 7).all())
+
+
+@DIMS
+@pytest.mark.parametrize("n", [63, 64, 65, 190, 191, 192, 193])
+@pytest.mark.parametrize("hq,hk", [(4, 2), (6, 1), (1, 1)])
+def test_half_tiles(n, hq, hk, D):
+    """Lengths whose last tile of tokens is half seen, in one of a CTA's tiles of rows or in both, with values
+    behind them that are not finite."""
+    def edit(q, k, v):
+        v[n:] = float("nan")
+        k[n:] = float("inf")
+    _check([n, 70], hq, hk, D, seed=n)
+    _check([n], hq, hk, D, seed=n, edit=edit, cu=[0, n], T=n + 80)
