@@ -123,6 +123,15 @@ struct Kv8 {
 template <int D>
 constexpr int kMaxRows8 = D == 128 ? 24 : 32;
 
+// Rows a head, at most, for this kernel; those past a tile read the cache once more. It works for the rows that
+// a sequence has, sv_attn8_tc.cu for 128. Measured in us, here / there, for 8 sequences of 16384 tokens and
+// for 64 of up to 8192 with up to that many rows. D = 128, 8 heads: 24 rows 72 / 97 and 93 / 160; 32 rows
+// 103 / 98 and 124 / 162; 48 rows 124 / 102 and 148 / 170; 64 rows 174 / 104 and 190 / 178; 20 rows of one
+// sequence of 524301 tokens 229 / 336. D = 64, 2 heads: 32 rows 25 / 33; 64 rows 36 / 36 and 40 / 45; 96
+// rows 45 / 40 and 51 / 48.
+template <int D>
+constexpr int kRegisterRows = D == 128 ? 32 : 64;
+
 template <int D>
 cudaError_t launch_dim8(const AttnParams& P, long long all, int sms, cudaStream_t stream) {
   // rows of a tile: a sequence's rows in as few tiles as hold them, evenly
@@ -140,7 +149,7 @@ cudaError_t launch_dim8(const AttnParams& P, long long all, int sms, cudaStream_
 
 cudaError_t launch_attention8(const AttnParams& P, int D, int max_new, int sms, cudaStream_t stream) {
   const long long all = std::max(1LL, static_cast<long long>(max_new) * P.group);
-  if (all > (D == 64 ? kMaxRows8<64> : kMaxRows8<128>)) return launch_attention8_tc(P, D, all, sms, stream);
+  if (all > (D == 64 ? kRegisterRows<64> : kRegisterRows<128>)) return launch_attention8_tc(P, D, all, sms, stream);
   return D == 64 ? launch_dim8<64>(P, all, sms, stream) : launch_dim8<128>(P, all, sms, stream);
 }
 
