@@ -17,13 +17,13 @@
  *
  * Memory: every pointer is DEVICE memory owned by the caller. All calls are asynchronous on
  * `stream` (a cudaStream_t, NULL for the legacy default stream), do not synchronise and may be
- * captured into a graph (spec_kv4_attention after one call on the same stream outside capture).
- * spec_kv4_attention keeps a workspace of fixed size for each device and stream; a captured call
+ * captured into a graph (the attention operators after one call on the same stream outside capture).
+ * The attention operators share a workspace of fixed size for each device and stream; a captured call
  * keeps that of the stream it was captured on, so its replays must not overlap other calls of
  * that stream, or replays of other graphs captured on it.
  *
  * Errors: arguments are checked on the host before anything is launched, as in spec_verify.h. A
- * copy that spec_kv4_attention waits for in vain raises the stream's error word; what that call and
+ * copy that an attention operator waits for in vain raises the stream's error word; what that call and
  * later ones on the stream wrote is not valid until spec_verify_device_error has reported it.
  *
  * The cache. uint8 [num_pages][Hkv][page_size * (D + D/8)], 16-byte aligned: a page holds

@@ -8,6 +8,12 @@
 // scores. That of its values joins the exponent of the weights: with t = score + e (base 2) and M the running
 // maximum of t, outputs are sums of 2^(t - M) code, and the softmax's sum is that of 2^(t - M) 2^-e, which is
 // sum of 2^(score - M): maxima, joins and the log-sum stay as they are.
+//
+// What bounds it, as with 4 bits, is latency: with 20 rows of 524301 tokens, 8 heads of 128, it takes 231 us,
+// 0.69 of the measured copy rate, with 0.54 of the issue slots and 0.37 of the tensor pipe used, and fixed
+// latencies and the pairs' barriers the largest stalls; 64 sequences of up to 8192 tokens and up to 24 rows
+// 103 us. The cut of the work (kOver, kLeast) is at its best here: kOver 48 and 200 take 105 and 107 us for
+// these, kLeast 4 and 16 12.8 and 12.3 us for one row of 4097 tokens where 12 takes 11.8.
 #include "spec_kv.h"
 #include "sv_attn_mma.cuh"
 

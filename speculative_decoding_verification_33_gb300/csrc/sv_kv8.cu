@@ -14,6 +14,7 @@
 // What bounds it: HBM for prompts (13 of 5001 tokens, 8 heads of 128, bf16: 114 us, 0.86 of the measured copy
 // rate; blocks of 128 threads at 64 registers took 118 where 256 at 80 took 126, and old codes rounded in a
 // loop of their own 114); for small calls the chain of slots, rows, maximum and stores of one block.
+// Steps whose places bring nothing are left out (one token of each of 384 sequences, 8 heads: 11.0 -> 7.8 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -177,10 +178,13 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_ker
     }
     const bool fresh = blk < 0 || (there & 1u);
 
+    // Steps whose places bring nothing are left out, the same ones in all lanes
+    auto any = [&](uint32_t places, int j) { return (places >> (TP * j)) & ((1u << TP) - 1u); };
     // marks, and the largest magnitude of the tokens without one
     uint32_t bad = 0, top = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+      if (!any(there, j)) continue;
       const uint32_t m = x[j].most();
       const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, m >= 0x7F800000u);
       const bool marked = (lanes >> (lane - l)) & ((1ull << LP) - 1);
@@ -219,6 +223,8 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_ker
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int p = TP * j + j0;
+      c[j] = make_uint2(0u, 0u);
+      if (!any(known, j)) continue;
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -243,13 +249,14 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_ker
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const int p = TP * j + j0;
-        if ((known >> p) & 1u)
+        if (any(known, j) && ((known >> p) & 1u))
           *reinterpret_cast<uint2*>(to + B::kKeyCodes + p * D + 16 * B::key_place(p, l >> 1) + 8 * (l & 1)) = c[j];
       }
     } else {
       // pairs: of two instructions, lanes of even tokens write the first one's, those of odd ones the second's
 #pragma unroll
       for (int j = 0; j < N; j += 2) {
+        if (!any(known, j) && !any(known, j + 1)) continue;
         const bool odd = j0 & 1;
         const uint2 give = odd ? c[j] : c[j + 1], keep = odd ? c[j + 1] : c[j];
         uint2 got;
@@ -322,10 +329,10 @@ extern "C" sv_status spec_kv8_append(int T, int Hkv, int D, int page_size, int n
   P.num_pages = num_pages;
   P.ps_log = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   // Tokens of a warp: many are few warps, and blocks that begin among them follow one another. Measured for 8
-  // heads of 128, groups of 1, 2, 4 and 16 tokens: 384 tokens in a run 5.2, 4.2, 4.1, 3.7 us, six to a block
-  // 6.2, 4.7, 4.6, 7.2, one to a block 10.0, 11.0, 12.3, 28.7; 1024 tokens 7.2, 5.7, 4.6, 4.6, then 10.0, 9.2,
-  // 7.3, 8.4, then 21.5, 22.0, 22.6, 34.4; 4096 tokens 18.7, 13.4, 10.8, 7.7, then 28.0, 23.2, 19.0, 18.0, then
-  // 76.8, 73.3, 72.8, 81.9.
+  // heads of 128, groups of 1, 2, 4 and 16 tokens: 384 tokens in a run 5.2, 4.7, 4.2, 4.2 us, six to a block
+  // 5.2, 4.1, 4.1, 6.7, one to a block 7.8, 7.9, 9.2, 23.8; 1024 tokens 7.7, 6.1, 4.7, 4.6, then 8.6, 7.9,
+  // 6.2, 7.7, then 14.9, 14.4, 14.4, 26.1; 4096 tokens 19.5, 13.9, 11.3, 8.2, then 23.5, 19.1, 15.4, 14.4, then
+  // 49.2, 44.2, 42.6, 46.6.
   const long long rows = static_cast<long long>(T) * Hkv;
   P.group_log = rows < (1 << 13) ? 1 : rows < (1 << 15) ? 2 : 4;
   P.ks = k_token_stride;

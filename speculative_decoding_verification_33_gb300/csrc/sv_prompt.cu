@@ -12,7 +12,17 @@
 //
 // One persistent CTA an SM, its warps specialised: eight take scores to weights, four take outputs to memory,
 // one issues products, one copies (TMA), one looks after values that no row may see, one fetches items. Items
-// come from a counter, in the order of their cost where that can be had, so that the last ones are short.
+// come from a counter, in the order of their cost where that can be had, so that the last ones are short, and
+// two at a time: with four, CTAs held items that others had time for (24 prompts of up to 1000 tokens, 28 + 4
+// heads: 55 -> 52 us; 12 + 12 heads of 64: 119 -> 101).
+//
+// What bounds it, on long prompts: the tensor cores, at 0.67 of their cycles and 0.83 of the measured bf16 rate
+// (8192 tokens, 32 + 8 heads of 128: 350 us, 1571 TFLOP/s by what rows see; 16384 tokens: 1615), held up by the
+// softmax's way from scores to weights, a latency: 0.37 of the issue slots are used. On short prompts: the
+// changes from item to item, about 5 us for each of 128 rows twice, most of it waits for memory. Tiles of 64
+// tokens with scores twice in tensor memory (long prompts 370 -> 516 us: such products read their queries
+// twice as often), the next item's first scores behind this one's last products (registers spilled: 350 ->
+// 390), and, for heads of 64, weights in columns of their own (no change) were built and not kept.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
