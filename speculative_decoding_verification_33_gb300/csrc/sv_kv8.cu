@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_ker
   const long long t0 = warp << P.group_log;
   if (t0 >= P.T) return;
   const long long most = static_cast<long long>(P.num_pages) << P.ps_log;
+  __nv_bfloat16* out = is_v ? P.ov : P.ok;
   auto block_no = [&](long long s) { return s >= 0 && s < most ? s >> 4 : -1LL; };
 
   // The tokens of this group that are the first of a block: the last token before it that is written, of the
@@ -135,11 +136,10 @@ __global__ void __launch_bounds__(kThreads8, sizeof(T) == 2 ? 8 : 5) append8_ker
     const int last = 31 - __clz(below ? below : above);
     const long long one = __shfl_sync(0xFFFFFFFFu, now, last & 31), other = __shfl_sync(0xFFFFFFFFu, before, last & 31);
     const bool goes_on = now >= 0 && (below ? one == now : above && other == now);
-    starts = __ballot_sync(0xFFFFFFFFu, lane < (1 << P.group_log) && t < P.T && !goes_on && (now >= 0 || P.ok));
+    starts = __ballot_sync(0xFFFFFFFFu, lane < (1 << P.group_log) && t < P.T && !goes_on && (now >= 0 || out));
   }
   const T* src = static_cast<const T*>(is_v ? P.v : P.k);
   const long long stride = is_v ? P.vs : P.ks;
-  __nv_bfloat16* out = is_v ? P.ov : P.ok;
   const int j0 = lane / LP, l = lane % LP;  // token of the instruction, place in its row
 
   while (starts) {

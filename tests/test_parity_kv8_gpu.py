@@ -504,3 +504,21 @@ def test_attention_streams_and_graphs(new):
         torch.cuda.synchronize()
         assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
     assert sv.device_error() == 0
+
+
+@pytest.mark.parametrize("keys", [True, False])
+def test_append_one_output(keys):
+    """The values as held of keys alone, or of values alone, for every token, written to the cache or not."""
+    from speculative_decoding_verification_33_gb300 import _lib
+    T, H, D, ps = 40, 2, 64, 16
+    slots = np.where(np.arange(T) % 7 == 3, -1, np.arange(T) + 5)
+    k, v = (torch.randn(T, H, D, device="cuda").to(BF16) for _ in range(2))
+    caches = [sv.kv8_cache(4, H, D, ps) for _ in range(2)]
+    want = sv.kv8_append(k, v, dev(slots, torch.int64), caches[0], page_size=ps, values=True)
+    out, s = torch.full_like(k, 7.0), dev(slots, torch.int64)
+    st = _lib.load().spec_kv8_append(
+        T, H, D, ps, 4, 1, k.data_ptr(), H * D, v.data_ptr(), H * D, s.data_ptr(), caches[1].data_ptr(),
+        out.data_ptr() if keys else 0, 0 if keys else out.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out, want["k" if keys else "v"]) and torch.equal(caches[0], caches[1])
