@@ -93,7 +93,7 @@ struct Shared8 {
   uint64_t s_full[2], p_full[2];         // scores; weights
   uint64_t o_done[2], o_free;            // outputs of an item; read
   uint64_t item_full[4], item_free[4];
-  uint64_t end;
+  uint64_t meet, end;
   Item8 items[4];
   uint32_t tmem;
   int last;
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
     }
     mbar_init(&S.q_free, 1);
     mbar_init(&S.o_free, 8);
+    mbar_init(&S.meet, kWarpUnpack);
     mbar_init(&S.end, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&S.q_full[i], 4);
@@ -215,6 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
     int phase = 0;
     uint32_t done0 = 0, done1 = 0;  // items that used a stream's outputs
     uint32_t unit0 = 0;  // units of the run before the item
+    uint32_t meets = 0;
+    auto meet = [&] {  // all softmax warps, those apart that gave up
+      arrive_warp(&S.meet);
+      wait_warp(&S.meet, meets++);
+    };
     for (int k = 0;; ++k) {
       wait_warp(&S.item_full[k & 3], k >> 2);
       if (tries <= 0) break;
@@ -403,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         S.top[k & 1][g][row] = m;
         S.sum[k & 1][g][row] = L;
         S.bad[k & 1][g][row] = poison;
-        named_sync(1, kSoftmaxThreads);
+        meet();
         const float m0 = S.top[k & 1][0][row], m1 = S.top[k & 1][1][row];
         M = fmaxf(m0, m1);
         f0 = ex2_fast(m0 - M);
@@ -464,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         }
       }
       if (!whole)
-        join_pieces<kSoftmaxThreads, C::kRows, D, 4>(P, w, S.run, rows, tid, &S.last,
-                                                     [] { named_sync(2, kSoftmaxThreads); });
+        join_pieces<kSoftmaxThreads, C::kRows, D, 4>(P, w, S.run, rows, tid, &S.last, meet);
       const int last = it.last;
       arrive_warp(&S.item_free[k & 3]);
       if (last) break;

@@ -150,14 +150,14 @@ struct PromptShared {
   uint64_t stat[2][2];                       // sums and maxima of a tile; tiles in turn use two
   uint64_t item_full[2], item_free[2];
   uint64_t clean[2];                         // an item's last values are fit for products
-  uint64_t end;
+  uint64_t meet, end;
   PromptItem items[2];
   float sum[2][2][128], top[2][2][128];
   float row[4][128];                         // a row's queries
   int bad[2];                                // the last token of the item with a value that is not finite
-  int4 fix[kFixes];                          // rows to be taken for themselves
+  int4 fix[4][kFixes];                       // rows to be taken for themselves: a list for each output warp
   uint32_t tmem;
-  int fixes, levels, total;
+  int levels, total;
   int count[kLevels + 1], more[kLevels + 1], start[kLevels + 1], order[kSeqs];
 };
 
@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       S.items[i] = PromptItem{};
       S.items[i].end = 1;  // what a role reads that gave up waiting
     }
+    mbar_init(&S.meet, 4);
     mbar_init(&S.end, 1);
     fence_mbar_init();
-    S.fixes = 0;
     S.levels = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
@@ -418,6 +418,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t outs = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
     const bool wide = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;  // whole sectors
     int use[2] = {0, 0};
+    int fixes = 0;  // items that have rows to compute once more, the same ones in each of these warps
+    uint32_t meets = 0;
+    auto meet = [&] {  // these warps, those apart that gave up
+      arrive_warp(&S.meet);
+      wait_warp(&S.meet, meets++);
+    };
     for (int k = 0;; ++k) {
       wait_warp(&S.item_full[k & 1], k >> 1);
       const PromptItem it = S.items[k & 1];
@@ -470,22 +476,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       arrive_warp(&S.item_free[k & 1]);  // and the places of that number elsewhere
       if (bad > it.tok) {  // rows before that token
         const int4 fix = make_int4(it.r0, it.tok, bad, it.head);
-        if (S.fixes < kFixes) {
-          named_sync(1, 128);
-          if (tid == 32 * kWarpOut) S.fix[S.fixes++] = fix;
-          named_sync(1, 128);
+        if (fixes < kFixes) {
+          if (lane == 0) S.fix[warp - kWarpOut][fixes] = fix;
+          ++fixes;
         } else {
-          named_sync(1, 128);  // what these rows got from the products is written
+          meet();  // what these rows got from the products is written
           for (int n = warp - kWarpOut; n < (bad - it.tok) * P.group; n += 4)
             prompt_row<D>(P, it.r0, it.r0 + it.tok + n / P.group, it.head * P.group + n % P.group,
                           S.row[warp - kWarpOut]);
         }
       }
     }
-    if (tries > 0) {
-      named_sync(1, 128);
-      for (int f = 0; f < S.fixes; ++f) {
-        const int4 fix = S.fix[f];
+    if (fixes && tries > 0) {
+      meet();
+      for (int f = 0; f < fixes; ++f) {
+        const int4 fix = S.fix[warp - kWarpOut][f];
         for (int n = warp - kWarpOut; n < (fix.z - fix.y) * P.group; n += 4)
           prompt_row<D>(P, fix.x, fix.x + fix.y + n / P.group, fix.w * P.group + n % P.group, S.row[warp - kWarpOut]);
       }
