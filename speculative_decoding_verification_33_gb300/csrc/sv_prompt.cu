@@ -17,7 +17,7 @@
 // heads: 55 -> 52 us; 12 + 12 heads of 64: 119 -> 101).
 //
 // What bounds it, on long prompts: the tensor cores, at 0.67 of their cycles and 0.83 of the measured bf16 rate
-// (8192 tokens, 32 + 8 heads of 128: 350 us, 1571 TFLOP/s by what rows see; 16384 tokens: 1615), held up by the
+// (8192 tokens, 32 + 8 heads of 128: 350 us, 1571 TFLOP/s by what rows see; 16384 tokens: 1674), held up by the
 // softmax's way from scores to weights, a latency: 0.37 of the issue slots are used. On short prompts: the
 // changes from item to item, about 5 us for each of 128 rows twice, most of it waits for memory. Tiles of 64
 // tokens with scores twice in tensor memory (long prompts 370 -> 516 us: such products read their queries
