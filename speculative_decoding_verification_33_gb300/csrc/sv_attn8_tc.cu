@@ -91,7 +91,7 @@ struct Shared8 {
   uint64_t full[6], empty[6];            // operands
   uint64_t q_full[4], q_free;            // queries of an item; spent
   uint64_t s_full[2], p_full[2];         // scores; weights
-  uint64_t o_done[2], o_free;            // outputs of an item; read
+  uint64_t o_done[2], o_free;            // outputs of an item; read (without PAIR)
   uint64_t item_full[4], item_free[4];
   uint64_t meet, end;
   Item8 items[4];
@@ -460,7 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         }
       }
       tc_fence_before();
-      if (units > 0) arrive_warp(&S.o_free);
+      // With PAIR a stream's outputs are read by its own warps alone, and the next item's first products into them
+      // wait for weights that these warps give afterwards. (Warps without rows would count here ahead of the
+      // others, item after item, and a phase that is two ahead is waited for in vain.)
+      if (!PAIR && units > 0) arrive_warp(&S.o_free);
       if ((PAIR || g == 0) && item_row < rows) {
         if (whole) {
           store_lse(P, at, M, L);
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
       if (elect_one()) {
         const uint32_t a_q = operand_lo(smem_u32(sq), 16), a_key = operand_lo(smem_u32(ring), 16);
         const uint32_t a_val = operand_lo(smem_u32(ring), C::kSlab);
-        uint32_t pos = 0, items = 0, weights[2] = {0, 0};
+        uint32_t pos = 0, items = 0, weights[2] = {0, 0};  // items: with units
         for (int k = 0;; ++k) {
           wait(&S.item_full[k & 3], k >> 2);
           const int units = S.items[k & 3].end - S.items[k & 3].unit, last = S.items[k & 3].last;
@@ -705,7 +708,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
               const uint32_t values = pos + 2 * u + 1, keys = values + 1;
               const bool more = u + 1 < units;
               full(values);
-              if (u == 0 && items > 0) wait(&S.o_free, items - 1);
               outputs(s0, values, u == 0);
               if (tries <= 0) break;
               if (more) full(keys); else tc_commit(&S.o_done[0]);

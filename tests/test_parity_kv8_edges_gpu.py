@@ -1,0 +1,59 @@
+"""Attention over the 8-bit cache at the edges of its definition, in each of its three forms: register operands
+(few rows a head), one tile of rows over two streams of tokens, two tiles of rows."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines too
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
+from tests.test_parity_kv8_gpu import BF16, _compare, dev, host, wide_cache  # noqa: E402
+
+DIMS = pytest.mark.parametrize("D", [64, 128])
+
+
+def dense_reference(q, kv, ev, lens, news, scale):
+    """What ``oracle.kvcache8.attention`` gives, in float64 on the GPU, for sequences of much the same size: keys
+    and values [2, B, H, L, D], the values' exponents [B, H, L]."""
+    B, H, L, D = kv.shape[1:]
+    hq, n = q.shape[1], int(news.max())
+    G = hq // H
+    cu = np.concatenate([[0], np.cumsum(news)])
+    at = torch.from_numpy(np.minimum(cu[:-1, None] + np.arange(n), len(q) - 1)).cuda()
+    x = q[at].double().view(B, n, H, G, D).permute(0, 2, 3, 1, 4).reshape(B, H, G * n, D)
+    z = x @ kv[0].transpose(-1, -2) * scale
+    sees = (torch.from_numpy(lens - news).cuda()[:, None] + torch.arange(n, device="cuda") + 1)[:, None, :, None]
+    hidden = (torch.arange(L, device="cuda") >= sees).repeat(1, G, 1, 1).view(B, 1, G * n, L)
+    z = z.masked_fill(hidden, -math.inf)
+    p = z.softmax(-1).nan_to_num(0.0)
+    two = ev.exp2()
+    o = {"out": p @ kv[1], "lse": z.logsumexp(-1), "room": p @ kv[1].abs(),
+         "vsum": (p * two[:, :, None]).amax(-1, keepdim=True) * (kv[1].abs() / two[..., None]).sum(2, keepdim=True),
+         "zroom": (x.abs() @ kv[0].abs().transpose(-1, -2)).amax(-1) * abs(scale)}
+    there = torch.from_numpy(np.arange(n)[None] < news[:, None]).cuda()
+    o = {k: host(y.unflatten(2, (G, n)).permute((0, 3, 1, 2, 4)[:y.dim() + 1]).flatten(2, 3)[there]) for k, y in o.items()}
+    return {**o, "emost": float(ev.abs().max())}
+
+
+@DIMS
+@pytest.mark.parametrize("L", [100, 128, 300])
+def test_tiles_without_rows(L, D):
+    """Two tiles of rows for sequences of which most bring one token: items of few units, many in a row, whose
+    second tile has no rows, between others that fill both."""
+    B, hq, H, ps = 330, 8, 2, 16
+    cache, table, kv, ev = wide_cache(B, L, H, D, ps, L)
+    r = np.random.default_rng([L, D])
+    news = np.where(r.random(B) < 0.02, r.integers(33, 80, B), 1)
+    lens = np.maximum(news, r.integers(1, L + 1, B))
+    q = torch.randn(int(news.sum()), hq, D, device="cuda").to(BF16)
+    cu = dev(np.concatenate([[0], np.cumsum(news)]))
+    ref = dense_reference(q, kv, ev, lens, news, D ** -0.5)
+    for _ in range(20):
+        o = sv.kv8_attention(q, cache, table, dev(lens), cu, page_size=ps, max_new=600)
+    _compare(o, ref, D)
+    assert sv.device_error() == 0
