@@ -11,7 +11,8 @@
 // the next scores were issued behind them.
 //
 // One persistent CTA an SM, its warps specialised: eight take scores to weights, four take outputs to memory,
-// one issues products, one copies (TMA), one looks after values that no row may see, one fetches items. Items
+// one issues products, one copies (TMA), one looks after values that no row may see, one fetches items. Values that
+// are not finite cost their items some microseconds, wherever they are and however many. Items
 // come from a counter, in the order of their cost where that can be had, so that the last ones are short, and
 // two at a time: with four, CTAs held items that others had time for (24 prompts of up to 1000 tokens, 28 + 4
 // heads: 55 -> 52 us; 12 + 12 heads of 64: 119 -> 101).
@@ -30,6 +31,7 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -51,78 +53,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 // ------------------------------------------------------------------------------------------
-// rows for themselves
-// ------------------------------------------------------------------------------------------
-// A warp takes one row of one query head and goes once over the tokens that the row sees, 32 at a time, a lane
-// a token for the scores and D / 32 values of the output. Only rows next to values that are not finite and that
-// they must not see are taken so: a weight of 0 in a product does not keep these out.
-// Row `row` of the call, of query head `head`, whose sequence starts at r0. q: the row as float32 in shared
-// memory, this warp's own.
-template <int D>
-__device__ __noinline__ void prompt_row(const PromptParams& P, int r0, int row, int head, float* q) {
-  constexpr int V = D / 32;  // values of a lane
-  const int lane = threadIdx.x & 31, hk = head / P.group;
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(P.q) + row * P.qs + static_cast<long long>(head) * D;
-  __syncwarp();
-  for (int i = lane; i < D; i += 32) q[i] = __bfloat162float(qp[i]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, o[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int t0 = r0; t0 <= row; t0 += 32) {
-    float z = -INFINITY;
-    if (t0 + lane <= row) {
-      const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.k) + (t0 + lane) * P.ks +
-                                                      static_cast<long long>(hk) * D);
-      float sum = 0.f;
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = __ldg(k + i);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum = fmaf(__uint_as_float(x[j] << 16), q[8 * i + 2 * j], sum);
-          sum = fmaf(__uint_as_float(x[j] & 0xFFFF0000u), q[8 * i + 2 * j + 1], sum);
-        }
-      }
-      z = sum * P.c;
-    }
-    float top = z;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.f : m1;
-    const float down = exp2f(m - base);  // 0 where m is -inf
-    const float p = exp2f(z - base);     // a NaN stays one
-    m = m1;
-    float add = p;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, d);
-    l = l * down + add;
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] *= down;
-    const int n = min(32, row - t0 + 1);
-    for (int j = 0; j < n; ++j) {
-      const float pj = __shfl_sync(0xFFFFFFFFu, p, j);
-      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(P.v) + (t0 + j) * P.vs +
-                               static_cast<long long>(hk) * D + V * lane;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = fmaf(pj, __bfloat162float(v[i]), o[i]);
-    }
-  }
-  const long long at = static_cast<long long>(row) * P.hq + head;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.out) + at * D + V * lane;
-#pragma unroll
-  for (int i = 0; i < V; ++i) out[i] = __float2bfloat16_rn(o[i] / l);
-  if (lane == 0 && P.lse) P.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
-}
-
-
-// ------------------------------------------------------------------------------------------
 // the kernel
 // ------------------------------------------------------------------------------------------
 constexpr int kWarpOut = 8, kWarpMma = 12, kWarpCopy = 13, kWarpValues = 14;  // and items
 constexpr int kPromptThreads = 512;
 constexpr int kSeqs = 1024, kLevels = 1024;  // sequences and tiles of one that items are ordered for
-constexpr int kFixes = 64;
 
 template <int D>
 struct PromptShape {
@@ -139,6 +74,7 @@ struct PromptItem {
   int tok, last;    // first and last token of the item
   int tiles[2];     // of keys, that a tile sees; 0: it has no rows
   int half[2];      // its rows see the first half alone of the last of these
+  int near;         // the first tile of keys with tokens behind `tok`
   int end;          // no item: the last one
 };
 
@@ -149,17 +85,72 @@ struct PromptShared {
   uint64_t o_done[2], o_free[2];             // outputs of an item; read
   uint64_t stat[2][2];                       // sums and maxima of a tile; tiles in turn use two
   uint64_t item_full[2], item_free[2];
-  uint64_t clean[2];                         // an item's last values are fit for products
-  uint64_t meet, end;
+  uint64_t fit[4];                           // values at an odd place of the ring are fit for products
+  uint64_t noted[2];                         // an item's values that are not finite
+  uint64_t end;
   PromptItem items[2];
   float sum[2][2][128], top[2][2][128];
-  float row[4][128];                         // a row's queries
-  int bad[2];                                // the last token of the item with a value that is not finite
-  int4 fix[4][kFixes];                       // rows to be taken for themselves: a list for each output warp
+  int bad[2];                                // some value behind the item's first token is not finite:
+  int first[2][3][128];                      // the first such token of each dimension: NaN, infinity, -infinity
   uint32_t tmem;
   int levels, total;
   int count[kLevels + 1], more[kLevels + 1], start[kLevels + 1], order[kSeqs];
 };
+
+// Values that are not finite, of tokens that some of an item's rows do not see (a weight of 0 would not keep
+// them out of a product): cleared for the products, and the first token of each kind in each dimension is
+// noted, for the rows that see it. `tile`: 128 tokens, of which from .. to - 1 are looked at; the first is token
+// t0, with its key at k. Where a key is not finite either, its weights are NaN or 0 and the values count as
+// NaN. A warp, eight lanes a token.
+template <int D>
+__device__ __forceinline__ void note_values(unsigned char* tile, int t0, int from, int to, const __nv_bfloat16* k,
+                                            long long stride, int (*first)[128]) {
+  const int lane = threadIdx.x & 31;
+  auto finite = [](uint32_t x) { return (x & 0x7F80u) != 0x7F80u; };
+  auto half = [](const uint4& w, int i) { return ((&w.x)[i >> 1] >> (16 * (i & 1))) & 0xFFFFu; };
+#pragma unroll 1
+  for (int r0 = from; r0 < to; r0 += 4) {
+    const int r = r0 + (lane >> 3);
+    bool fine = true;  // its key
+#pragma unroll 1
+    for (int s = 0; s < D / 64; ++s) {
+      if (r >= to) continue;
+      const uint4 w = *reinterpret_cast<const uint4*>(k + r * stride + 64 * s + 8 * (lane & 7));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fine = fine && finite(half(w, i));
+    }
+    fine = ((__ballot_sync(0xFFFFFFFFu, fine) >> (lane & 24)) & 0xFFu) == 0xFFu;
+#pragma unroll 1
+    for (int s = 0; s < D / 64; ++s) {
+      if (r >= to) continue;
+      uint4* at = reinterpret_cast<uint4*>(tile + s * 128 * 128 + 128 * r + 16 * (lane & 7));
+      const int d = 64 * s + 8 * ((lane & 7) ^ (r & 7));  // the 128-byte swizzle
+      uint4 w = *at;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = half(w, i);
+        if (finite(x)) continue;
+        atomicMin(&first[x & 0x7Fu || !fine ? 0 : x >> 15 ? 2 : 1][d + i], t0 + r);
+        (&w.x)[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+      }
+      *at = w;
+    }
+  }
+}
+// ... and added to what the products gave the row of this token: a weight of finite scores is more than 0, so that
+// the result is the same infinity, or NaN.
+template <int D>
+__device__ __forceinline__ void add_noted(__nv_bfloat16* out, int token, const int (*first)[128]) {
+#pragma unroll 1
+  for (int d = 0; d < D; ++d) {
+    const bool nan = token >= first[0][d], up = token >= first[1][d], down = token >= first[2][d];
+    if (!nan && !up && !down) continue;
+    float x = __bfloat162float(out[d]);
+    if (up) x += INFINITY;
+    if (down) x -= INFINITY;
+    out[d] = __float2bfloat16_rn(nan ? NAN : x);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
@@ -199,13 +190,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&S.stat[i][1], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.clean[i], 1);
+      mbar_init(&S.noted[i], 1);
       mbar_init(&S.item_full[i], 1);
       mbar_init(&S.item_free[i], 15);
       S.items[i] = PromptItem{};
       S.items[i].end = 1;  // what a role reads that gave up waiting
     }
-    mbar_init(&S.meet, 4);
+    for (int i = 0; i < C::kStages / 2; ++i) mbar_init(&S.fit[i], 1);
     mbar_init(&S.end, 1);
     fence_mbar_init();
     S.levels = 0;
@@ -418,11 +409,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t outs = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kColO;
     const bool wide = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;  // whole sectors
     int use[2] = {0, 0};
-    int fixes = 0;  // items that have rows to compute once more, the same ones in each of these warps
-    uint32_t meets = 0;
-    auto meet = [&] {  // these warps, those apart that gave up
-      arrive_warp(&S.meet);
-      wait_warp(&S.meet, meets++);
+    auto row_of = [&](const PromptItem& it, int tok) {
+      return static_cast<long long>(it.r0 + tok) * P.hq + it.head * P.group + row - i * P.group;
     };
     for (int k = 0;; ++k) {
       wait_warp(&S.item_full[k & 1], k >> 1);
@@ -438,9 +426,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
         const float l = S.sum[u & 1][g][row], m = S.top[u & 1][g][row];
         const float inv = 1.f / l;
-        const int tok = it.tok + g * per + i, head = it.head * P.group + row - i * P.group;
+        const int tok = it.tok + g * per + i;
         const bool there = i < per && tok <= it.last;
-        const long long at = static_cast<long long>(it.r0 + tok) * P.hq + head;
+        const long long at = row_of(it, tok);
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(P.out) + at * D;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
@@ -470,30 +458,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         if (there && P.lse) P.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
       }
-      wait_warp(&S.clean[k & 1], k >> 1);
+      wait_warp(&S.noted[k & 1], k >> 1);
       if (tries <= 0) break;
-      const int bad = S.bad[k & 1];
-      arrive_warp(&S.item_free[k & 1]);  // and the places of that number elsewhere
-      if (bad > it.tok) {  // rows before that token
-        const int4 fix = make_int4(it.r0, it.tok, bad, it.head);
-        if (fixes < kFixes) {
-          if (lane == 0) S.fix[warp - kWarpOut][fixes] = fix;
-          ++fixes;
-        } else {
-          meet();  // what these rows got from the products is written
-          for (int n = warp - kWarpOut; n < (bad - it.tok) * P.group; n += 4)
-            prompt_row<D>(P, it.r0, it.r0 + it.tok + n / P.group, it.head * P.group + n % P.group,
-                          S.row[warp - kWarpOut]);
+      if (S.bad[k & 1] && i < per)
+        for (int g = 0; g < 2; ++g) {
+          const int tok = it.tok + g * per + i;
+          if (tok <= it.last)
+            add_noted<D>(static_cast<__nv_bfloat16*>(P.out) + row_of(it, tok) * D, tok, S.first[k & 1]);
         }
-      }
-    }
-    if (fixes && tries > 0) {
-      meet();
-      for (int f = 0; f < fixes; ++f) {
-        const int4 fix = S.fix[warp - kWarpOut][f];
-        for (int n = warp - kWarpOut; n < (fix.z - fix.y) * P.group; n += 4)
-          prompt_row<D>(P, fix.x, fix.x + fix.y + n / P.group, fix.w * P.group + n % P.group, S.row[warp - kWarpOut]);
-      }
+      arrive_warp(&S.item_free[k & 1]);  // and the places of that number elsewhere
     }
   } else {
     fewer_registers<72>();
@@ -539,8 +512,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tc_commit(&S.empty[pos % C::kStages]);
           for (int j = 0; j < most; ++j) {
             const uint32_t values = pos + 2 * j + 1, keys = values + 1;
-            wait_full(values);
-            if (j + 1 < most) wait_full(keys); else wait(&S.clean[k & 1], k >> 1);
+            // tokens that some row does not see lie in the last two tiles
+            wait(j + 2 >= most ? &S.fit[values % C::kStages / 2] : &S.full[values % C::kStages], values / C::kStages);
+            if (j + 1 < most) wait_full(keys);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (j >= tiles[g]) continue;
@@ -619,18 +593,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (use[g] > 0 && !mbar_wait_bounded(&S.q_full[g], (use[g] - 1) & 1, kWaitCycles)) tries = 0;
     } else if (warp == kWarpValues) {
       // ---- values next to the rows' own tokens. Those behind the item's last token, which no row sees, are
-      // cleared; of those behind its first one the last that is not finite is noted.
+      // cleared; of those behind its first one, what is not finite is cleared and noted.
       int pos = 1;
       PromptItem it;
       for (int k = 0; item(k, it); ++k) {
         const int most = max(it.tiles[0], it.tiles[1]);
-        int bad = -1;
+        bool noted = false;
         for (int j = 0; j < most; ++j, pos += 2) {
           const int stage = pos % C::kStages;
           wait_warp(&S.full[stage], pos / C::kStages);
           if (tries <= 0) break;
-          const int from = max(it.tok + 1 - 128 * j, 0), to = min(it.last + 1 - 128 * j, 128);
-          if (to > from || j == most - 1) {
+          if (j >= it.near) {
+            const int from = max(it.tok + 1 - 128 * j, 0), to = min(it.last + 1 - 128 * j, 128);
+            bool bad = false;
             unsigned char* tile = ring + stage * C::kTile + 16 * (lane & 7);
 #pragma unroll 1
             for (int r0 = (from & ~15) + (lane >> 3); r0 < 128; r0 += 16) {  // 16 rows at a time, all read at once
@@ -650,15 +625,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                   x = __vmaxu2(x, __vmaxu2(__vmaxu2(w[u][s].x & f, w[u][s].y & f), __vmaxu2(w[u][s].z & f, w[u][s].w & f)));
                   if (r >= to) *reinterpret_cast<uint4*>(tile + s * C::kSlab + 128 * r) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (r >= from && r < to && ((x & 0xFFFFu) >= 0x7F80u || (x >> 16) >= 0x7F80u)) bad = max(bad, 128 * j + r);
+                if (r >= from && r < to && ((x & 0xFFFFu) >= 0x7F80u || (x >> 16) >= 0x7F80u)) bad = true;
               }
             }
-          }
-          if (j == most - 1) {
-            bad = __reduce_max_sync(0xFFFFFFFFu, bad);
-            if (lane == 0) S.bad[k & 1] = bad;
+            if (__any_sync(0xFFFFFFFFu, bad)) {
+              if (!noted)
+                for (int i = lane; i < 3 * 128; i += 32) S.first[k & 1][i / 128][i % 128] = INT_MAX;
+              noted = true;
+              __syncwarp();
+              const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(P.k) + (it.r0 + 128LL * j) * P.ks +
+                                          static_cast<long long>(it.head) * D;
+              note_values<D>(ring + stage * C::kTile, 128 * j, from, to, keys, P.ks, S.first[k & 1]);
+            }
             fence_async_shared();
-            arrive_warp(&S.clean[k & 1]);
+          }
+          arrive_warp(&S.fit[stage / 2]);
+          if (j == most - 1) {
+            if (lane == 0) S.bad[k & 1] = noted;
+            arrive_warp(&S.noted[k & 1]);
           }
           arrive_warp(&S.empty[stage]);
         }
@@ -717,6 +701,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int last0 = min(it.tok + per - 1, it.last);
             it.tiles[0] = last0 / 128 + 1;
             it.tiles[1] = last0 < it.last ? it.last / 128 + 1 : 0;
+            it.near = (it.tok + 1) / 128;
             it.half[0] = last0 % 128 < 64;
             it.half[1] = it.last % 128 < 64;
           }
