@@ -113,3 +113,31 @@ def test_values_not_finite_throughout_a_long_prompt():
     rows = np.unique(np.concatenate([np.arange(60), np.random.default_rng(2).integers(0, T, 24), [T - 1, T - 32, 2048, 2054, 2055]]))
     o = check(q, k, v, [T], rows, chunk=2)
     assert o["lse"].isfinite().all()
+
+
+@DIMS
+@pytest.mark.parametrize("B,empty", [(1023, 0.0), (1024, 0.3), (1025, 0.3), (3000, 0.9), (3000, 0.05)])
+def test_sequences_around_the_limit_of_ordering(B, empty, D):
+    """Up to 1024 sequences are taken in the order of their cost, more as they come."""
+    r = np.random.default_rng([B, D])
+    lens = np.where(r.random(B) < empty, 0, r.integers(1, 40, B))
+    lens[r.integers(0, B, 3)] = 300
+    q, k, v = inputs(int(lens.sum()) + 9, 4, 2, D, B)
+    check(q, k, v, lens, chunk=1024)
+
+
+@DIMS
+@pytest.mark.parametrize("lens", [[2046], [2047], [2048], [2049], [2100], [3, 2300, 0, 70, 2050], [1500, 2052, 2400]])
+def test_tiles_around_the_limit_of_ordering(lens, D):
+    """128 query heads on one: two tokens are an item, and more than 1024 of a sequence are taken as they come."""
+    q, k, v = inputs(sum(lens), 128, 1, D, sum(lens))
+    check(q, k, v, lens, chunk=64)
+
+
+@DIMS
+def test_more_sequences_than_an_order_holds_and_long_ones(D):
+    r = np.random.default_rng(D)
+    lens = r.integers(0, 9, 1500)
+    lens[[3, 700, 1499]] = 2600, 1900, 3001
+    q, k, v = inputs(int(lens.sum()), 14, 2, D, 4)
+    check(q, k, v, lens, np.unique(r.integers(0, int(lens.sum()), 700)), chunk=50)
