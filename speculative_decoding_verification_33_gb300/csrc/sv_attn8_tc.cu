@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         const int lim = sees - kUnit * (first_unit + u);
         const bool masked = kUnit * (first_unit + u + 1) > all_see;  // some row does not see some of these
         // A row's factor of the scores for keys times this: held, so that a sum of 0 stays 0 and what is not seen
-        // stays so; past that either way nothing but the signs of the scores counts
+        // stays so. Operands are below 2^16 and 2^7: at the lower limit, a scale of 0 among what comes there, no
+        // score counts; at the upper one nothing but their signs does.
         auto factor = [&](float keys) {
           return copysignf(fminf(fmaxf(fabsf(qc * keys), 7.8886091e-31f), 1.2676506e30f), P.c);
         };
@@ -879,7 +880,7 @@ cudaError_t launch_dim8_tc(const AttnParams& P, int sms, cudaStream_t stream) {
 
 cudaError_t launch_attention8_tc(const AttnParams& params, int D, long long rows, int sms, cudaStream_t stream) {
   AttnParams P = params;
-  if (P.c == 0.f) P.c = FLT_MIN;  // so that what is not seen stays so; scores count as nothing all the same
+  if (P.c == 0.f) P.c = 0.f;  // without a sign, which would be that of the scores
   // Measured in us with pairs / without. 8 sequences of 16384 tokens, 8 heads of 128: 160 rows 144 / 195, 256 rows
   // 166 / 196; 6000 rows of two 688 / 1008; 2 heads of 64: 160 rows 54 / 60, 12000 rows 297 / 467. Against it:
   // 256 rows of two sequences of 32768 tokens 137 / 120, whose pieces of twice the rows take longer to join.

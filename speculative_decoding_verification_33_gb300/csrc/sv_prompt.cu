@@ -778,7 +778,9 @@ cudaError_t launch_prompt_dim(const PromptParams& P, int sms, cudaStream_t strea
 
 cudaError_t launch_prompt(const PromptParams& params, int D, int sms, cudaStream_t stream) {
   PromptParams P = params;
-  if (P.c == 0.f) P.c = FLT_MIN;  // so that what is not seen stays so; scores count as nothing all the same
+  // A scale of 0 is taken as the least one, so that what is not seen stays so: a product, whatever it is, counts
+  // as less than 2^-20
+  if (P.c == 0.f) P.c = FLT_TRUE_MIN;
   return D == 64 ? launch_prompt_dim<64>(P, sms, stream) : launch_prompt_dim<128>(P, sms, stream);
 }
 

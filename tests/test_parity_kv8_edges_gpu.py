@@ -12,7 +12,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines t
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
-from tests.test_parity_kv8_gpu import BF16, _compare, dev, host, wide_cache  # noqa: E402
+from tests.test_parity_kv8_gpu import BF16, _check_attention, _compare, dev, host, wide_cache  # noqa: E402
 
 DIMS = pytest.mark.parametrize("D", [64, 128])
 
@@ -57,3 +57,18 @@ def test_tiles_without_rows(L, D):
         o = sv.kv8_attention(q, cache, table, dev(lens), cu, page_size=ps, max_new=600)
     _compare(o, ref, D)
     assert sv.device_error() == 0
+
+
+FORMS = pytest.mark.parametrize("rows", [4, 100, 600])  # a head, as the caller says: one for each form of the kernel
+
+
+@FORMS
+@DIMS
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_scale_of_zero(rows, D, scale):
+    """Every token counts alike, however large keys and queries are: their products pass 2^120 and more."""
+    def edit(c, table, q):
+        c[..., 32 * D] = np.random.default_rng(1).integers(60, 122, c.shape[:3])
+        q[3:] *= 1e15
+    o, ref = _check_attention([150, 300, 3], [2, 3, 1], 4, 2, D, 16, scale=scale, max_new=rows // 2, edit=edit)
+    assert np.allclose(ref["lse"][:, 0], np.log([149, 150, 298, 299, 300, 3]))

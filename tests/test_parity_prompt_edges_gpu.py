@@ -116,6 +116,17 @@ def test_values_not_finite_throughout_a_long_prompt():
 
 
 @DIMS
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_scale_of_zero(D, scale):
+    """Every token counts alike, however large keys and queries are: their products reach 2^125."""
+    q, k, v = inputs(290, 4, 2, D, 9)
+    q[100:], k[100:] = q[100:] * 1e18, k[100:] * 1e18
+    q[50] *= 1e35
+    o = check(q, k, v, [90, 200], scale=scale)
+    assert np.allclose(host(o["lse"])[:, 0], np.log(np.concatenate([np.arange(90), np.arange(200)]) + 1.0))
+
+
+@DIMS
 @pytest.mark.parametrize("B,empty", [(1023, 0.0), (1024, 0.3), (1025, 0.3), (3000, 0.9), (3000, 0.05)])
 def test_sequences_around_the_limit_of_ordering(B, empty, D):
     """Up to 1024 sequences are taken in the order of their cost, more as they come."""
