@@ -163,7 +163,8 @@ sv_status spec_kv4_append(int T, int Hkv, int D, int page_size, int num_pages, s
  *   block_table [B][max_blocks] int32; a page outside 0..num_pages-1 is not read, and the rows
  *       that see one of its tokens are NaN. kv_lens above max_blocks * page_size count as that.
  *   cu_new [B+1] int32, ascending; entries are held to 0..T
- *   scale, k_scale, v_scale: finite; the cache's tensor scales as in spec_kv4_append
+ *   scale, k_scale, v_scale: finite, scale * k_scale * log2(e) a float32; the cache's tensor scales as in
+ *       spec_kv4_append
  *   max_new: the largest number of new tokens of a sequence, as far as the caller knows. It picks
  *       the kernel's tiles; any value gives the same results to rounding.
  *   out bfloat16 [T][Hq][D] contiguous; out_lse float32 [T][Hq]: natural log of the softmax's
@@ -233,7 +234,7 @@ sv_status spec_kv8_attention(int B, int T, int Hq, int Hkv, int D, int page_size
  *   q   bfloat16 [T][Hq][D], k, v bfloat16 [T][Hkv][D], rows as in spec_qk_norm_rope, 16-byte aligned
  *       (pointers, strides); Hq a multiple of Hkv, query head h reads key/value head h / (Hq / Hkv)
  *   cu  [B+1] int32, ascending; entries are held to 0..T
- *   scale: finite
+ *   scale: finite, with scale * log2(e) a float32
  *   out bfloat16 [T][Hq][D] contiguous, 16-byte aligned, no part of the inputs; out_lse float32 [T][Hq]:
  *       natural log of the softmax's sum, or NULL. Rows of no sequence are not written.
  * D is 64 or 128, Hq / Hkv at most 128. Products take bfloat16 operands, the softmax's weights rounded to

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -882,6 +883,14 @@ bool aligned16(const void* p, long long stride, size_t elt) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * static_cast<long long>(elt)) % 16 == 0;
 }
 
+// What takes a product of query and key to a score in base 2; false if that is no float32.
+bool score_factor(float scale, float k_scale, float* c) {
+  const double x = static_cast<double>(scale) * static_cast<double>(k_scale) * 1.4426950408889634;
+  if (!(std::fabs(x) <= static_cast<double>(FLT_MAX))) return false;
+  *c = static_cast<float>(x);
+  return true;
+}
+
 // Arguments of attention over a paged cache, checked; B == 0 or T == 0 leaves the rest unset.
 sv_status cache_attention_params(sv::AttnParams* out_params, int B, int T, int Hq, int Hkv, int D, int page_size,
                                  int num_pages, int max_blocks, const void* q, long long q_token_stride,
@@ -891,7 +900,8 @@ sv_status cache_attention_params(sv::AttnParams* out_params, int B, int T, int H
   if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || num_pages < 1 ||
       max_blocks < 1 || max_new < 0)
     return SV_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+  sv::AttnParams& P = *out_params;
+  if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale) || !score_factor(scale, k_scale, &P.c))
     return SV_ERR_INVALID_ARG;
   if (!sv::kv_page_size_ok(page_size) || !sv::kv_head_dim_ok(D)) return SV_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_blocks) * page_size >= (1LL << 31)) return SV_ERR_INVALID_ARG;
@@ -901,7 +911,6 @@ sv_status cache_attention_params(sv::AttnParams* out_params, int B, int T, int H
   if (!aligned16(q, q_token_stride, 2) || !aligned16(cache, 0, 1) || !aligned16(out, 0, 1))
     return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * Hq >= (1LL << 31)) return SV_ERR_UNSUPPORTED;
-  sv::AttnParams& P = *out_params;
   P.B = B;
   P.T = T;
   P.hq = Hq;
@@ -916,8 +925,6 @@ sv_status cache_attention_params(sv::AttnParams* out_params, int B, int T, int H
   P.table = block_table;
   P.lens = kv_lens;
   P.cu = cu_new;
-  P.c = static_cast<float>(static_cast<double>(scale) * static_cast<double>(k_scale) *
-                           1.4426950408889634);
   P.vs = v_scale;
   P.out = out;
   P.lse = out_lse;
@@ -1224,7 +1231,8 @@ sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void
                                 const void* v, long long v_token_stride, const int32_t* cu,
                                 float scale, void* out, float* out_lse, void* stream) {
   if (B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return SV_ERR_INVALID_ARG;
-  if (!std::isfinite(scale)) return SV_ERR_INVALID_ARG;
+  sv::PromptParams P;
+  if (!std::isfinite(scale) || !score_factor(scale, 1.f, &P.c)) return SV_ERR_INVALID_ARG;
   if (!sv::kv_head_dim_ok(D) || Hq / Hkv > 128) return SV_ERR_UNSUPPORTED;
   const long long row = static_cast<long long>(Hkv) * D;
   if (q_token_stride < static_cast<long long>(Hq) * D || k_token_stride < row || v_token_stride < row)
@@ -1235,7 +1243,6 @@ sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void
       !aligned16(out, 0, 1))
     return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * Hq >= (1LL << 31)) return SV_ERR_UNSUPPORTED;
-  sv::PromptParams P;
   P.B = B;
   P.T = T;
   P.hq = Hq;
@@ -1248,7 +1255,6 @@ sv_status spec_prompt_attention(int B, int T, int Hq, int Hkv, int D, const void
   P.k = k;
   P.v = v;
   P.cu = cu;
-  P.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   P.out = out;
   P.lse = out_lse;
   return with_attention_workspace(stream, [&](void* base, int sms, cudaStream_t s) {
