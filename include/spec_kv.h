@@ -217,8 +217,7 @@ sv_status spec_kv8_append(int T, int Hkv, int D, int page_size, int num_pages, s
  * sees a token with a marked value is NaN. Scores, softmax and sums are held in float32; products take
  * float16 operands: codes are exact in it, queries as in spec_kv4_attention; the weights times 2^e of
  * the values' block are rounded to it (by up to 2^-11 of each, or 2^-32 of the row's largest where that is
- * more). The exponents of the blocks of values that a row sees should lie within 100 of one another; past
- * that the weights of the small ones may count as 0 in its sum.
+ * more; in the softmax's sum each counts as it is, whatever its block's exponent).
  */
 sv_status spec_kv8_attention(int B, int T, int Hq, int Hkv, int D, int page_size, int num_pages,
                              int max_blocks, const void* q, long long q_token_stride,

@@ -117,6 +117,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 constexpr int kWaitTries = 1 << 19;  // a second or more
 
+// Over the 8-bit cache weights carry 2^e of their values' block, so that the maximum M that they are held to, of
+// score + e, says nothing of how large the softmax's sum is beside it: that is sum of 2^(score - M), down
+// to 2^-121 of the largest weight. So sums are scaled in two steps, for a factor of less than 2^-126 may have one of
+// 2^60 to take to where it counts; and tokens whose e lies so far below the largest one there that their weights
+// may be none are added to them by score - M itself. (A weight of none is lost below 2^(-126 - e). M is
+// 2^7 below score + e of some token at least, of which the sum has 2^(7 - e) or more: what is lost is less than 2^-43 of it.)
+constexpr unsigned kQuiet = 90;  // exponents of values, all from -60 on
+__device__ __forceinline__ float times_two_to(float x, float d) {
+  const float half = ex2_fast(0.5f * d);
+  return x * half * half;
+}
+
 // Weights and values (o: 4 dimensions from d of row r of the item's tile, sum L at maximum M, in
 // base 2) into the output and its log-sum.
 __device__ __forceinline__ long long out_row(const AttnParams& P, const Walk& w, int tile_rows,
@@ -230,8 +242,8 @@ __device__ __forceinline__ bool find_run(const AttnParams& P, longlong2* scan, R
 // A CTA has two pieces of items at most, one that ends an item or goes on with it and one that
 // starts one, at P.part in this order (R x D outputs, maxima, sums). A piece is written: counts
 // it, and in the last CTA to arrive at the item joins its pieces, in their order. THREADS threads
-// call it, tid of them this one, with `sync` a barrier among them.
-template <int THREADS, int R, int D, int BATCH, class Sync>
+// call it, tid of them this one, with `sync` a barrier among them. HEADS: of the 8-bit cache.
+template <int THREADS, int R, int D, int BATCH, bool HEADS, class Sync>
 __device__ __forceinline__ void join_pieces(const AttnParams& P, const Walk& w, const Run& run,
                                             int rows, int tid, int* s_last, Sync sync) {
   constexpr long long kPart = R * (D + 2);
@@ -269,14 +281,14 @@ __device__ __forceinline__ void join_pieces(const AttnParams& P, const Walk& w, 
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) top = fmaxf(top, m[i]);
-      const float down = ex2_fast(M - top);
+      const float half = ex2_fast((HEADS ? 0.5f : 1.f) * (M - top)), down = HEADS ? half * half : half;
+      L = HEADS ? L * half * half : L * down;
       M = top;
-      L *= down;
       o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const float f = ex2_fast(m[i] - M);
-        L += l[i] * f;
+        const float half = ex2_fast((HEADS ? 0.5f : 1.f) * (m[i] - M)), f = HEADS ? half * half : half;
+        L += HEADS ? l[i] * half * half : l[i] * f;
         o.x += x[i].x * f;
         o.y += x[i].y * f;
         o.z += x[i].z * f;

@@ -50,7 +50,8 @@ constexpr int kWarpUnpack = 8, kWarpMma = 12, kWarpCopy = 13, kWarpItems = 14;
 constexpr int kThreads = 512, kSoftmaxThreads = 256;
 constexpr int kR = 128, kUnit = 128;  // rows of a tile, tokens of a unit
 
-constexpr uint32_t kMarked = 1 << 16, kUneven = 1 << 17;  // some token is marked; the exponents of a unit are too far apart
+// Some token is marked; the exponents of a unit are too far apart, or those of values too far below others before it
+constexpr uint32_t kMarked = 1 << 16, kUneven = 1 << 17;
 // ... by more than this: a code times 2^-14 is exact in float16; weights times 2^e of a unit's largest values
 // are held to 2^-36 of the row's largest, which is 2^-32 of it by each block's own e.
 constexpr int kEvenKeys = 14, kEvenValues = 4;
@@ -104,7 +105,7 @@ struct Shared8 {
   alignas(16) long long off[16][8];      // ... and where its blocks lie
   // per unit modulo 8: what its operands were multiplied with, and the same of each block by itself
   uint32_t unit[8];                      // e of keys and of values plus 64, kMarked, kUneven, 14 bits of its number
-  alignas(16) float4 heads[8][8];        // 2^e of keys, e of values, 2^-e, marks
+  alignas(16) float4 heads[8][8];        // 2^e of keys, e of values, marks
   float qc[4][2 * kR];                   // per row: score of a product of the operands
   float top[2][2][kR], sum[2][2][kR], bad[2][2][kR];  // of two items, of two streams
 };
@@ -137,6 +138,71 @@ __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
 }
 template <int N>
 using Upto = std::make_integer_sequence<int, N>;
+
+// A row's factor of the scores for keys times this: held, so that a sum of 0 stays 0 and what is not seen stays
+// so. Operands are below 2^16 and 2^7: at the lower limit, a scale of 0 among what comes there, no score counts;
+// at the upper one nothing but their signs does.
+__device__ __forceinline__ float score_factor(float qc, float keys, float c) {
+  return copysignf(fminf(fmaxf(fabsf(qc * keys), 7.8886091e-31f), 1.2676506e30f), c);
+}
+
+// A unit whose codes are operands as they are: each block with its own factors, and weights that may be none. 32
+// columns at a time, twice.
+struct Uneven8 {
+  uint32_t cols;  // of the scores
+  const float4* heads;
+  int lim;        // tokens that the row sees
+  float qc, c;
+  __device__ __forceinline__ void scores(int b, const float* x, float2* z) const {  // of block b
+    const float4 hb = heads[b];
+    const float f = score_factor(qc, hb.x, c);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      z[n] = make_float2(__fmaf_rn(x[2 * n], f, hb.y), __fmaf_rn(x[2 * n + 1], f, hb.y));
+      if (16 * b + 2 * n >= lim) z[n].x = -INFINITY;
+      if (16 * b + 2 * n + 1 >= lim) z[n].y = -INFINITY;
+    }
+  }
+  __device__ __noinline__ float maximum() const {
+    float t = -INFINITY;
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+      float x[32];
+      tmem_ld32(cols + 32 * part, x);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float2 z[8];
+        scores(2 * part + b, x + 16 * b, z);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) t = max3(t, z[n].x, z[n].y);
+      }
+    }
+    return t;
+  }
+  // Weights, over the scores; returns their part of the softmax's sum
+  __device__ __noinline__ float2 weights(float m) const {
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+      float x[32];
+      uint32_t w[16];
+      tmem_ld32(cols + 32 * part, x);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float2 z[8];
+        scores(2 * part + b, x + 16 * b, z);
+        const float e = heads[2 * part + b].y;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          sum = add2(sum, make_float2(ex2_fast(z[n].x - e - m), ex2_fast(z[n].y - e - m)));
+          w[8 * b + n] = pack_f16x2(ex2_fast(__fadd_rn(z[n].x, -m)), ex2_fast(__fadd_rn(z[n].y, -m)));
+        }
+      }
+      tmem_st16(cols + 16 * part, w);  // over scores that have been read
+    }
+    return sum;
+  }
+};
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_constant__ AttnParams P) {
@@ -247,12 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         const float keys = __int_as_float(((about & 0xFFu) + 63) << 23);
         const int lim = sees - kUnit * (first_unit + u);
         const bool masked = kUnit * (first_unit + u + 1) > all_see;  // some row does not see some of these
-        // A row's factor of the scores for keys times this: held, so that a sum of 0 stays 0 and what is not seen
-        // stays so. Operands are below 2^16 and 2^7: at the lower limit, a scale of 0 among what comes there, no
-        // score counts; at the upper one nothing but their signs does.
-        auto factor = [&](float keys) {
-          return copysignf(fminf(fmaxf(fabsf(qc * keys), 7.8886091e-31f), 1.2676506e30f), P.c);
-        };
         // The row's maximum t has come: moves m, with the sums and outputs
         auto move_to = [&](float t) {
           const bool move = t - m > kSlack;
@@ -261,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
           } else if (__any_sync(0xFFFFFFFFu, move)) {
             // the products before these scores are done: nobody else is at the outputs
             const float now = move ? t - kLift8 : m, down = ex2_fast(m - now);
+            l2.x = times_two_to(l2.x, m - now);
+            l2.y = times_two_to(l2.y, m - now);
             m = now;
-            l2.x *= down;
-            l2.y *= down;
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               float o[32];
@@ -277,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         };
         if (about & kMarked) {
           for (int b = 0; b < 8; ++b) {
-            const uint32_t w = __float_as_uint(heads[b].w);
+            const uint32_t w = __float_as_uint(heads[b].z);
             const int here = lim - 16 * b;
             const uint32_t seen = here >= 16 ? 0xFFFFu : here > 0 ? (1u << here) - 1u : 0u;
             if (w & seen) l2.x = NAN;
@@ -288,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
           uint32_t r[128];
           tmem_ld64(cols, r);
           tmem_ld64(cols + 64, r + 64);
-          const float f = factor(keys), e = static_cast<float>(unit_e);
+          const float f = score_factor(qc, keys, P.c), e = static_cast<float>(unit_e);
           tmem_wait_ld(r);
           tmem_wait_ld(r + 64);
           if (masked) {
@@ -345,52 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
           const float undo = __int_as_float((127 - unit_e) << 23);
           l2 = fma2(sum, make_float2(undo, undo), l2);
         } else {
-          // Codes as they are: each block with its own factors, 32 columns at a time, twice
-          auto scores = [&](int b, const float* x, float2* z) {  // of block b
-            const float4 hb = heads[b];
-            const float f = factor(hb.x);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              z[n] = make_float2(__fmaf_rn(x[2 * n], f, hb.y), __fmaf_rn(x[2 * n + 1], f, hb.y));
-              if (16 * b + 2 * n >= lim) z[n].x = -INFINITY;
-              if (16 * b + 2 * n + 1 >= lim) z[n].y = -INFINITY;
-            }
-          };
-          float t = -INFINITY;
-#pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
-            float x[32];
-            tmem_ld32(cols + 32 * part, x);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float2 z[8];
-              scores(2 * part + b, x + 16 * b, z);
-#pragma unroll
-              for (int n = 0; n < 8; ++n) t = max3(t, z[n].x, z[n].y);
-            }
-          }
-          move_to(t);
-#pragma unroll 1
-          for (int part = 0; part < 4; ++part) {
-            float x[32];
-            uint32_t w[16];
-            tmem_ld32(cols + 32 * part, x);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float2 z[8], sum = make_float2(0.f, 0.f);
-              scores(2 * part + b, x + 16 * b, z);
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                z[n].x = ex2_fast(__fadd_rn(z[n].x, -m));
-                z[n].y = ex2_fast(__fadd_rn(z[n].y, -m));
-                sum = add2(sum, z[n]);
-                w[8 * b + n] = pack_f16x2(z[n].x, z[n].y);
-              }
-              const float undo = heads[2 * part + b].z;
-              l2 = fma2(sum, make_float2(undo, undo), l2);
-            }
-            tmem_st16(cols + 16 * part, w);  // over scores that have been read
-          }
+          const Uneven8 slow{cols, heads, lim, qc, P.c};
+          move_to(slow.maximum());
+          l2 = add2(l2, slow.weights(m));
         }
         tmem_wait_st();
         tc_fence_before();
@@ -415,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         M = fmaxf(m0, m1);
         f0 = ex2_fast(m0 - M);
         f1 = ex2_fast(m1 - M);
-        L = S.sum[k & 1][0][row] * f0 + S.sum[k & 1][1][row] * f1;
+        L = times_two_to(S.sum[k & 1][0][row], m0 - M) + times_two_to(S.sum[k & 1][1][row], m1 - M);
         all = S.bad[k & 1][0][row] + S.bad[k & 1][1][row];
         from = D / 2 * g;
         to = from + D / 2;
@@ -474,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
         }
       }
       if (!whole)
-        join_pieces<kSoftmaxThreads, C::kRows, D, 4>(P, w, S.run, rows, tid, &S.last, meet);
+        join_pieces<kSoftmaxThreads, C::kRows, D, 4, true>(P, w, S.run, rows, tid, &S.last, meet);
       const int last = it.last;
       arrive_warp(&S.item_free[k & 3]);
       if (last) break;
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
       };
       // What codes of values are multiplied with, of the last unit whose heads were read and of the one before
       uint32_t now_by0 = 0, now_by1 = 0, old_by0 = 0, old_by1 = 0;
-      int heads_at = -1;
+      int heads_at = -1, loud = -128;  // the largest exponent of values of the item's units
       for (int p = 0; p < places; ++p) {
         int u;
         const bool values = tile_at(p, &u);
@@ -587,7 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
           const int ev = min(max(static_cast<int>(static_cast<signed char>((head.x >> 8) & 0xFFu)), kKv8Low), kKv8High);
           const int most_k = __reduce_max_sync(0xFFFFFFFFu, there ? ek : kKv8Low);
           const int most_v = __reduce_max_sync(0xFFFFFFFFu, there ? ev : kKv8Low);
-          const bool uneven = __any_sync(0xFFFFFFFFu, there && (most_k - ek > kEvenKeys || most_v - ev > kEvenValues));
+          loud = max(loud, most_v);
+          const bool uneven = __any_sync(0xFFFFFFFFu, there && (most_k - ek > kEvenKeys || most_v - ev > kEvenValues)) ||
+                              most_v < loud - static_cast<int>(kQuiet);
           const uint32_t marked = __any_sync(0xFFFFFFFFu, head.y != 0) ? kMarked : 0u;
           // 2^(e - the largest) twice, in float16
           const uint32_t by_k = uneven || !there ? 0x3C003C00u : static_cast<uint32_t>(15 + ek - most_k) * 0x04000400u;
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
           heads_at = u;
           auto two = [](int e) { return __int_as_float((e + 127) << 23); };
           if (wid == 0 && lane < 8)
-            S.heads[(unit0 + u) & 7][lane] = make_float4(two(ek), static_cast<float>(ev), two(-ev), __uint_as_float(head.y));
+            S.heads[(unit0 + u) & 7][lane] = make_float4(two(ek), static_cast<float>(ev), __uint_as_float(head.y), 0.f);
           if (wid == 0 && lane == 8)
             *const_cast<volatile uint32_t*>(&S.unit[(unit0 + u) & 7]) =
                 static_cast<uint32_t>(most_k + 64) | static_cast<uint32_t>(most_v + 64) << 8 | marked |

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
   __shared__ Producer s_prod[NP];
   __shared__ long long s_queue[NP][32][NB];  // where the blocks of a pair's next units lie
   __shared__ int s_last;
+  __shared__ int s_low[NP][2];  // per warp: kQuiet below the largest exponent of values that it has come to in the item
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = warp >> 1, h = warp & 1;
   const int g = lane >> 2, c = lane & 3;
@@ -255,6 +256,7 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
     const int rows = min(R, w.n * P.group - w.rt * R);  // rows of this tile
     const int tiles = (rows + 7) >> 3;
     store_q(w);
+    if (tid < 2 * NP) s_low[0][tid] = kKv8Low;
     if (tid == 0) {
       Walk nw = w;
       next_item<S>(P, nw);
@@ -264,6 +266,7 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
     const int all_see = svis[0];  // tokens that every row of the tile sees
 
     float O[NT][MH][4], m[NT][2], l[NT][2];
+    int low = 0;  // exponents of values from here to kQuiet above need nothing but their weights
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -295,9 +298,17 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
         uint32_t marks = 0;
 #pragma unroll
         for (int o = 0; o < OWN; ++o) head[o].load(sb + (h * OWN + o) * S::kBlock, (lost >> (h * OWN + o)) & 1u);
+        bool masked = t0 + UNIT > all_see || lost;
+        if constexpr (F::kHeads) {
+          low = s_low[pair][h];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) marks |= F::marks(sb + b * S::kBlock);
-        const bool masked = t0 + UNIT > all_see || lost || marks;
+          for (int b = 0; b < NB; ++b) {
+            const uint2 w = F::head(sb + b * S::kBlock);
+            marks |= w.y;
+            masked = masked || static_cast<unsigned>(F::lift(w) - low) > kQuiet;
+          }
+        }
+        masked = masked || marks;
 
         // scores of this warp's blocks and the tile's rows
         float s[OWN][TN][4];
@@ -337,7 +348,26 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
             }
           }
         }
+        // Tokens of a block whose weights may be none, into the sums
+        auto add_quiet = [&](int o) {
+          if constexpr (F::kHeads) {
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) l[t][k & 1] += ex2_fast(s[o][t][k] - head[o].lift - m[t][k & 1]);
+            head[o].undo = 0.f;
+          }
+        };
+        bool later = false;
+        static_assert(!F::kHeads || OWN == 1, "one block of its own for each warp");
         if (masked) {
+          if constexpr (F::kHeads) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if (!((lost >> b) & 1u)) low = max(low, F::lift(F::head(sb + b * S::kBlock)) - static_cast<int>(kQuiet));
+            __syncwarp();
+            if (lane == 0) s_low[pair][h] = low;
+          }
 #pragma unroll
           for (int o = 0; o < OWN; ++o) {
             const int tb = t0 + 16 * (h * OWN + o) + g;
@@ -352,6 +382,15 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
                 else if constexpr (F::kHeads)
                   if ((head[o].marks >> (g + 8 * (k >> 1))) & 1u) s[o][t][k] = NAN;
               }
+            if constexpr (F::kHeads) {
+              if (head[o].e < low) {  // far above the maximum they would be infinite: they come when it has moved
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) later = later || s[o][t][k] - m[t][k & 1] > kSlack;
+                if (!later) add_quiet(o);
+              }
+            }
           }
         }
         float top = -INFINITY;
@@ -386,15 +425,18 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
             for (int e = 0; e < 2; ++e) {
               const int r = 8 * t + 2 * c + e;
               const float y = fmaxf(m[t][e], fmaxf(x[r], x[R + r]) - kLift);
-              const float down = ex2_fast(m[t][e] - y);
+              const float half = F::kHeads ? ex2_fast(0.5f * (m[t][e] - y)) : 0.f;
+              const float down = F::kHeads ? half * half : ex2_fast(m[t][e] - y);
+              l[t][e] = F::kHeads ? l[t][e] * half * half : l[t][e] * down;
               m[t][e] = y;
-              l[t][e] *= down;
 #pragma unroll
               for (int j = 0; j < MH; ++j) {
                 O[t][j][e] *= down;
                 O[t][j][e + 2] *= down;
               }
             }
+          if constexpr (F::kHeads)
+            if (later) add_quiet(0);
         }
 #pragma unroll
         for (int o = 0; o < OWN; ++o)
@@ -514,7 +556,8 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
         for (int k = 0; k < NP; ++k) M = fmaxf(M, swm[k * R + r]);
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          L += (swl[2 * k * R + r] + swl[(2 * k + 1) * R + r]) * ex2_fast(swm[k * R + r] - M);
+          const float l2 = swl[2 * k * R + r] + swl[(2 * k + 1) * R + r], dm = swm[k * R + r] - M;
+          if constexpr (F::kHeads) L += times_two_to(l2, dm); else L += l2 * ex2_fast(dm);
           const float4 x = *reinterpret_cast<const float4*>(buf + (k * 8 + place) * S::kOutStride + d);
           o.x += x.x;
           o.y += x.y;
@@ -533,7 +576,7 @@ __global__ void __launch_bounds__(AttnShape<F, NT>::kThreads, AttnShape<F, NT>::
       }
     }
     if (!whole)
-      join_pieces<S::kThreads, R, D, 8>(P, w, s_run, rows, tid, &s_last, [] { __syncthreads(); });
+      join_pieces<S::kThreads, R, D, 8, F::kHeads>(P, w, s_run, rows, tid, &s_last, [] { __syncthreads(); });
     if (!more) break;
     __syncthreads();  // the joining buffers and statistics are free
   }

@@ -59,7 +59,7 @@ def test_tiles_without_rows(L, D):
     assert sv.device_error() == 0
 
 
-FORMS = pytest.mark.parametrize("rows", [4, 100, 600])  # a head, as the caller says: one for each form of the kernel
+FORMS = pytest.mark.parametrize("rows", [4, 20, 100, 600])  # a head, as the caller says: each form of the kernel
 
 
 @FORMS
@@ -72,3 +72,45 @@ def test_scale_of_zero(rows, D, scale):
         q[3:] *= 1e15
     o, ref = _check_attention([150, 300, 3], [2, 3, 1], 4, 2, D, 16, scale=scale, max_new=rows // 2, edit=edit)
     assert np.allclose(ref["lse"][:, 0], np.log([149, 150, 298, 299, 300, 3]))
+
+
+def values_exponents(c, which, D):
+    """Exponents of the values of blocks [pages, heads, blocks, bytes], from a function of page and block."""
+    pages, _, blocks, _ = c.shape
+    for p in range(pages):
+        for j in range(blocks):
+            c[p, :, j, 32 * D + 1] = which(p, j) % 256
+
+
+@FORMS
+@DIMS
+@pytest.mark.parametrize("sharp", [1.0, 20.0, 60.0])
+def test_exponents_of_the_whole_range(rows, D, sharp):
+    """Values of every exponent that the append writes, from -60 to 121, side by side."""
+    def edit(c, table, q):
+        c[..., 32 * D + 1] = np.random.default_rng(7).integers(-60, 122, c.shape[:3]) % 256
+    _check_attention([330, 50, 1200], [3, 2, 4], 4, 1, D, 16, edit=edit, max_new=rows // 4, sharp=sharp)
+
+
+@FORMS
+@DIMS
+@pytest.mark.parametrize("order", ["quiet first", "loud first", "in turn", "nothing but zeros beside"])
+def test_quiet_and_loud_values(rows, D, order):
+    """Whole runs of blocks of the least exponents beside those of the largest: all count in the softmax's sum, in
+    whatever order they come and wherever the work is cut."""
+    L, ps = 2600, 32
+    blocks = -(-L // ps)
+
+    def edit(c, table, q):
+        r, at = np.random.default_rng(3), {int(p): i for i, p in enumerate(table[0])}
+        late = order == "quiet first"
+
+        def e(p, j):
+            i = at.get(p, 0)
+            loud = (i >= blocks // 2) == late if order in ("quiet first", "loud first") else (i + j) % 3 == 0
+            return int(r.integers(110, 122)) if loud else -60
+        values_exponents(c, e, D)
+        if order == "nothing but zeros beside":
+            c.reshape(-1, 32 * D + 16)[c[..., 32 * D + 1].reshape(-1) == 196, 16 * D:32 * D] = 128
+    for sharp in (1.0, 30.0):
+        _check_attention([L], [3], 4, 1, D, ps, edit=edit, max_new=rows // 4, sharp=sharp)
