@@ -12,6 +12,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines t
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import speculative_decoding_verification_33_gb300 as sv  # noqa: E402
+from tests import test_parity_kv8_gpu as K  # noqa: E402
 from tests.test_parity_kv8_gpu import BF16, _check_attention, _compare, dev, host, wide_cache  # noqa: E402
 
 DIMS = pytest.mark.parametrize("D", [64, 128])
@@ -114,3 +115,25 @@ def test_quiet_and_loud_values(rows, D, order):
             c.reshape(-1, 32 * D + 16)[c[..., 32 * D + 1].reshape(-1) == 196, 16 * D:32 * D] = 128
     for sharp in (1.0, 30.0):
         _check_attention([L], [3], 4, 1, D, ps, edit=edit, max_new=rows // 4, sharp=sharp)
+
+
+@DIMS
+@pytest.mark.parametrize("hint", [32, 60])  # 64 to 128 rows a head for groups of two and four
+@pytest.mark.parametrize("case", [
+    K.test_attention_empty, K.test_attention_sharp_and_flat, K.test_attention_exponents_far_apart,
+    K.test_attention_ignores_what_rows_do_not_see, K.test_attention_marks_inside_a_prompt,
+    K.test_attention_infinite_queries, K.test_attention_pages_outside_the_cache,
+    K.test_attention_lengths_past_the_table, K.test_attention_every_order_of_four_pages],
+    ids=lambda f: f.__name__[15:])
+def test_one_tile_of_rows(case, hint, D):
+    """The cases of the other forms where one tile of rows goes over two streams of tokens: values lag keys by a
+    unit, and streams with maxima of their own are joined."""
+    case(hint=hint, D=D)
+
+
+@pytest.mark.parametrize("B,L,n,hq,hk,D,ps", [
+    (2, 6000, 16, 16, 2, 64, 32), (40, 900, 25, 8, 2, 64, 16), (1, 20000, 100, 1, 1, 64, 64),
+    (3, 4000, 30, 8, 2, 128, 64), (1, 9001, 65, 2, 1, 128, 16), (60, 400, 40, 4, 2, 128, 32)])
+def test_one_tile_of_rows_long_and_many(B, L, n, hq, hk, D, ps):
+    """Rings of operands and bytes that wrap many times, work cut over a sequence's tokens."""
+    K.test_attention_long_and_many(B, L, n, hq, hk, D, ps)
