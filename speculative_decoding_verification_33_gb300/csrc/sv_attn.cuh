@@ -1,5 +1,6 @@
-// Shared by the attention kernels over the 4-bit cache (sv_attn.cu, sv_attn_tc.cu): how the work is
-// cut between CTAs and joined, and conversions.
+// Shared by the attention kernels over the paged caches (4 bits: sv_attn.cu, sv_attn_tc.cu; 8 bits: sv_attn8.cu,
+// sv_attn8_tc.cu): how the work is cut between CTAs and joined, and conversions. Prompts (sv_prompt.cu) take the
+// waits from here.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -195,7 +195,7 @@ struct Uneven8 {
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
           sum = add2(sum, make_float2(ex2_fast(z[n].x - e - m), ex2_fast(z[n].y - e - m)));
-          w[8 * b + n] = pack_f16x2(ex2_fast(__fadd_rn(z[n].x, -m)), ex2_fast(__fadd_rn(z[n].y, -m)));
+          w[8 * b + n] = pack_f16(ex2_fast(__fadd_rn(z[n].x, -m)), ex2_fast(__fadd_rn(z[n].y, -m)));
         }
       }
       tmem_st16(cols + 16 * part, w);  // over scores that have been read
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_tc_kernel(const __grid_cons
                 p.x = ex2_fast(p.x);
                 p.y = ex2_fast(p.y);
                 sum = add2(sum, p);
-                w[n] = pack_f16x2(p.x, p.y);
+                w[n] = pack_f16(p.x, p.y);
               }
               tmem_st16(cols + 16 * part, w);
             }
