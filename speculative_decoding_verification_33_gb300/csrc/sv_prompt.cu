@@ -512,9 +512,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tc_commit(&S.empty[pos % C::kStages]);
           for (int j = 0; j < most; ++j) {
             const uint32_t values = pos + 2 * j + 1, keys = values + 1;
-            // tokens that some row does not see lie in the last two tiles
-            wait(j + 2 >= most ? &S.fit[values % C::kStages / 2] : &S.full[values % C::kStages], values / C::kStages);
+            // Values come by way of the warp that looks after them, always: a barrier that is not waited for in
+            // each of its phases can be one behind, and seem to be done
             if (j + 1 < most) wait_full(keys);
+            wait(&S.fit[values % C::kStages / 2], values / C::kStages);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               if (j >= tiles[g]) continue;
