@@ -119,11 +119,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 constexpr int kWaitTries = 1 << 19;  // a second or more
 
 // Over the 8-bit cache weights carry 2^e of their values' block, so that the maximum M that they are held to, of
-// score + e, says nothing of how large the softmax's sum is beside it: that is sum of 2^(score - M), down
-// to 2^-121 of the largest weight. So sums are scaled in two steps, for a factor of less than 2^-126 may have one of
-// 2^60 to take to where it counts; and tokens whose e lies so far below the largest one there that their weights
-// may be none are added to them by score - M itself. (A weight of none is lost below 2^(-126 - e). M is
-// 2^7 below score + e of some token at least, of which the sum has 2^(7 - e) or more: what is lost is less than 2^-43 of it.)
+// score + e, says nothing of how large the softmax's sum is beside them: that is the sum of 2^(score - M), from
+// 2^-121 up to 2^75. So sums are scaled in two steps, for a factor of less than 2^-126 may take one of 2^60 to
+// where it still counts; and tokens whose e lies so far below the largest one there that their weights may be none
+// come into them by score - M itself. (Otherwise what is lost of a weight is below 2^(-126 - e) in the sum. M lies
+// 2^7 below score + e of some token, whose part of the sum is 2^(7 - e): 2^43 times as much or more.)
 constexpr unsigned kQuiet = 90;  // exponents of values, all from -60 on
 __device__ __forceinline__ float times_two_to(float x, float d) {
   const float half = ex2_fast(0.5f * d);

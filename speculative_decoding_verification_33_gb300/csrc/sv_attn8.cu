@@ -10,11 +10,13 @@
 // sum of 2^(score - M): maxima and the log-sum stay as they are, and joins but for the sums' range (times_two_to in
 // sv_attn.cuh).
 //
-// What bounds it, as with 4 bits, is latency: with 20 rows of 524301 tokens, 8 heads of 128, it takes 231 us,
-// 0.69 of the measured copy rate, with 0.54 of the issue slots and 0.37 of the tensor pipe used, and fixed
+// What bounds it, as with 4 bits, is latency: with 20 rows of 524301 tokens, 8 heads of 128, it takes 234 us,
+// 0.68 of the measured copy rate, with 0.53 of the issue slots and 0.36 of the tensor pipe used, and fixed
 // latencies and the pairs' barriers the largest stalls; 64 sequences of up to 8192 tokens and up to 24 rows
-// 103 us. The cut of the work (kOver, kLeast) is at its best here: kOver 48 and 200 take 105 and 107 us for
-// these, kLeast 4 and 16 12.8 and 12.3 us for one row of 4097 tokens where 12 takes 11.8.
+// 104 us. The cut of the work (kOver, kLeast) is at its best here: kOver 48 and 200 take 106 and 107 us for
+// these, kLeast 4 and 16 12.9 and 12.8 us for one row of 4097 tokens where 12 takes 11.8. Exponents of values of the
+// whole range cost 1 to 4 %: without what add_quiet and times_two_to do these take 231 and 103 us, and 100 sequences
+// of up to 4000 tokens, 32 rows of heads of 64, 25.6 instead of 26.7.
 #include "spec_kv.h"
 #include "sv_attn_mma.cuh"
 
@@ -138,10 +140,10 @@ constexpr int kMaxRows8 = D == 128 ? 24 : 32;
 
 // Rows a head, at most, for this kernel; those past a tile read the cache once more. It works for the rows that
 // a sequence has, sv_attn8_tc.cu for 128. Measured in us, here / there, for 8 sequences of 16384 tokens and
-// for 64 of up to 8192 with up to that many rows. D = 128, 8 heads: 24 rows 72 / 97 and 93 / 160; 32 rows
-// 103 / 98 and 124 / 162; 48 rows 124 / 102 and 148 / 170; 64 rows 174 / 104 and 190 / 178; 20 rows of one
-// sequence of 524301 tokens 229 / 336. D = 64, 2 heads: 32 rows 25 / 33; 64 rows 36 / 36 and 40 / 45; 96
-// rows 45 / 40 and 51 / 48.
+// for 64 of up to 8192 with up to that many rows. D = 128, 8 heads: 24 rows 73 / 97 and 96 / 143; 32 rows
+// 105 / 99 and 125 / 146; 48 rows 125 / 101 and 150 / 154; 64 rows 175 / 104 and 193 / 159; 20 rows of one
+// sequence of 524301 tokens 232 / 335. D = 64, 2 heads: 32 rows 26 / 33; 64 rows 37 / 36 and 41 / 45; 96
+// rows 46 / 40 and 53 / 48.
 template <int D>
 constexpr int kRegisterRows = D == 128 ? 32 : 64;
 

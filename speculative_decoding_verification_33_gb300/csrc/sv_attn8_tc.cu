@@ -10,21 +10,21 @@
 // of its own, so that codes are unpacked once for both.
 //
 // Codes come as they are, by bulk copies into a ring, and become float16 on their way through registers to
-// operands in the 128-byte swizzle. With the conversion, for nothing, goes a power of two that brings a unit's blocks to one exponent, for keys and for values, which joins the factor of
-// the scores and the exponent of the weights as in sv_attn8.cu. That is exact where the exponents are within
-// 2^14 (2^4 for values) of one another; a unit where they are not has its codes as they are, and each block its own factors in
-// the softmax. With each block's own factors always, its threads ran out of registers and took a half more
+// operands in the 128-byte swizzle. With the conversion, for nothing, goes a power of two that brings a unit's
+// blocks to one exponent, for keys and for values, which joins the factor of the scores and the exponent of the
+// weights as in sv_attn8.cu. That is exact where the exponents are within 2^14 (2^4 for values) of one another; a
+// unit where they are not has its codes as they are, and each block its own factors in the softmax. With each block's own factors always, its threads ran out of registers and took a half more
 // time; values as bfloat16, which need none, cost twice the instructions where codes are converted.
 //
 // One persistent CTA an SM, its warps specialised: eight for the softmax, four unpack keys and values
 // (and bring queries), one issues products, one copies, one walks through the items. The work is cut and
 // joined as in sv_attn.cu, in units of 128 tokens.
 //
-// What bounds it: 1500 new of 16384 tokens twice, 32 + 8 heads of 128, take 688 us, 1117 TFLOP/s, 0.59 of the
-// measured bf16 rate, with the tensor cores busy for 0.48 of their cycles and 0.44 of the issue slots used:
+// What bounds it: 1500 new of 16384 tokens twice, 32 + 8 heads of 128, take 660 us, 1165 TFLOP/s, 0.60 of the
+// measured bf16 rate, with the tensor cores busy for 0.51 of their cycles and 0.47 of the issue slots used:
 // softmax and conversion wait for each other's bytes in the shared memory, which the products' operands keep
 // busy. With few rows the conversion bounds it, whatever the rows (64 sequences of up to 8192 tokens, 48 rows a
-// head: 170 us, 0.32 of the copy rate). Plain loads into registers a
+// head: 154 us, 0.35 of the copy rate). Plain loads into registers a
 // tile ahead took 1079 us; more threads to unpack and operands in bfloat16 were slower than these, too.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -146,8 +146,9 @@ __device__ __forceinline__ float score_factor(float qc, float keys, float c) {
   return copysignf(fminf(fmaxf(fabsf(qc * keys), 7.8886091e-31f), 1.2676506e30f), c);
 }
 
-// A unit whose codes are operands as they are: each block with its own factors, and weights that may be none. 32
-// columns at a time, twice.
+// A unit whose codes are operands as they are: each block with its own factors, and weights that may be none (see
+// times_two_to), so that the sum takes exponentials of its own. 32 columns at a time, twice. Functions of their
+// own: inlined, they make the kernel slower that hardly ever comes here (1500 of 16384 tokens twice: 712 -> 725 us).
 struct Uneven8 {
   uint32_t cols;  // of the scores
   const float4* heads;
@@ -900,9 +901,9 @@ cudaError_t launch_dim8_tc(const AttnParams& P, int sms, cudaStream_t stream) {
 cudaError_t launch_attention8_tc(const AttnParams& params, int D, long long rows, int sms, cudaStream_t stream) {
   AttnParams P = params;
   if (P.c == 0.f) P.c = 0.f;  // without a sign, which would be that of the scores
-  // Measured in us with pairs / without. 8 sequences of 16384 tokens, 8 heads of 128: 160 rows 144 / 195, 256 rows
-  // 166 / 196; 6000 rows of two 688 / 1008; 2 heads of 64: 160 rows 54 / 60, 12000 rows 297 / 467. Against it:
-  // 256 rows of two sequences of 32768 tokens 137 / 120, whose pieces of twice the rows take longer to join.
+  // Measured in us with pairs / without. 8 sequences of 16384 tokens, 8 heads of 128: 160 rows 141 / 194, 256 rows
+  // 161 / 196; 6000 rows of two 660 / 980; 2 heads of 64: 160 rows 54 / 60, 12000 rows 295 / 462. Against it:
+  // 256 rows of two sequences of 32768 tokens 137 / 121, whose pieces of twice the rows take longer to join.
   const bool pair = rows > kR;
   if (D == 64) return pair ? launch_dim8_tc<64, true>(P, sms, stream) : launch_dim8_tc<64, false>(P, sms, stream);
   return pair ? launch_dim8_tc<128, true>(P, sms, stream) : launch_dim8_tc<128, false>(P, sms, stream);

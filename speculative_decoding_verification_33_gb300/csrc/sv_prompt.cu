@@ -6,9 +6,9 @@
 //   outputs [128 rows x D] += weights [tensor memory] v [shared memory]
 // with scores and outputs of both tiles in tensor memory. While the tensor cores work for one tile, the
 // softmax of the other runs: a thread a row, one pass with the running maximum and sum; the weights go back
-// over the scores as bfloat16. A row's maximum is moved only when a score exceeds it by 2^8, and only then
-// are outputs read back and scaled, by the row's own threads: the products before have ended by then, since
-// the next scores were issued behind them.
+// over the scores as bfloat16, since the operands of a product have one type and the values are that. A row's
+// maximum is moved only when a score exceeds it by 2^8, and only then are outputs read back and scaled, by the
+// row's own threads: the products before have ended by then, since the next scores were issued behind them.
 //
 // One persistent CTA an SM, its warps specialised: eight take scores to weights, four take outputs to memory,
 // one issues products, one copies (TMA), one looks after values that no row may see, one fetches items. Values that
@@ -17,9 +17,9 @@
 // two at a time: with four, CTAs held items that others had time for (24 prompts of up to 1000 tokens, 28 + 4
 // heads: 55 -> 52 us; 12 + 12 heads of 64: 119 -> 101).
 //
-// What bounds it, on long prompts: the tensor cores, at 0.67 of their cycles and 0.83 of the measured bf16 rate
-// (8192 tokens, 32 + 8 heads of 128: 350 us, 1571 TFLOP/s by what rows see; 16384 tokens: 1674), held up by the
-// softmax's way from scores to weights, a latency: 0.37 of the issue slots are used. On short prompts: the
+// What bounds it, on long prompts: the tensor cores, at 0.68 of their cycles and 0.81 of the measured bf16 rate
+// (8191 tokens, 32 + 8 heads of 128: 351 us, 1566 TFLOP/s by what rows see; 16384 tokens: 1320, 1666), held up by the
+// softmax's way from scores to weights, a latency: 0.38 of the issue slots are used. On short prompts: the
 // changes from item to item, about 5 us for each of 128 rows twice, most of it waits for memory. Tiles of 64
 // tokens with scores twice in tensor memory (long prompts 370 -> 516 us: such products read their queries
 // twice as often), the next item's first scores behind this one's last products (registers spilled: 350 ->

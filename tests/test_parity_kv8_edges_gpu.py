@@ -37,7 +37,8 @@ def dense_reference(q, kv, ev, lens, news, scale):
          "vsum": (p * two[:, :, None]).amax(-1, keepdim=True) * (kv[1].abs() / two[..., None]).sum(2, keepdim=True),
          "zroom": (x.abs() @ kv[0].abs().transpose(-1, -2)).amax(-1) * abs(scale)}
     there = torch.from_numpy(np.arange(n)[None] < news[:, None]).cuda()
-    o = {k: host(y.unflatten(2, (G, n)).permute((0, 3, 1, 2, 4)[:y.dim() + 1]).flatten(2, 3)[there]) for k, y in o.items()}
+    o = {k: host(y.unflatten(2, (G, n)).permute((0, 3, 1, 2, 4)[:y.dim() + 1]).flatten(2, 3)[there])
+         for k, y in o.items()}
     return {**o, "emost": float(ev.abs().max())}
 
 

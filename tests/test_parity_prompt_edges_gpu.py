@@ -110,7 +110,8 @@ def test_values_not_finite_throughout_a_long_prompt():
     q, k, v = inputs(T, hq, hk, D, 5)
     t = torch.arange(7, T, 32, device="cuda")
     v[t, :, t // 2048] = math.inf
-    rows = np.unique(np.concatenate([np.arange(60), np.random.default_rng(2).integers(0, T, 24), [T - 1, T - 32, 2048, 2054, 2055]]))
+    rows = np.unique(np.concatenate([np.arange(60), np.random.default_rng(2).integers(0, T, 24),
+                                     [T - 1, T - 32, 2048, 2054, 2055]]))
     o = check(q, k, v, [T], rows, chunk=2)
     assert o["lse"].isfinite().all()
 
