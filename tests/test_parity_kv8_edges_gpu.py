@@ -138,3 +138,34 @@ def test_one_tile_of_rows(case, hint, D):
 def test_one_tile_of_rows_long_and_many(B, L, n, hq, hk, D, ps):
     """Rings of operands and bytes that wrap many times, work cut over a sequence's tokens."""
     K.test_attention_long_and_many(B, L, n, hq, hk, D, ps)
+
+
+@FORMS
+@DIMS
+def test_key_exponents_of_the_whole_range(rows, D):
+    """Keys of every exponent side by side, with queries that bring the loudest ones' scores to the order of 1."""
+    def edit(c, table, q):
+        c[..., 32 * D] = np.random.default_rng(11).integers(-60, 122, c.shape[:3]) % 256
+    _check_attention([330, 50, 900], [3, 2, 4], 4, 1, D, 16, edit=edit, max_new=rows // 4, sharp=1e-30, scale=1e-9)
+
+
+@FORMS
+@DIMS
+def test_append_and_attend_at_every_magnitude(rows, D):
+    """Values from 1e-25 to 1e37 and blocks of zeros, appended as they come and attended to."""
+    L, H, ps = 700, 2, 32
+    r, g = np.random.default_rng(D), torch.Generator("cuda").manual_seed(D)
+    k, v = (torch.randn(L, H, D, device="cuda", generator=g) for _ in "kv")
+    size = 10.0 ** torch.from_numpy(r.uniform(-25, 37, -(-L // 16))).cuda().repeat_interleave(16)[:L]
+    size[::100] *= 0.01
+    v = (v * size[:, None, None]).to(BF16)
+    v[160:208] = 0.0
+    table = r.permutation(-(-L // ps))[None]
+    slots = table[0][np.arange(L) // ps] * ps + np.arange(L) % ps
+    cache = sv.kv8_cache(table.size, H, D, ps)
+    for a, b in ((0, 16), (16, 333), (333, 334), (334, L)):
+        sv.kv8_append(k[a:b].to(BF16), v[a:b], dev(slots[a:b], torch.int64), cache, page_size=ps)
+    q = torch.randn(6, 4 * H, D, device="cuda", generator=g).to(BF16)
+    lens, cu = np.array([L]), np.array([0, 6])
+    o = sv.kv8_attention(q, cache, dev(table), dev(lens), dev(cu), page_size=ps, max_new=rows // 4)
+    _compare(o, K.O.attention(host(q), cache.cpu().numpy(), table, lens, cu, ps, D ** -0.5), D)
